@@ -13,6 +13,7 @@ same HIP runtime as torch (both carry the soname libamdhip64.so.7).
 """
 import ctypes
 import os
+import sys
 
 import torch
 
@@ -522,3 +523,11 @@ def p3d_proj_linear_grouped(S, weights, outs, biases=None, accumulate=False, str
                                      for g, b in enumerate(biases)])
     _check(lib.p3d_proj_linear_grouped(_dev(S, "S", torch.bfloat16, (n, K)), n, K, P3D_BF16, G,
                                        wp, bp, D, op, int(bool(accumulate)), _stream(stream)))
+
+
+# the transformer block's operators (include/p3d_block.h)
+from . import block                                                   # noqa: E402
+from .block import *                                                  # noqa: E402,F401,F403
+
+block.bind(sys.modules[__name__])
+__all__ += block.__all__

@@ -303,6 +303,23 @@ p3d_status scratch_address(const char* fn, void** out) {
 
 }  // namespace
 
+// The same message slot for the entry points of block_api.hip.
+namespace p3d {
+
+p3d_status set_error(p3d_status s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_err = buf;
+    return s;
+}
+
+p3d_status set_ok() { return ok(); }
+
+}  // namespace p3d
+
 extern "C" {
 
 const char* p3d_version(void) { return "p3d 1.0.0 gfx950"; }

@@ -1,0 +1,494 @@
+// attention_bwd.hip -- p3d_attention_backward (include/p3d_block.h). With the
+// forward call's lse the probabilities are one exponential away from the
+// scores, P = exp(scale S - lse), so both kernels recompute them tile by tile:
+//
+//   rows kernel   D_i = dout_i . out_i and lse in the exponent's unit, once
+//   dq kernel     a wave holds 32 query rows and walks the keys:
+//                 dS^T = P^T (V dO^T - D),  dQ^T += K^T dS^T
+//   dkv kernel    a wave holds 32 keys and walks the query rows:
+//                 dV^T += dO^T P,  dK^T += Q^T dS
+//
+// Each product's second factor is the softmax tile as the first product left
+// it in registers (attn_tile.h). The scores are computed twice, once per
+// kernel (7 products instead of 5): the alternative, adding dQ from the dkv
+// kernel with atomics, changes results from run to run and moves 4 bytes per
+// 1280 operations through the caches.
+//
+// Where few tiles face a long axis the walked axis is cut into parts whose
+// binary32 sums go to the workspace and are joined by join_kernel.
+#include <algorithm>
+
+#include "attn_tile.h"
+
+namespace p3d {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kWaves = 4;
+constexpr int kHeld = 32 * kWaves;       // rows (dq) or keys (dkv) held by a workgroup
+constexpr int kWalk = 64;                // keys (dq) or rows (dkv) of one walked tile
+
+struct BwdArgs {
+    AttnArgs a;
+    ItemTable tiles;                     // first tile of every item, of rows or keys
+    Group group;
+    int splits;
+    float *lse2, *delta;                 // [kv_heads][nq * group]
+    float *part, *part2;                 // [splits][n * heads][head_dim]: dq, or dk and dv
+};
+
+// D and lse2 of every row; 32 lanes per (token, head), 4 columns a lane. lse2
+// of a row that sees no key is +inf, so its P is exp2(-inf) = 0.
+__global__ __launch_bounds__(256) void rows_kernel(BwdArgs f, int64_t rows) {
+    const AttnArgs& a = f.a;
+    const int d = (threadIdx.x & 31) * 4;
+    for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows;
+         row += (int64_t)gridDim.x * 8) {
+        const int64_t token = row / a.heads;
+        const int head = (int)(row - token * a.heads);
+        float s = 0.f;
+        if (d < a.head_dim) {
+            const uint2 x = *reinterpret_cast<const uint2*>(
+                reinterpret_cast<const uint16_t*>(a.dout) + token * a.dout_stride +
+                head * a.head_dim + d);
+            const uint2 y = *reinterpret_cast<const uint2*>(
+                reinterpret_cast<const uint16_t*>(a.out_in) + token * a.out_stride +
+                head * a.head_dim + d);
+            s = bf16lo(x.x) * bf16lo(y.x) + bf16hi(x.x) * bf16hi(y.x) +
+                bf16lo(x.y) * bf16lo(y.y) + bf16hi(x.y) * bf16hi(y.y);
+        }
+        s = lane_sum<32>(s);
+        if (d) continue;
+        const int kv_head = head / (int)f.group.size;
+        const int64_t at = (rows / a.heads * kv_head + token) * f.group.size + head -
+                           kv_head * (int)f.group.size;
+        const float l = a.lse_in[row];
+        f.delta[at] = s;
+        f.lse2[at] = l == -INFINITY ? INFINITY : l * kLog2e;
+    }
+}
+
+// A held tile's binary32 sums to the workspace; `row` counts (token, head).
+template <int HD>
+__device__ __forceinline__ void store_sums(const f32x16 (&o)[Tile<HD>::kBlocks], float* out,
+                                           int hd, int lane) {
+    const int h = lane >> 5;
+#pragma unroll
+    for (int b = 0; b < Tile<HD>::kBlocks; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int d = 32 * b + 8 * j + 4 * h;
+            if (d < hd)
+                *reinterpret_cast<float4*>(out + d) = make_float4(
+                    o[b][4 * j], o[b][4 * j + 1], o[b][4 * j + 2], o[b][4 * j + 3]);
+        }
+}
+
+template <int HD>
+__global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
+    using T = Tile<HD>;
+    __shared__ uint4 kt[2][kWalk * T::kChunks];
+    __shared__ uint4 vt[2][kWalk * T::kChunks];
+    const AttnArgs& a = f.a;
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int chunks = a.head_dim >> 3;
+
+    const int tile = blockIdx.x / a.kv_heads, kv_head = blockIdx.x - tile * a.kv_heads;
+    const int item = item_of_tile(f.tiles, a.batch, tile);
+    const int tiles = f.tiles.start[item + 1] - f.tiles.start[item];
+    const int nth = tile - f.tiles.start[item];
+    const uint32_t row0 = (uint32_t)(a.causal ? tiles - 1 - nth : nth) * kHeld;
+    const int q0 = a.q_items.start[item], nq = a.q_items.start[item + 1] - q0;
+    const int k0 = a.k_items.start[item], nk = a.k_items.start[item + 1] - k0;
+    const uint32_t rows = (uint32_t)nq * f.group.size;
+
+    const uint32_t row = row0 + 32 * wave + (lane & 31);
+    const bool live = row < rows;
+    uint32_t token, member;
+    f.group.split(live ? row : 0, token, member);
+    const int head = kv_head * f.group.size + member;
+    bf16x8_t q[T::kSteps], dout[T::kSteps];
+    load_query<HD>(q,
+                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
+                                                  (int64_t)(q0 + (int)token) * a.q_stride +
+                                                  head * a.head_dim),
+                   live, chunks, lane);
+    load_query<HD>(dout,
+                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.dout) +
+                                                  (int64_t)(q0 + (int)token) * a.dout_stride +
+                                                  head * a.head_dim),
+                   live, chunks, lane);
+    const int64_t stat = ((int64_t)a.q_items.start[a.batch] * kv_head + q0) * f.group.size + row;
+    const float lse2 = live ? f.lse2[stat] : INFINITY;
+    const float delta = live ? f.delta[stat] : 0.f;
+
+    int part = (nk + f.splits - 1) / f.splits;
+    part = (part + kWalk - 1) / kWalk * kWalk;
+    const int begin = (int)min((int64_t)blockIdx.y * part, (int64_t)nk);
+    int end = (int)min((int64_t)begin + part, (int64_t)nk);
+    int limit = end;
+    if (a.causal) {
+        limit = min(end, live ? (int)token + nk - nq + 1 : end);
+        uint32_t last, m;
+        f.group.split(min(row0 + kHeld, rows) - 1, last, m);
+        end = min(end, (int)last + nk - nq + 1);
+    }
+    const int all_see = __builtin_amdgcn_readfirstlane(limit);
+    const float c = a.scale * kLog2e;
+
+    f32x16 dq[T::kBlocks];
+#pragma unroll
+    for (int b = 0; b < T::kBlocks; ++b) dq[b] = zero16();
+    if (chunks < T::kChunks) {
+        for (int i = 0; i < 2; ++i) {
+            T::clear(kt[i], kWalk, 64 * kWaves, threadIdx.x);
+            T::clear(vt[i], kWalk, 64 * kWaves, threadIdx.x);
+        }
+        __syncthreads();
+    }
+    const uint16_t* kb = reinterpret_cast<const uint16_t*>(a.k) + (int64_t)k0 * a.k_stride +
+                         kv_head * a.head_dim;
+    const uint16_t* vb = reinterpret_cast<const uint16_t*>(a.v) + (int64_t)k0 * a.v_stride +
+                         kv_head * a.head_dim;
+    // rows past the item's last key repeat it; their dS is 0
+    auto fetch = [&](int buf, int key) {
+        T::template load<kWalk, kWaves>(kt[buf], wave, lane, chunks, [&](int r) {
+            return reinterpret_cast<const uint4*>(kb + (int64_t)min(key + r, nk - 1) * a.k_stride);
+        });
+        T::template load<kWalk, kWaves>(vt[buf], wave, lane, chunks, [&](int r) {
+            return reinterpret_cast<const uint4*>(vb + (int64_t)min(key + r, nk - 1) * a.v_stride);
+        });
+    };
+    if (begin < end) fetch(0, begin);
+    int buf = 0;
+    for (int key = begin; key < end; key += kWalk, buf ^= 1) {
+        tile_barrier();
+        if (key + kWalk < end) fetch(buf ^ 1, key + kWalk);
+        const bool masked = key + kWalk > all_see;
+#pragma unroll
+        for (int b = 0; b < kWalk / 32; ++b) {
+            f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+            for (int k = 0; k < T::kSteps; ++k) {
+                s = mfma(T::row_frag(kt[buf], 32 * b, lane, k), q[k], s);
+                dp = mfma(T::row_frag(vt[buf], 32 * b, lane, k), dout[k], dp);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[i] = __builtin_amdgcn_exp2f(s[i] * c - lse2) * (dp[i] - delta);
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (key + 32 * b + acc_row(i, h) >= limit) s[i] = 0.f;
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const bf16x8_t ds = acc_frag(s, t);
+#pragma unroll
+                for (int d = 0; d < T::kBlocks; ++d)
+                    dq[d] = mfma(T::tr_frag(kt[buf], 32 * b + 16 * t, lane, d), ds, dq[d]);
+            }
+        }
+    }
+
+    const int64_t out_row = (int64_t)(q0 + (int)token) * a.heads + head;
+    if (f.splits > 1) {
+        const int64_t all = (int64_t)a.q_items.start[a.batch] * a.heads;
+        if (live)
+            store_sums<HD>(dq, f.part + (blockIdx.y * all + out_row) * a.head_dim, a.head_dim,
+                           lane);
+        return;
+    }
+    tile_barrier();
+    // a row that sees nothing has dS = 0 * (...): its dq is 0 by definition
+    const float by = lse2 == INFINITY ? 0.f : a.scale;
+    uint4* stage = wave < 2 ? kt[wave] : vt[wave - 2];
+    store_rows<HD>(dq, by, stage, chunks, lane, [&](int r) -> uint4* {
+        const uint32_t at = row0 + 32 * wave + r;
+        if (at >= rows) return nullptr;
+        uint32_t t, m;
+        f.group.split(at, t, m);
+        return reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.dq) +
+                                        (int64_t)(q0 + (int)t) * a.dq_stride +
+                                        (kv_head * f.group.size + m) * a.head_dim);
+    });
+}
+
+template <int HD>
+__global__ __launch_bounds__(64 * kWaves, 1) void dkv_kernel(BwdArgs f) {
+    using T = Tile<HD>;
+    __shared__ uint4 qt[2][kWalk * T::kChunks];
+    __shared__ uint4 ot[2][kWalk * T::kChunks];
+    __shared__ alignas(16) float stats[2][2][kWalk];     // [buffer][lse2, delta]
+    const AttnArgs& a = f.a;
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int chunks = a.head_dim >> 3;
+
+    const int tile = blockIdx.x / a.kv_heads, kv_head = blockIdx.x - tile * a.kv_heads;
+    const int item = item_of_tile(f.tiles, a.batch, tile);
+    const int key0 = (tile - f.tiles.start[item]) * kHeld;
+    const int q0 = a.q_items.start[item], nq = a.q_items.start[item + 1] - q0;
+    const int k0 = a.k_items.start[item], nk = a.k_items.start[item + 1] - k0;
+    const int group = f.group.size;
+    const int rows = nq * group;
+
+    const int key = key0 + 32 * wave + (lane & 31);
+    const bool live = key < nk;
+    bf16x8_t kf[T::kSteps], vf[T::kSteps];
+    load_query<HD>(kf,
+                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.k) +
+                                                  (int64_t)(k0 + (live ? key : 0)) * a.k_stride +
+                                                  kv_head * a.head_dim),
+                   live, chunks, lane);
+    load_query<HD>(vf,
+                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.v) +
+                                                  (int64_t)(k0 + (live ? key : 0)) * a.v_stride +
+                                                  kv_head * a.head_dim),
+                   live, chunks, lane);
+
+    // rows of this part; the first that see this workgroup's and this lane's
+    // keys (a causal row's token sees key j from token j - (nk - nq) on)
+    int part = (int)(((int64_t)rows + f.splits - 1) / f.splits);
+    part = (part + kWalk - 1) / kWalk * kWalk;
+    int begin = (int)min((int64_t)blockIdx.y * part, (int64_t)rows);
+    const int end = (int)min((int64_t)begin + part, (int64_t)rows);
+    int from = 0, all_from = 0;
+    if (a.causal) {
+        const int64_t r = (int64_t)(key - (nk - nq)) * group;
+        from = (int)min(max(r, (int64_t)0), (int64_t)rows);
+        all_from = (int)min(
+            max((int64_t)(key0 + 32 * wave + 31 - (nk - nq)) * group, (int64_t)0), (int64_t)rows);
+        const int64_t first = (int64_t)(key0 - (nk - nq)) * group;
+        if (first > begin) begin += (int)((min(first, (int64_t)end) - begin) / kWalk * kWalk);
+    }
+    const float c = a.scale * kLog2e;
+
+    f32x16 dk[T::kBlocks], dv[T::kBlocks];
+#pragma unroll
+    for (int b = 0; b < T::kBlocks; ++b) dk[b] = dv[b] = zero16();
+    if (chunks < T::kChunks) {
+        for (int i = 0; i < 2; ++i) {
+            T::clear(qt[i], kWalk, 64 * kWaves, threadIdx.x);
+            T::clear(ot[i], kWalk, 64 * kWaves, threadIdx.x);
+        }
+        __syncthreads();
+    }
+    const uint16_t* qb = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)q0 * a.q_stride +
+                         kv_head * group * a.head_dim;
+    const uint16_t* ob = reinterpret_cast<const uint16_t*>(a.dout) + (int64_t)q0 * a.dout_stride +
+                         kv_head * group * a.head_dim;
+    const int64_t stat = ((int64_t)a.q_items.start[a.batch] * kv_head + q0) * group;
+    // rows past the last repeat it; their P and dS are 0
+    float stat_next = 0.f;
+    auto fetch = [&](int buf, int row) {
+        if (threadIdx.x < 2 * kWalk) {
+            const int64_t at = stat + min(row + (int)(threadIdx.x % kWalk), rows - 1);
+            stat_next = threadIdx.x < kWalk ? f.lse2[at] : f.delta[at];
+        }
+        T::template load<kWalk, kWaves>(qt[buf], wave, lane, chunks, [&](int r) {
+            uint32_t t, m;
+            f.group.split(min(row + r, rows - 1), t, m);
+            return reinterpret_cast<const uint4*>(qb + (int64_t)t * a.q_stride + m * a.head_dim);
+        });
+        T::template load<kWalk, kWaves>(ot[buf], wave, lane, chunks, [&](int r) {
+            uint32_t t, m;
+            f.group.split(min(row + r, rows - 1), t, m);
+            return reinterpret_cast<const uint4*>(ob + (int64_t)t * a.dout_stride +
+                                                  m * a.head_dim);
+        });
+    };
+    if (begin < end) fetch(0, begin);
+    int buf = 0;
+    for (int row = begin; row < end; row += kWalk, buf ^= 1) {
+        if (threadIdx.x < 2 * kWalk) stats[buf][threadIdx.x / kWalk][threadIdx.x % kWalk] = stat_next;
+        tile_barrier();
+        if (row + kWalk < end) fetch(buf ^ 1, row + kWalk);
+        const bool masked = row < all_from || row + kWalk > end;
+#pragma unroll
+        for (int b = 0; b < kWalk / 32; ++b) {
+            f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+            for (int k = 0; k < T::kSteps; ++k) {
+                s = mfma(T::row_frag(qt[buf], 32 * b, lane, k), kf[k], s);
+                dp = mfma(T::row_frag(ot[buf], 32 * b, lane, k), vf[k], dp);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 l4 =
+                    *reinterpret_cast<const float4*>(&stats[buf][0][32 * b + 8 * j + 4 * h]);
+                const float4 d4 =
+                    *reinterpret_cast<const float4*>(&stats[buf][1][32 * b + 8 * j + 4 * h]);
+                const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[4 * j + i] = __builtin_amdgcn_exp2f(s[4 * j + i] * c - ls[i]);
+                    dp[4 * j + i] = s[4 * j + i] * (dp[4 * j + i] - ds[i]);
+                }
+            }
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int at = row + 32 * b + acc_row(i, h);
+                    if (at < from || at >= end) s[i] = dp[i] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const bf16x8_t p = acc_frag(s, t), ds = acc_frag(dp, t);
+#pragma unroll
+                for (int d = 0; d < T::kBlocks; ++d) {
+                    dv[d] = mfma(T::tr_frag(ot[buf], 32 * b + 16 * t, lane, d), p, dv[d]);
+                    dk[d] = mfma(T::tr_frag(qt[buf], 32 * b + 16 * t, lane, d), ds, dk[d]);
+                }
+            }
+        }
+    }
+
+    if (f.splits > 1) {
+        if (!live) return;
+        const int64_t all = (int64_t)a.k_items.start[a.batch] * a.kv_heads;
+        const int64_t at = (blockIdx.y * all + (int64_t)(k0 + key) * a.kv_heads + kv_head) *
+                           a.head_dim;
+        store_sums<HD>(dk, f.part + at, a.head_dim, lane);
+        store_sums<HD>(dv, f.part2 + at, a.head_dim, lane);
+        return;
+    }
+    tile_barrier();
+    uint4* stage = wave < 2 ? qt[wave] : ot[wave - 2];
+    auto to = [&](void* base, int64_t stride) {
+        return [=](int r) -> uint4* {
+            const int at = key0 + 32 * wave + r;
+            if (at >= nk) return nullptr;
+            return reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) +
+                                            (int64_t)(k0 + at) * stride + kv_head * a.head_dim);
+        };
+    };
+    store_rows<HD>(dk, a.scale, stage, chunks, lane, to(a.dk, a.dk_stride));
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    store_rows<HD>(dv, 1.0f, stage, chunks, lane, to(a.dv, a.dv_stride));
+}
+
+// Adds the parts of (token, head) rows in order: 32 lanes per row.
+__global__ __launch_bounds__(256) void join_kernel(const float* part, int splits, int64_t rows,
+                                                   int heads, int hd, float by, void* out,
+                                                   int64_t stride) {
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int d = (threadIdx.x & 31) * 4;
+    if (row >= rows || d >= hd) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < splits; ++p) {
+        const float4 v = *reinterpret_cast<const float4*>(part + (p * rows + row) * hd + d);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    const int64_t token = row / heads;
+    const int head = (int)(row - token * heads);
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + token * stride + head * hd + d) =
+        make_uint2(pack_bf16x2(s.x * by, s.y * by), pack_bf16x2(s.z * by, s.w * by));
+}
+
+hipError_t join(const float* part, int splits, int64_t rows, int heads, int hd, float by,
+                void* out, int64_t stride, hipStream_t s) {
+    join_kernel<<<dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s>>>(part, splits, rows, heads,
+                                                                      hd, by, out, stride);
+    return hipGetLastError();
+}
+
+template <int HD>
+hipError_t backward_as(BwdArgs& f, const AttnPlan& p, hipStream_t s) {
+    const AttnArgs& a = f.a;
+    const int64_t q_rows = (int64_t)a.q_items.start[a.batch] * a.heads;
+    const int64_t k_rows = (int64_t)a.k_items.start[a.batch] * a.kv_heads;
+    hipError_t e;
+    if (q_rows > 0) {
+        cut_items(a.q_items, a.batch, f.group.size, kHeld, &f.tiles);
+        f.splits = p.dq_splits;
+        dq_kernel<HD><<<dim3((unsigned)f.tiles.start[a.batch] * a.kv_heads, (unsigned)f.splits),
+                        dim3(64 * kWaves), 0, s>>>(f);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (f.splits > 1 && (e = join(f.part, f.splits, q_rows, a.heads, a.head_dim, a.scale, a.dq,
+                                      a.dq_stride, s)) != hipSuccess)
+            return e;
+    }
+    if (k_rows > 0) {
+        cut_items(a.k_items, a.batch, 1, kHeld, &f.tiles);
+        f.splits = p.dk_splits;
+        f.part2 = f.part + f.splits * k_rows * a.head_dim;
+        dkv_kernel<HD><<<dim3((unsigned)f.tiles.start[a.batch] * a.kv_heads, (unsigned)f.splits),
+                         dim3(64 * kWaves), 0, s>>>(f);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (f.splits > 1) {
+            if ((e = join(f.part, f.splits, k_rows, a.kv_heads, a.head_dim, a.scale, a.dk,
+                          a.dk_stride, s)) != hipSuccess)
+                return e;
+            return join(f.part2, f.splits, k_rows, a.kv_heads, a.head_dim, 1.0f, a.dv,
+                        a.dv_stride, s);
+        }
+    }
+    return hipSuccess;
+}
+
+// Parts of a walked axis of `most` entries when `blocks` workgroups hold the
+// other: none while the CUs are covered, else at least 256 entries each.
+int parts(int64_t blocks, int64_t most) {
+    if (blocks == 0 || blocks >= kComputeUnits) return 1;
+    const int64_t wanted = (2 * kComputeUnits + blocks - 1) / blocks;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(wanted, most / 256));
+}
+
+size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+}  // namespace
+
+void plan_attention_backward(const AttnArgs& a, AttnPlan* p) {
+    const Group g = group_of(a);
+    ItemTable rt, kt;
+    cut_items(a.q_items, a.batch, g.size, kHeld, &rt);
+    cut_items(a.k_items, a.batch, 1, kHeld, &kt);
+    int64_t most_rows = 0, most_keys = 0;
+    for (int b = 0; b < a.batch; ++b) {
+        most_rows = std::max<int64_t>(
+            most_rows, (int64_t)(a.q_items.start[b + 1] - a.q_items.start[b]) * g.size);
+        most_keys = std::max<int64_t>(most_keys, a.k_items.start[b + 1] - a.k_items.start[b]);
+    }
+    p->dq_splits = parts((int64_t)rt.start[a.batch] * a.kv_heads, most_keys);
+    p->dk_splits = parts((int64_t)kt.start[a.batch] * a.kv_heads, most_rows);
+    const size_t q_rows = (size_t)a.q_items.start[a.batch] * a.heads;
+    const size_t k_rows = (size_t)a.k_items.start[a.batch] * a.kv_heads;
+    const size_t dq = p->dq_splits > 1 ? p->dq_splits * q_rows : 0;
+    const size_t dk = p->dk_splits > 1 ? 2 * p->dk_splits * k_rows : 0;
+    p->backward_bytes = 256 + 2 * padded(q_rows * sizeof(float)) +
+                        std::max(dq, dk) * a.head_dim * sizeof(float);
+}
+
+hipError_t launch_attention_backward(const AttnArgs& a, const AttnPlan& p, void* ws,
+                                     hipStream_t s) {
+    const int64_t q_rows = (int64_t)a.q_items.start[a.batch] * a.heads;
+    BwdArgs f{};
+    f.a = a;
+    f.group = group_of(a);
+    char* at = static_cast<char*>(ws);
+    f.lse2 = reinterpret_cast<float*>(at);
+    at += padded(q_rows * sizeof(float));
+    f.delta = reinterpret_cast<float*>(at);
+    at += padded(q_rows * sizeof(float));
+    f.part = reinterpret_cast<float*>(at);
+    if (q_rows > 0) {
+        // (a launch holds under 2^32 threads)
+        const int64_t blocks = std::min<int64_t>((q_rows + 7) / 8, int64_t(1) << 22);
+        rows_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(f, q_rows);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return a.head_dim <= 64   ? backward_as<64>(f, p, s)
+           : a.head_dim <= 96 ? backward_as<96>(f, p, s)
+                              : backward_as<128>(f, p, s);
+}
+
+}  // namespace p3d

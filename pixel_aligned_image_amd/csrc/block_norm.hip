@@ -1,0 +1,495 @@
+// block_norm.hip -- p3d_gated_norm and p3d_gated_norm_backward: the step
+// between two branches of a transformer block (include/p3d_block.h).
+//
+//   t = post(y) post_weight,  r = x + s gate t,
+//   h = (pre(r) weight + bias)(1 + scale) + shift
+//
+// Both directions read every tensor once and keep a row in registers between
+// the read and the last write: the forward call moves 4 planes (x, y in; r, h
+// out), the backward call 6 (x, y, dh, dr in; dx, dy out), and nothing else
+// grows with the rows. Both are bound by memory. A row belongs to a group of
+// 16, 32, 64 or 256 threads, the smallest that holds it in at most VPT
+// 16-byte vectors each, so that its sums stay inside a wave wherever they can
+// (DPP, no LDS) and no lane idles on narrow rows.
+//
+// The variance is the mean of squared deviations from the mean already known
+// (the row is in registers, so the second pass is free), not a difference of
+// two large sums.
+#include <algorithm>
+
+#include "block_internal.h"
+
+namespace p3d {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Item of a row: the last one that starts at or before it.
+__device__ __forceinline__ int item_of(const ItemTable& t, int batch, int64_t row) {
+    int lo = 0, hi = batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.start[mid] <= row) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Sum over the TPR threads of a row. For TPR == kThreads, `red` holds one
+// float per wave and the two barriers keep its uses apart.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+    if constexpr (TPR <= 64) {
+        return lane_sum<TPR>(v);
+    } else {
+        v = lane_sum<64>(v);
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        return (red[0] + red[1]) + (red[2] + red[3]);
+    }
+}
+
+// A thread's vectors of a row: vector u * TPR + t, zeros past the row's end.
+template <typename T, int VPT, int TPR>
+struct RowVec {
+    static constexpr int N = Vec<T>::N;
+    float f[VPT][N];
+
+    __device__ __forceinline__ void load(const void* base, int64_t row, int nv, int t) {
+        const uint4* p = reinterpret_cast<const uint4*>(base) + row * nv;
+        uint4 q[VPT];
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int v = u * TPR + t;
+            q[u] = v < nv ? p[v] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) Vec<T>::widen(q[u], f[u]);
+    }
+    __device__ __forceinline__ void store(void* base, int64_t row, int nv, int t) const {
+        uint4* p = reinterpret_cast<uint4*>(base) + row * nv;
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int v = u * TPR + t;
+            if (v < nv) p[v] = Vec<T>::narrow(f[u]);
+        }
+    }
+};
+
+// One vector of a per-column parameter, `other` where it is absent.
+template <typename T>
+__device__ __forceinline__ void param(const void* base, int64_t offset, int v, int nv,
+                                      float other, float (&f)[Vec<T>::N]) {
+    if (base) {
+        const uint4* p = reinterpret_cast<const uint4*>(base) + offset;
+        Vec<T>::widen(v < nv ? p[v] : make_uint4(0, 0, 0, 0), f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < Vec<T>::N; ++e) f[e] = other;
+    }
+}
+
+// v <- (v - mean) / deviation in place (0 past the row's end); returns the
+// reciprocal deviation (1 for NONE).
+template <typename T, int VPT, int TPR>
+__device__ __forceinline__ float normalise(RowVec<T, VPT, TPR>& v, int kind, int nv, int t,
+                                           float inv_dim, float eps, float* red) {
+    constexpr int N = Vec<T>::N;
+    if (kind == P3D_NORM_NONE) return 1.0f;
+    if (kind == P3D_NORM_LAYER) {
+        float s = 0.f;
+#pragma unroll
+        for (int u = 0; u < VPT; ++u)
+#pragma unroll
+            for (int e = 0; e < N; ++e) s += v.f[u][e];
+        const float mean = row_sum<TPR>(s, red) * inv_dim;
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const bool in = u * TPR + t < nv;
+#pragma unroll
+            for (int e = 0; e < N; ++e) v.f[u][e] = in ? v.f[u][e] - mean : 0.f;
+        }
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u)
+#pragma unroll
+        for (int e = 0; e < N; ++e) q += v.f[u][e] * v.f[u][e];
+    const float rstd = 1.0f / sqrtf(row_sum<TPR>(q, red) * inv_dim + eps);
+#pragma unroll
+    for (int u = 0; u < VPT; ++u)
+#pragma unroll
+        for (int e = 0; e < N; ++e) v.f[u][e] *= rstd;
+    return rstd;
+}
+
+// d <- the gradient of the norm's input from the gradient d of its output n:
+// rstd (d - n mean(d n) - mean(d)), the last term for LAYER only.
+template <typename T, int VPT, int TPR>
+__device__ __forceinline__ void normalise_backward(RowVec<T, VPT, TPR>& d,
+                                                   const RowVec<T, VPT, TPR>& n, int kind,
+                                                   float rstd, int nv, int t, float inv_dim,
+                                                   float* red) {
+    constexpr int N = Vec<T>::N;
+    if (kind == P3D_NORM_NONE) return;
+    float s = 0.f, q = 0.f;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            s += d.f[u][e];
+            q += d.f[u][e] * n.f[u][e];
+        }
+    const float dot = row_sum<TPR>(q, red) * inv_dim;
+    const float mean = kind == P3D_NORM_LAYER ? row_sum<TPR>(s, red) * inv_dim : 0.f;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u)
+#pragma unroll
+        for (int e = 0; e < N; ++e) d.f[u][e] = rstd * (d.f[u][e] - n.f[u][e] * dot - mean);
+}
+
+template <typename T, int VPT, int TPR>
+__global__ __launch_bounds__(kThreads) void gated_norm_kernel(NormArgs a, ItemTable items) {
+    constexpr int N = Vec<T>::N;
+    __shared__ float red[4];
+    const int t = threadIdx.x % TPR;
+    const int nv = a.dim / N;
+    const float inv_dim = 1.0f / (float)a.dim;
+    // a row's threads take every turn of the loop together
+    for (int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR; row < a.n;
+         row += (int64_t)gridDim.x * (kThreads / TPR)) {
+        const int64_t mod = item_of(items, a.batch, row) * (a.mod_stride / N);
+        RowVec<T, VPT, TPR> x;
+        x.load(a.x, row, nv, t);
+        if (a.y) {
+            RowVec<T, VPT, TPR> y;
+            y.load(a.y, row, nv, t);
+            normalise(y, a.post, nv, t, inv_dim, a.eps, red);
+#pragma unroll
+            for (int u = 0; u < VPT; ++u) {
+                const int v = u * TPR + t;
+                float g[N], w[N];
+                param<T>(a.gate, mod, v, nv, 1.f, g);
+                param<T>(a.post_weight, 0, v, nv, 1.f, w);
+#pragma unroll
+                for (int e = 0; e < N; ++e) x.f[u][e] += a.res_scale * g[e] * (y.f[u][e] * w[e]);
+            }
+        }
+        if (a.r) x.store(a.r, row, nv, t);
+        normalise(x, a.pre, nv, t, inv_dim, a.eps, red);
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int v = u * TPR + t;
+            float w[N], b[N], sc[N], sh[N];
+            param<T>(a.weight, 0, v, nv, 1.f, w);
+            param<T>(a.bias, 0, v, nv, 0.f, b);
+            param<T>(a.scale, mod, v, nv, 0.f, sc);
+            param<T>(a.shift, mod, v, nv, 0.f, sh);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                x.f[u][e] = (x.f[u][e] * w[e] + b[e]) * (1.0f + sc[e]) + sh[e];
+        }
+        x.store(a.h, row, nv, t);
+    }
+}
+
+// The three column sums that every parameter gradient is made of, per item:
+// A = sum dh n, S = sum dh, G = sum dr t^ (n, t^ the normalised r and y). A
+// workgroup walks one chunk of one item's rows with its sums in registers,
+// joins its row groups through LDS in a fixed order and writes [3][dim]
+// binary32 values; no atomics, so the sums' order never changes.
+template <typename T, int VPT, int TPR>
+__global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(NormArgs a,
+                                                                       ItemTable items,
+                                                                       ItemTable chunks,
+                                                                       int64_t rows_per_chunk) {
+    constexpr int N = Vec<T>::N;
+    constexpr int R = kThreads / TPR;        // rows in flight
+    __shared__ float red[4];
+    __shared__ float cols[R * TPR * VPT * N];
+    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const int nv = a.dim / N;
+    const float inv_dim = 1.0f / (float)a.dim;
+    const int item = item_of(chunks, a.batch, blockIdx.x);
+    const int64_t first = items.start[item] +
+                          (int64_t)((int)blockIdx.x - chunks.start[item]) * rows_per_chunk;
+    const int64_t end = min(first + rows_per_chunk, (int64_t)items.start[item + 1]);
+    const int64_t mod = item * (a.mod_stride / N);
+
+    float sums[3][VPT][N];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int u = 0; u < VPT; ++u)
+#pragma unroll
+            for (int e = 0; e < N; ++e) sums[k][u][e] = 0.f;
+
+    for (int64_t row = first + group; row < end; row += R) {
+        RowVec<T, VPT, TPR> x, y, d, dr;
+        x.load(a.x, row, nv, t);
+        if (a.y) y.load(a.y, row, nv, t);
+        d.load(a.dh, row, nv, t);
+        if (a.dr) dr.load(a.dr, row, nv, t);
+        float y_rstd = 1.f;
+        if (a.y) {
+            y_rstd = normalise(y, a.post, nv, t, inv_dim, a.eps, red);
+#pragma unroll
+            for (int u = 0; u < VPT; ++u) {
+                const int v = u * TPR + t;
+                float g[N], w[N];
+                param<T>(a.gate, mod, v, nv, 1.f, g);
+                param<T>(a.post_weight, 0, v, nv, 1.f, w);
+#pragma unroll
+                for (int e = 0; e < N; ++e) x.f[u][e] += a.res_scale * g[e] * (y.f[u][e] * w[e]);
+            }
+        }
+        const float rstd = normalise(x, a.pre, nv, t, inv_dim, a.eps, red);
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int v = u * TPR + t;
+            float w[N], sc[N];
+            param<T>(a.weight, 0, v, nv, 1.f, w);
+            param<T>(a.scale, mod, v, nv, 0.f, sc);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                sums[0][u][e] += d.f[u][e] * x.f[u][e];
+                sums[1][u][e] += d.f[u][e];
+                d.f[u][e] *= (1.0f + sc[e]) * w[e];
+            }
+        }
+        normalise_backward(d, x, a.pre, rstd, nv, t, inv_dim, red);
+        if (a.dr) {
+#pragma unroll
+            for (int u = 0; u < VPT; ++u)
+#pragma unroll
+                for (int e = 0; e < N; ++e) d.f[u][e] += dr.f[u][e];
+        }
+        d.store(a.dx, row, nv, t);
+        if (a.y) {
+#pragma unroll
+            for (int u = 0; u < VPT; ++u) {
+                const int v = u * TPR + t;
+                float g[N], w[N];
+                param<T>(a.gate, mod, v, nv, 1.f, g);
+                param<T>(a.post_weight, 0, v, nv, 1.f, w);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    sums[2][u][e] += d.f[u][e] * y.f[u][e];
+                    d.f[u][e] *= a.res_scale * g[e] * w[e];
+                }
+            }
+            if (a.dy) {
+                normalise_backward(d, y, a.post, y_rstd, nv, t, inv_dim, red);
+                d.store(a.dy, row, nv, t);
+            }
+        }
+    }
+
+    if (!a.partial) return;
+    float* out = a.partial + (int64_t)blockIdx.x * 3 * a.dim;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < VPT; ++u)
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                cols[(group * VPT * TPR + u * TPR + t) * N + e] = sums[k][u][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.dim; c += kThreads) {
+            float s = 0.f;
+            for (int g = 0; g < R; ++g) s += cols[g * VPT * TPR * N + c];
+            out[k * a.dim + c] = s;
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float column(const void* base, int64_t i, float other) {
+    if (!base) return other;
+    if constexpr (sizeof(T) == 4) return reinterpret_cast<const float*>(base)[i];
+    else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[i] << 16);
+}
+
+// Joins an item's chunks: 32 columns by 32 chunk lanes per workgroup, each
+// lane a fixed share of the chunks.
+constexpr int kJoinCols = 32, kJoinLanes = 32;
+
+template <typename T>
+__global__ __launch_bounds__(kJoinCols* kJoinLanes) void norm_join_kernel(NormArgs a,
+                                                                          ItemTable chunks,
+                                                                          float* item_sums) {
+    __shared__ float part[3][kJoinLanes][kJoinCols + 1];
+    const int col = threadIdx.x % kJoinCols, lane = threadIdx.x / kJoinCols;
+    const int c = blockIdx.x * kJoinCols + col;
+    const int item = blockIdx.y;
+    const int64_t D = a.dim;
+    float s[3] = {0.f, 0.f, 0.f};
+    if (c < D) {
+        for (int q = chunks.start[item] + lane; q < chunks.start[item + 1]; q += kJoinLanes) {
+            const float* p = a.partial + q * 3 * D + c;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) s[k] += p[k * D];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) part[k][lane][col] = s[k];
+    __syncthreads();
+    if (lane || c >= D) return;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        s[k] = 0.f;
+        for (int l = 0; l < kJoinLanes; ++l) s[k] += part[k][l][col];
+    }
+    const float A = s[0], S = s[1], G = s[2];
+    const int64_t at = item * D + c;
+    const float gate = column<T>(a.gate, item * a.mod_stride + c, 1.f);
+    const float scale = 1.0f + column<T>(a.scale, item * a.mod_stride + c, 0.f);
+    if (a.dgate) a.dgate[at] = a.res_scale * column<T>(a.post_weight, c, 1.f) * G;
+    if (a.dscale)
+        a.dscale[at] = column<T>(a.weight, c, 1.f) * A + column<T>(a.bias, c, 0.f) * S;
+    if (a.dshift) a.dshift[at] = S;
+    if (item_sums) {
+        float* o = item_sums + (int64_t)item * 3 * D + c;
+        o[0] = scale * A;
+        o[D] = scale * S;
+        o[2 * D] = a.res_scale * gate * G;
+    } else {                                 // one item: its sums are the whole
+        if (a.dweight) a.dweight[c] = scale * A;
+        if (a.dbias) a.dbias[c] = scale * S;
+        if (a.dpost_weight) a.dpost_weight[c] = a.res_scale * gate * G;
+    }
+}
+
+// The [dim] parameters' gradients: the items' shares added in item order.
+__global__ __launch_bounds__(kThreads) void norm_items_kernel(NormArgs a,
+                                                              const float* item_sums) {
+    const int c = blockIdx.x * kThreads + threadIdx.x;
+    if (c >= a.dim) return;
+    const int64_t D = a.dim;
+    float s[3] = {0.f, 0.f, 0.f};
+    for (int b = 0; b < a.batch; ++b)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) s[k] += item_sums[(b * 3 + k) * D + c];
+    if (a.dweight) a.dweight[c] = s[0];
+    if (a.dbias) a.dbias[c] = s[1];
+    if (a.dpost_weight) a.dpost_weight[c] = s[2];
+}
+
+template <typename T, int VPT, int TPR>
+hipError_t forward_as(const NormArgs& a, const ItemTable& items, hipStream_t s) {
+    const int64_t rows = kThreads / TPR;
+    // (a launch holds under 2^32 threads)
+    const int64_t blocks = std::min<int64_t>((a.n + rows - 1) / rows, int64_t(1) << 22);
+    gated_norm_kernel<T, VPT, TPR><<<dim3((unsigned)blocks), dim3(kThreads), 0, s>>>(a, items);
+    return hipGetLastError();
+}
+
+template <typename T, int VPT, int TPR>
+hipError_t backward_as(const NormArgs& a, const ItemTable& items, const ItemTable& chunks,
+                       int64_t rows_per_chunk, hipStream_t s) {
+    gated_norm_backward_kernel<T, VPT, TPR>
+        <<<dim3((unsigned)chunks.start[a.batch]), dim3(kThreads), 0, s>>>(a, items, chunks,
+                                                                        rows_per_chunk);
+    return hipGetLastError();
+}
+
+// The group of threads of a row of `nv` vectors, and its vectors per thread:
+// the smallest group that needs at most 4 (bf16) or 8 (binary32, half as wide)
+// vectors per thread.
+#define P3D_NORM_SHAPES(T, CALL)                                                        \
+    if (nv <= 16) return CALL(T, 1, 16);                                                \
+    if (nv <= 32) return CALL(T, 1, 32);                                                \
+    if (nv <= 64) return CALL(T, 1, 64);                                                \
+    if (nv <= 128) return CALL(T, 2, 64);                                               \
+    if (nv <= 192) return CALL(T, 3, 64);                                               \
+    if (nv <= 256) return CALL(T, 4, 64);
+
+template <typename T>
+hipError_t forward_of(const NormArgs& a, const ItemTable& items, hipStream_t s) {
+    const int nv = a.dim / Vec<T>::N;
+#define CALL(T, V, P) forward_as<T, V, P>(a, items, s)
+    P3D_NORM_SHAPES(T, CALL)
+    if constexpr (Vec<T>::N == 4) {
+        if (nv <= 384) return CALL(T, 6, 64);
+        if (nv <= 512) return CALL(T, 8, 64);
+    }
+    if constexpr (Vec<T>::N == 4) {
+        if (nv > 1024) return CALL(T, 8, 256);
+    }
+    if (nv <= 512) return CALL(T, 2, 256);
+    return CALL(T, 4, 256);
+#undef CALL
+}
+
+template <typename T>
+hipError_t backward_of(const NormArgs& a, const ItemTable& items, const ItemTable& chunks,
+                       int64_t rpc, hipStream_t s) {
+    const int nv = a.dim / Vec<T>::N;
+#define CALL(T, V, P) backward_as<T, V, P>(a, items, chunks, rpc, s)
+    P3D_NORM_SHAPES(T, CALL)
+    if constexpr (Vec<T>::N == 4) {
+        if (nv <= 384) return CALL(T, 6, 64);
+        if (nv <= 512) return CALL(T, 8, 64);
+    }
+    if constexpr (Vec<T>::N == 4) {
+        if (nv > 1024) return CALL(T, 8, 256);
+    }
+    if (nv <= 512) return CALL(T, 2, 256);
+    return CALL(T, 4, 256);
+#undef CALL
+}
+
+}  // namespace
+
+// About four workgroups per CU, and at least 16 rows each, so that the chunk
+// sums (12 bytes per column and chunk, written and read once) stay small
+// beside the rows.
+int64_t norm_chunks(int64_t n, int32_t batch, const ItemTable& items, ItemTable* chunks) {
+    int64_t rpc = (n + 4 * kComputeUnits - 1) / (4 * kComputeUnits);
+    if (rpc < 16) rpc = 16;
+    int32_t at = 0;
+    for (int32_t b = 0; b < batch; ++b) {
+        chunks->start[b] = at;
+        at += (int32_t)((items.start[b + 1] - items.start[b] + rpc - 1) / rpc);
+    }
+    for (int32_t b = batch; b <= P3D_MAX_BATCH; ++b) chunks->start[b] = at;
+    return rpc;
+}
+
+hipError_t launch_gated_norm(const NormArgs& a, p3d_dtype dt, const ItemTable& items,
+                             hipStream_t s) {
+    return dt == P3D_BF16 ? forward_of<Bf16>(a, items, s) : forward_of<float>(a, items, s);
+}
+
+hipError_t launch_gated_norm_backward(const NormArgs& args, p3d_dtype dt, const ItemTable& items,
+                                      hipStream_t s) {
+    NormArgs a = args;
+    ItemTable chunks;
+    const int64_t rpc = norm_chunks(a.n, a.batch, items, &chunks);
+    const bool shared = a.dweight || a.dbias || a.dpost_weight;
+    const bool sums = shared || a.dgate || a.dscale || a.dshift;
+    if (!sums) a.partial = nullptr;
+    if (chunks.start[a.batch] > 0) {
+        const hipError_t e = dt == P3D_BF16 ? backward_of<Bf16>(a, items, chunks, rpc, s)
+                                            : backward_of<float>(a, items, chunks, rpc, s);
+        if (e != hipSuccess) return e;
+    }
+    if (!sums) return hipSuccess;
+    float* item_sums = shared && a.batch > 1
+                           ? a.partial + (int64_t)chunks.start[a.batch] * 3 * a.dim
+                           : nullptr;
+    const dim3 grid((unsigned)((a.dim + kJoinCols - 1) / kJoinCols), (unsigned)a.batch);
+    if (dt == P3D_BF16)
+        norm_join_kernel<Bf16><<<grid, dim3(kJoinCols * kJoinLanes), 0, s>>>(a, chunks, item_sums);
+    else
+        norm_join_kernel<float><<<grid, dim3(kJoinCols * kJoinLanes), 0, s>>>(a, chunks, item_sums);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !item_sums) return e;
+    norm_items_kernel<<<dim3((unsigned)((a.dim + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(
+        a, item_sums);
+    return hipGetLastError();
+}
+
+}  // namespace p3d
