@@ -17,6 +17,7 @@
 // Where few tiles face a long axis the walked axis is cut into parts whose
 // binary32 sums go to the workspace and are joined by join_kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_tile.h"
 
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
 }
 
 template <int HD>
-__global__ __launch_bounds__(64 * kWaves, 1) void dkv_kernel(BwdArgs f) {
+__global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     using T = Tile<HD>;
     __shared__ uint4 qt[2][kWalk * T::kChunks];
     __shared__ uint4 ot[2][kWalk * T::kChunks];
@@ -302,20 +303,24 @@ __global__ __launch_bounds__(64 * kWaves, 1) void dkv_kernel(BwdArgs f) {
         });
     };
     if (begin < end) fetch(0, begin);
-    int buf = 0;
-    for (int row = begin; row < end; row += kWalk, buf ^= 1) {
+    auto walk = [&](auto which, int row) {
+        constexpr int buf = decltype(which)::value;
         if (threadIdx.x < 2 * kWalk) stats[buf][threadIdx.x / kWalk][threadIdx.x % kWalk] = stat_next;
         tile_barrier();
         if (row + kWalk < end) fetch(buf ^ 1, row + kWalk);
+        __builtin_amdgcn_sched_barrier(0);
         const bool masked = row < all_from || row + kWalk > end;
 #pragma unroll
         for (int b = 0; b < kWalk / 32; ++b) {
+            int l = lane;
+            asm volatile("" : "+v"(l));
             f32x16 s = zero16(), dp = zero16();
 #pragma unroll
             for (int k = 0; k < T::kSteps; ++k) {
-                s = mfma(T::row_frag(qt[buf], 32 * b, lane, k), kf[k], s);
-                dp = mfma(T::row_frag(ot[buf], 32 * b, lane, k), vf[k], dp);
+                s = mfma(T::row_frag(qt[buf], 32 * b, l, k), kf[k], s);
+                dp = mfma(T::row_frag(ot[buf], 32 * b, l, k), vf[k], dp);
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float4 l4 =
@@ -336,16 +341,23 @@ __global__ __launch_bounds__(64 * kWaves, 1) void dkv_kernel(BwdArgs f) {
                     if (at < from || at >= end) s[i] = dp[i] = 0.f;
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("" : "+v"(l));
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const bf16x8_t p = acc_frag(s, t), ds = acc_frag(dp, t);
 #pragma unroll
                 for (int d = 0; d < T::kBlocks; ++d) {
-                    dv[d] = mfma(T::tr_frag(ot[buf], 32 * b + 16 * t, lane, d), p, dv[d]);
-                    dk[d] = mfma(T::tr_frag(qt[buf], 32 * b + 16 * t, lane, d), ds, dk[d]);
+                    dv[d] = mfma(T::tr_frag(ot[buf], 32 * b + 16 * t, l, d), p, dv[d]);
+                    dk[d] = mfma(T::tr_frag(qt[buf], 32 * b + 16 * t, l, d), ds, dk[d]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    for (int row = begin; row < end; row += 2 * kWalk) {
+        walk(std::integral_constant<int, 0>{}, row);
+        if (row + kWalk < end) walk(std::integral_constant<int, 1>{}, row + kWalk);
     }
 
     if (f.splits > 1) {
@@ -435,11 +447,12 @@ hipError_t backward_as(BwdArgs& f, const AttnPlan& p, hipStream_t s) {
 }
 
 // Parts of a walked axis of `most` entries when `blocks` workgroups hold the
-// other: none while the CUs are covered, else at least 256 entries each.
+// other.
 int parts(int64_t blocks, int64_t most) {
-    if (blocks == 0 || blocks >= kComputeUnits) return 1;
-    const int64_t wanted = (2 * kComputeUnits + blocks - 1) / blocks;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(wanted, most / 256));
+    if (blocks == 0 || blocks >= 4 * kComputeUnits) return 1;
+    const bool few = blocks < kComputeUnits;
+    const int64_t wanted = ((few ? 2 : 4) * kComputeUnits + blocks - 1) / blocks;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(wanted, most / (few ? 256 : 1024)));
 }
 
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
