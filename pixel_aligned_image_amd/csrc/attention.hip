@@ -12,9 +12,11 @@
 // larger than with the exact maximum, which costs no bits, and the 2^5 or 2^6
 // multiplications that a new maximum brings are rarely due.
 //
-// With few rows and many keys the keys are cut into `splits` parts, each of
-// which leaves (m, l, O) in the workspace, joined by combine_kernel.
+// Where the row tiles do not fill the chip's last round the keys of the last
+// ones are cut into parts, each of which leaves (m, l, O) in the workspace,
+// joined by combine_kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_tile.h"
 
@@ -27,101 +29,210 @@ using namespace attn;
 constexpr int kKeys = 64;                // keys per tile of attention_kernel
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;       // query rows per workgroup
+constexpr int kSingleRows = 32;          // query rows of attention_single_kernel
 constexpr int kSingleKeys = 32;          // keys per wave tile of attention_single_kernel
+constexpr int kMostParts = 64;           // a wave joins them, one lane each
 
 struct FwdArgs {
     AttnArgs a;
     ItemTable tiles;                     // first row tile of every item
     Group group;
-    int splits;
-    float* part_o;                       // [splits][nq * heads][head_dim]
-    float2* part_ml;                     // [splits][nq * heads]
+    int whole, parts;                    // units run whole; parts of every later one
+    float* part_o;                       // [(unit - whole) * parts + part][rows][head_dim]
+    float2* part_ml;                     // [(unit - whole) * parts + part][rows]
 };
+
+// A unit of the launch: one row tile of one key head. Tiles of an item run
+// the longest causal ones first and key heads fastest: workgroups go to the
+// XCDs in turn, so with 8 (or 16, 24, ...) key heads an XCD's L2 holds the
+// same heads throughout.
+struct Unit {
+    int item, kv_head, q0, nq, k0, nk;
+    uint32_t row0, rows;                 // first row of the tile, rows of the item
+
+    __device__ __forceinline__ Unit(const FwdArgs& f, int unit, int per_tile) {
+        const AttnArgs& a = f.a;
+        const int tile = unit / a.kv_heads;
+        kv_head = unit - tile * a.kv_heads;
+        item = item_of_tile(f.tiles, a.batch, tile);
+        const int tiles = f.tiles.start[item + 1] - f.tiles.start[item];
+        const int nth = tile - f.tiles.start[item];
+        row0 = (uint32_t)(a.causal ? tiles - 1 - nth : nth) * per_tile;
+        q0 = a.q_items.start[item];
+        nq = a.q_items.start[item + 1] - q0;
+        k0 = a.k_items.start[item];
+        nk = a.k_items.start[item + 1] - k0;
+        rows = (uint32_t)nq * f.group.size;
+    }
+};
+
+// The unit of a workgroup, and which part of its keys (-1: all).
+__device__ __forceinline__ int unit_of(const FwdArgs& f, int block, int& part) {
+    part = -1;
+    if (block < f.whole) return block;
+    const int u = (block - f.whole) / f.parts;
+    part = block - f.whole - u * f.parts;
+    return f.whole + u;
+}
 
 // One row tile's running softmax: lane l's query is l % 32, and the two
 // halves hold different keys (and different columns of O).
 template <int HD>
 struct Softmax {
-    f32x16 o[Tile<HD>::kBlocks];
+    using T = Tile<HD>;
+    f32x16 o[T::kBlocks];
     float m, l;                          // l: this half's share
 
     __device__ __forceinline__ void init() {
 #pragma unroll
-        for (int b = 0; b < Tile<HD>::kBlocks; ++b) o[b] = zero16();
+        for (int b = 0; b < T::kBlocks; ++b) o[b] = zero16();
         m = -INFINITY;
         l = 0.f;
     }
 
-    // Keys key0 .. key0 + 32 NB - 1 in the tiles' rows 0 ..; those at or past
-    // `limit` are not seen. c = scale log2(e).
+    // S^T of 64 keys (two blocks of 32).
+    __device__ __forceinline__ void scores(f32x16 (&s)[2], const bf16x8_t (&q)[T::kSteps],
+                                           const uint4* kt, int lane) const {
+        const uint32_t at = T::row_base(kt, lane);
+        s[0] = s[1] = zero16();
+#pragma unroll
+        for (int k = 0; k < T::kSteps; ++k)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) s[b] = mfma(T::row_frag(at, 32 * b, k), q[k], s[b]);
+        // reads run six matrix instructions ahead
+        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * T::kSteps; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+    }
+
+    // Keys at or past `limit` are not seen.
     template <int NB>
-    __device__ __forceinline__ void attend(const bf16x8_t (&q)[Tile<HD>::kSteps], const uint4* kt,
-                                           const uint4* vt, int key0, int limit, bool masked,
-                                           float c, int lane) {
-        using T = Tile<HD>;
-        const int h = lane >> 5;
-        f32x16 s[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            s[b] = zero16();
-#pragma unroll
-            for (int k = 0; k < T::kSteps; ++k)
-                s[b] = mfma(T::row_frag(kt, 32 * b, lane, k), q[k], s[b]);
-        }
-        if (masked) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (key0 + 32 * b + acc_row(i, h) >= limit) s[b][i] = -INFINITY;
-        }
-        float top = -INFINITY;
+    __device__ __forceinline__ void mask(f32x16 (&s)[NB], int key0, int limit, int lane) const {
+        const int left = limit - key0 - 4 * (lane >> 5);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+            for (int i = 0; i < 16; ++i)
+                if (32 * b + acc_row(i, 0) >= left) s[b][i] = -INFINITY;
+    }
+
+    template <int NB>
+    __device__ __forceinline__ float top(const f32x16 (&s)[NB]) const {
+        float t = s[0][0];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) t = fmaxf(t, s[b][i]);
         float own;
-        const float other = other_half(top, own);
-        top = fmaxf(own, other);
-        if (__any((top - m) * c > 8.0f || (m == -INFINITY && top > m))) {
-            const float raised = fmaxf(m, top);
-            const float by = raised == -INFINITY ? 0.f
-                                                 : __builtin_amdgcn_exp2f((m - raised) * c);
-            m = raised;
-            l *= by;
+        const float other = other_half(t, own);
+        return fmaxf(own, other);
+    }
+
+    // Whether a query of the wave needs a new maximum.
+    template <int NB>
+    __device__ __forceinline__ bool exceeds(const f32x16 (&s)[NB], float c) const {
+        return __any((top(s) - m) * c > 8.0f);
+    }
+
+    // The new maximum.
+    template <int NB>
+    __device__ __forceinline__ void raise(const f32x16 (&s)[NB], float c) {
+        const float raised = fmaxf(m, top(s));
+        const float by = raised == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - raised) * c);
+        m = raised;
+        l *= by;
 #pragma unroll
-            for (int b = 0; b < T::kBlocks; ++b)
+        for (int b = 0; b < T::kBlocks; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[b][i] *= by;
-        }
+            for (int i = 0; i < 16; ++i) o[b][i] *= by;
+    }
+
+    // P^T of 64 keys and its share of l.
+    __device__ __forceinline__ void exponentials(const f32x16 (&s)[2], bf16x8_t (&p)[4],
+                                                 float c) {
         const float base = m == -INFINITY ? 0.f : m * c;
         float sum = 0.f;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < 2; ++b) {
+            f32x16 e;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                s[b][i] = __builtin_amdgcn_exp2f(s[b][i] * c - base);
-                sum += s[b][i];
+                e[i] = __builtin_amdgcn_exp2f(s[b][i] * c - base);
+                sum += e[i];
             }
+            p[2 * b] = acc_frag(e, 0);
+            p[2 * b + 1] = acc_frag(e, 1);
+        }
+        l += sum;
+    }
+
+    // O^T += V^T P^T over 64 keys.
+    __device__ __forceinline__ void add(const bf16x8_t (&p)[4], const uint4* vt, int lane) {
+        const uint32_t at = T::tr_base(vt, lane);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int d = 0; d < T::kBlocks; ++d)
+                o[d] = mfma(T::tr_frag(at, 16 * t, d), p[t], o[d]);
+    }
+
+    // add() of the tile before with `p`, and exponentials() of this one into
+    // it: independent of each other, issued in turn.
+    __device__ __forceinline__ void exponentials_and_add(const f32x16 (&s)[2], bf16x8_t (&p)[4],
+                                                         const uint4* vt, float c, int lane) {
+        bf16x8_t next[4];
+        add(p, vt, lane);
+        exponentials(s, next, c);
+        // 8 transposed reads ahead, then per matrix instruction 2 reads and
+        // its share of the 128 vector instructions
+        __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+        for (int i = 0; i < 4 * T::kBlocks; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 32 / T::kBlocks, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = next[i];
+    }
+
+    // One block of 32 keys, start to end.
+    __device__ __forceinline__ void attend(const bf16x8_t (&q)[T::kSteps], const uint4* kt,
+                                           const uint4* vt, int key0, int limit, bool masked,
+                                           float c, int lane) {
+        const uint32_t k_at = T::row_base(kt, lane), v_at = T::tr_base(vt, lane);
+        f32x16 s[1];
+        s[0] = zero16();
+#pragma unroll
+        for (int k = 0; k < T::kSteps; ++k) s[0] = mfma(T::row_frag(k_at, 0, k), q[k], s[0]);
+        if (masked) mask(s, key0, limit, lane);
+        if (exceeds(s, c)) raise(s, c);
+        const float base = m == -INFINITY ? 0.f : m * c;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[0][i] = __builtin_amdgcn_exp2f(s[0][i] * c - base);
+            sum += s[0][i];
+        }
         l += sum;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int t = 0; t < 2; ++t) {
+            const bf16x8_t p = acc_frag(s[0], t);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const bf16x8_t p = acc_frag(s[b], t);
-#pragma unroll
-                for (int d = 0; d < T::kBlocks; ++d)
-                    o[d] = mfma(T::tr_frag(vt, 32 * b + 16 * t, lane, d), p, o[d]);
-            }
+            for (int d = 0; d < T::kBlocks; ++d)
+                o[d] = mfma(T::tr_frag(v_at, 16 * t, d), p, o[d]);
+        }
     }
 };
 
-// A part's (m, l, O) to the workspace; `row` is token * heads + head.
+// A part's (m, l, O) to the workspace; `at` counts rows of parts.
 template <int HD>
-__device__ __forceinline__ void store_part(const FwdArgs& f, const Softmax<HD>& st, int part,
-                                           int64_t row, int64_t rows, float l, int lane) {
+__device__ __forceinline__ void store_part(const FwdArgs& f, const Softmax<HD>& st, int64_t at,
+                                           float l, int lane) {
     const int h = lane >> 5, hd = f.a.head_dim;
-    const int64_t at = part * rows + row;
     if (h == 0) f.part_ml[at] = make_float2(st.m, l);
     float* o = f.part_o + at * hd;
 #pragma unroll
@@ -140,23 +251,17 @@ template <int HD>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(FwdArgs f) {
     using T = Tile<HD>;
     __shared__ uint4 kt[2][kKeys * T::kChunks];
-    __shared__ uint4 vt[2][kKeys * T::kChunks];
+    __shared__ uint4 vt[3][kKeys * T::kChunks];
     const AttnArgs& a = f.a;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int chunks = a.head_dim >> 3;
 
-    // Row tiles of an item, the longest causal ones first, key heads fastest:
-    // workgroups go to the XCDs in turn, so with 8 (or 16, 24, ...) key heads
-    // an XCD's L2 holds the same heads throughout.
-    const int tile = blockIdx.x / a.kv_heads, kv_head = blockIdx.x - tile * a.kv_heads;
-    const int item = item_of_tile(f.tiles, a.batch, tile);
-    const int tiles = f.tiles.start[item + 1] - f.tiles.start[item];
-    const int nth = tile - f.tiles.start[item];
-    const uint32_t row0 = (uint32_t)(a.causal ? tiles - 1 - nth : nth) * kRows;
-    const int q0 = a.q_items.start[item], nq = a.q_items.start[item + 1] - q0;
-    const int k0 = a.k_items.start[item], nk = a.k_items.start[item + 1] - k0;
-    const uint32_t rows = (uint32_t)nq * f.group.size;
+    int which;
+    const int unit = unit_of(f, blockIdx.x, which);
+    const Unit u(f, unit, kRows);
+    const int kv_head = u.kv_head, q0 = u.q0, nq = u.nq, k0 = u.k0, nk = u.nk;
+    const uint32_t row0 = u.row0, rows = u.rows;
 
     // this lane's query
     const uint32_t row = row0 + 32 * wave + (lane & 31);
@@ -172,10 +277,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(FwdArgs f) {
                    live, chunks, lane);
 
     // keys of this part, and those this workgroup and this lane see
-    int part = (nk + f.splits - 1) / f.splits;
-    part = (part + kKeys - 1) / kKeys * kKeys;
-    const int begin = (int)min((int64_t)blockIdx.y * part, (int64_t)nk);
-    int end = (int)min((int64_t)begin + part, (int64_t)nk);
+    const int parts = which < 0 ? 1 : f.parts;
+    int share = (nk + parts - 1) / parts;
+    share = (share + kKeys - 1) / kKeys * kKeys;
+    const int begin = (int)min((int64_t)max(which, 0) * share, (int64_t)nk);
+    int end = (int)min((int64_t)begin + share, (int64_t)nk);
     int limit = end;
     if (a.causal) {
         limit = min(end, live ? (int)token + nk - nq + 1 : end);
@@ -190,41 +296,81 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(FwdArgs f) {
     Softmax<HD> st;
     st.init();
     if (chunks < T::kChunks) {
-        for (int i = 0; i < 2; ++i) {
-            T::clear(kt[i], kKeys, 64 * kWaves, threadIdx.x);
-            T::clear(vt[i], kKeys, 64 * kWaves, threadIdx.x);
-        }
+        for (int i = 0; i < 2; ++i) T::clear(kt[i], kKeys, 64 * kWaves, threadIdx.x);
+        for (int i = 0; i < 3; ++i) T::clear(vt[i], kKeys, 64 * kWaves, threadIdx.x);
         __syncthreads();
     }
     const uint16_t* kb = reinterpret_cast<const uint16_t*>(a.k) + (int64_t)k0 * a.k_stride +
                          kv_head * a.head_dim;
     const uint16_t* vb = reinterpret_cast<const uint16_t*>(a.v) + (int64_t)k0 * a.v_stride +
                          kv_head * a.head_dim;
+    const int64_t k_pitch = a.k_stride * 2, v_pitch = a.v_stride * 2;
+    const bool near = max(k_pitch, v_pitch) <= T::kMaxPitch;
+    const uint32_t k_off = T::lane_offset(wave, lane, k_pitch);
+    const uint32_t v_off = T::lane_offset(wave, lane, v_pitch);
+    const bool on = T::lane_chunk(wave, lane) < chunks;
     // rows past the item's last key repeat it; their weight is 0
-    auto fetch = [&](int buf, int key) {
-        T::template load<kKeys, kWaves>(kt[buf], wave, lane, chunks, [&](int r) {
-            return reinterpret_cast<const uint4*>(kb + (int64_t)min(key + r, nk - 1) * a.k_stride);
+    auto fetch = [&](int key) {
+        uint4* kd = kt[key / kKeys & 1];
+        uint4* vd = vt[key / kKeys % 3];
+        if (near && begin + key + kKeys <= nk) {
+            T::template load_rows<kKeys, kWaves>(kd, wave, kb + (int64_t)(begin + key) * a.k_stride,
+                                                 k_pitch, k_off, on);
+            T::template load_rows<kKeys, kWaves>(vd, wave, vb + (int64_t)(begin + key) * a.v_stride,
+                                                 v_pitch, v_off, on);
+            return;
+        }
+        T::template load<kKeys, kWaves>(kd, wave, lane, chunks, [&](int r) {
+            return reinterpret_cast<const uint4*>(
+                kb + (int64_t)min(begin + key + r, nk - 1) * a.k_stride);
         });
-        T::template load<kKeys, kWaves>(vt[buf], wave, lane, chunks, [&](int r) {
-            return reinterpret_cast<const uint4*>(vb + (int64_t)min(key + r, nk - 1) * a.v_stride);
+        T::template load<kKeys, kWaves>(vd, wave, lane, chunks, [&](int r) {
+            return reinterpret_cast<const uint4*>(
+                vb + (int64_t)min(begin + key + r, nk - 1) * a.v_stride);
         });
     };
-    if (begin < end) fetch(0, begin);
-    int buf = 0;
-    for (int key = begin; key < end; key += kKeys, buf ^= 1) {
+    // Tile by tile (`key` counts from `begin`): the scores of a tile, then
+    // the second product of the tile before it in between this tile's
+    // exponentials, so that the matrix cores run under them. V therefore
+    // stays a tile longer than K (three buffers, two).
+    bf16x8_t p[4];
+    const int span = end - begin;
+    auto step = [&](auto first, int key) {
         tile_barrier();
-        if (key + kKeys < end) fetch(buf ^ 1, key + kKeys);
-        st.template attend<2>(q, kt[buf], vt[buf], key, limit, key + kKeys > all_see, c, lane);
+        if (key + kKeys < span) fetch(key + kKeys);
+        f32x16 sc[2];
+        st.scores(sc, q, kt[key / kKeys & 1], lane);
+        if (begin + key + kKeys > all_see) st.mask(sc, begin + key, limit, lane);
+        const uint4* before = vt[(key / kKeys + 2) % 3];
+        if (st.exceeds(sc, c)) {
+            if constexpr (!decltype(first)::value) {
+                // what the old maximum scaled goes in before the new one does
+                st.add(p, before, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = bf16x8_t{};
+            }
+            st.raise(sc, c);
+        }
+        if constexpr (decltype(first)::value) st.exponentials(sc, p, c);
+        else st.exponentials_and_add(sc, p, before, c, lane);
+    };
+    if (span > 0) {
+        fetch(0);
+        step(std::true_type{}, 0);
+        int key = kKeys;
+        for (; key < span; key += kKeys) step(std::false_type{}, key);
+        st.add(p, vt[(key / kKeys + 2) % 3], lane);
     }
 
     float own;
     const float other = other_half(st.l, own);
     const float l = own + other;
     const int64_t out_row = (int64_t)(q0 + (int)token) * a.heads + head;
-    if (f.splits > 1) {
+    if (which >= 0) {
         if (live)
-            store_part<HD>(f, st, blockIdx.y, out_row,
-                           (int64_t)a.q_items.start[a.batch] * a.heads, l, lane);
+            store_part<HD>(f, st,
+                           ((int64_t)(unit - f.whole) * f.parts + which) * kRows + row - row0, l,
+                           lane);
         return;
     }
     if (a.lse && live && lane < 32)
@@ -258,12 +404,11 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int chunks = a.head_dim >> 3;
-    const int item = blockIdx.x / a.kv_heads, kv_head = blockIdx.x - item * a.kv_heads;
-    const int q0 = a.q_items.start[item], nq = a.q_items.start[item + 1] - q0;
-    const int k0 = a.k_items.start[item], nk = a.k_items.start[item + 1] - k0;
-    const uint32_t rows = (uint32_t)nq * f.group.size;
-    if (rows == 0) return;
-    const uint32_t row = lane & 31;
+    int which;
+    const int unit = unit_of(f, blockIdx.x, which);
+    const Unit u(f, unit, kSingleRows);
+    const int kv_head = u.kv_head, q0 = u.q0, nq = u.nq, k0 = u.k0, nk = u.nk;
+    const uint32_t row = lane & 31, rows = u.rows;
     const bool live = row < rows;
     uint32_t token, member;
     f.group.split(live ? row : 0, token, member);
@@ -275,10 +420,11 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
                                                   (int64_t)(q0 + (int)token) * a.q_stride +
                                                   head * a.head_dim),
                    live, chunks, lane);
-    int part = (nk + f.splits - 1) / f.splits;
-    part = (part + kSingleKeys - 1) / kSingleKeys * kSingleKeys;
-    const int begin = (int)min((int64_t)blockIdx.y * part, (int64_t)nk);
-    const int end = (int)min((int64_t)begin + part, (int64_t)nk);
+    const int parts = which < 0 ? 1 : f.parts;
+    int share = (nk + parts - 1) / parts;
+    share = (share + kSingleKeys - 1) / kSingleKeys * kSingleKeys;
+    const int begin = (int)min((int64_t)max(which, 0) * share, (int64_t)nk);
+    const int end = (int)min((int64_t)begin + share, (int64_t)nk);
     const int limit = a.causal && live ? min(end, (int)token + nk - nq + 1) : end;
     const int all_see = __builtin_amdgcn_readfirstlane(limit);
     const float c = a.scale * kLog2e;
@@ -314,8 +460,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
         } else {
             wave_wait<0>();
         }
-        st.template attend<1>(q, tiles[wave][buf][0], tiles[wave][buf][1], key, limit,
-                              key + kSingleKeys > all_see, c, lane);
+        st.attend(q, tiles[wave][buf][0], tiles[wave][buf][1], key, limit,
+                  key + kSingleKeys > all_see, c, lane);
     }
 
     // Join the waves: each scales its state to the common maximum; wave 0
@@ -360,9 +506,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
     st.m = m;
     const int64_t out_row = (int64_t)(q0 + (int)token) * a.heads + head;
     if (!live) return;
-    if (f.splits > 1) {
-        store_part<HD>(f, st, blockIdx.y, out_row, (int64_t)a.q_items.start[a.batch] * a.heads, l,
-                       lane);
+    if (which >= 0) {
+        store_part<HD>(f, st,
+                       ((int64_t)(unit - f.whole) * f.parts + which) * kSingleRows + row, l, lane);
         return;
     }
     if (a.lse && lane < 32)
@@ -383,56 +529,76 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
         }
 }
 
-// Joins the parts of a row, 32 lanes per row, 4 columns a lane.
-__global__ __launch_bounds__(256) void combine_kernel(FwdArgs f, int64_t rows) {
+// Joins the parts of a row, one wave per row: lane p weighs part p, then each
+// half adds every other part, 4 columns a lane.
+__global__ __launch_bounds__(256) void combine_kernel(FwdArgs f, int per_tile) {
     const AttnArgs& a = f.a;
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int d = (threadIdx.x & 31) * 4;
-    if (row >= rows) return;
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tail = blockIdx.x * 4 / per_tile;
+    const int r = (blockIdx.x * 4 + wave) % per_tile;
+    const Unit u(f, f.whole + tail, per_tile);
+    const uint32_t row = u.row0 + r;
+    if (row >= u.rows) return;
     const float c = a.scale * kLog2e;
-    float m = -INFINITY;
-    for (int s = 0; s < f.splits; ++s) m = fmaxf(m, f.part_ml[s * rows + row].x);
-    float l = 0.f;
+    const int64_t first = (int64_t)tail * f.parts * per_tile + r;
+    const float2 ml = lane < f.parts ? f.part_ml[first + (int64_t)lane * per_tile]
+                                     : make_float2(-INFINITY, 0.f);
+    const float m = lane_max(ml.x);
+    const float weight = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((ml.x - m) * c);
+    const float l = lane_sum<64>(ml.y * weight);
+    const int d = (lane & 31) * 4;
+    const float* from = f.part_o + first * a.head_dim + (d < a.head_dim ? d : 0);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m != -INFINITY) {
-        for (int s = 0; s < f.splits; ++s) {
-            const float2 v = f.part_ml[s * rows + row];
-            const float by = __builtin_amdgcn_exp2f((v.x - m) * c);
-            l += v.y * by;
-            if (d < a.head_dim) {
-                const float4 p = *reinterpret_cast<const float4*>(
-                    f.part_o + (s * rows + row) * a.head_dim + d);
-                o.x += p.x * by;
-                o.y += p.y * by;
-                o.z += p.z * by;
-                o.w += p.w * by;
-            }
+    for (int p = 0; p < f.parts; p += 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {            // (four loads in flight)
+            const int mine = p + 2 * i + h, there = min(mine, f.parts - 1);
+            const float other = __shfl(weight, there);
+            const float w = mine < f.parts ? other : 0.f;
+            const float4 v = *reinterpret_cast<const float4*>(
+                from + (int64_t)there * per_tile * a.head_dim);
+            o.x += v.x * w;
+            o.y += v.y * w;
+            o.z += v.z * w;
+            o.w += v.w * w;
         }
     }
+    float own;
+    o.x = other_half(o.x, own) + own;
+    o.y = other_half(o.y, own) + own;
+    o.z = other_half(o.z, own) + own;
+    o.w = other_half(o.w, own) + own;
     const float inv = l == 0.f ? 0.f : 1.0f / l;
-    const int64_t token = row / a.heads;
-    const int head = (int)(row - token * a.heads);
-    if (d < a.head_dim)
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + token * a.out_stride +
+    uint32_t token, member;
+    f.group.split(row, token, member);
+    const int head = u.kv_head * f.group.size + member;
+    const int64_t at = u.q0 + (int)token;
+    if (h == 0 && d < a.head_dim)
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at * a.out_stride +
                                   head * a.head_dim + d) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (a.lse && d == 0)
-        a.lse[row] = l == 0.f ? -INFINITY : m * a.scale + kLn2 * __builtin_amdgcn_logf(l);
+    if (a.lse && lane == 0)
+        a.lse[at * a.heads + head] =
+            l == 0.f ? -INFINITY : m * a.scale + kLn2 * __builtin_amdgcn_logf(l);
 }
 
 template <int HD>
-hipError_t forward_as(const FwdArgs& f, const AttnPlan& p, int tiles, hipStream_t s) {
+hipError_t forward_as(const FwdArgs& f, const AttnPlan& p, int blocks, hipStream_t s) {
     if (p.single)
-        attention_single_kernel<HD><<<dim3((unsigned)(f.a.batch * f.a.kv_heads), (unsigned)f.splits),
-                                      dim3(64 * kWaves), 0, s>>>(f);
+        attention_single_kernel<HD><<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(f);
     else
-        attention_kernel<HD><<<dim3((unsigned)tiles * f.a.kv_heads, (unsigned)f.splits),
-                               dim3(64 * kWaves), 0, s>>>(f);
+        attention_kernel<HD><<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(f);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// The units of a launch fill the chip in rounds of `slots` workgroups. The
+// units past the last full round are cut along the keys into as many parts as
+// fit one round (at least 256 keys each), so that a last round of a few long
+// units does not run on a few CUs alone. Causal launches of more than a round
+// end on their shortest tiles and are left whole.
 AttnPlan attention_plan(const AttnArgs& a) {
     AttnPlan p{};
     const int group = a.heads / a.kv_heads;
@@ -442,43 +608,46 @@ AttnPlan attention_plan(const AttnArgs& a) {
             most_rows, (int64_t)(a.q_items.start[b + 1] - a.q_items.start[b]) * group);
         most_keys = std::max<int64_t>(most_keys, a.k_items.start[b + 1] - a.k_items.start[b]);
     }
-    p.single = most_rows <= 32;
+    p.single = most_rows <= kSingleRows;
+    p.per_tile = p.single ? kSingleRows : kRows;
     ItemTable tiles;
-    cut_items(a.q_items, a.batch, group, kRows, &tiles);
-    // Workgroups before a split. Fewer than the CUs: parts of at least 256
-    // keys, about two workgroups per CU (one of the single-token kernel,
-    // whose tiles fill a CU's LDS).
-    const int64_t blocks = (int64_t)(p.single ? a.batch : tiles.start[a.batch]) * a.kv_heads;
-    p.splits = 1;
-    if (blocks > 0 && blocks < kComputeUnits) {
-        const int64_t wanted = ((p.single ? 1 : 2) * kComputeUnits + blocks - 1) / blocks;
-        p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>(wanted, most_keys / 256));
+    cut_items(a.q_items, a.batch, group, p.per_tile, &tiles);
+    p.units = tiles.start[a.batch] * a.kv_heads;
+    // workgroups a CU holds: by LDS (single), by LDS and registers
+    const int slots = kComputeUnits * (p.single ? 1 : a.head_dim <= 64 ? 3 : 2);
+    p.whole = a.causal && p.units >= slots ? p.units : p.units / slots * slots;
+    p.parts = 1;
+    if (p.whole < p.units)
+        p.parts = (int32_t)std::min<int64_t>(
+            {slots / (p.units - p.whole), most_keys / 256, kMostParts});
+    if (p.parts <= 1) {
+        p.whole = p.units;
+        p.parts = 1;
     }
-    const int64_t rows = (int64_t)a.q_items.start[a.batch] * a.heads;
-    p.forward_bytes = 256;
-    if (p.splits > 1)
-        p.forward_bytes += (size_t)p.splits * rows * (a.head_dim * sizeof(float) + sizeof(float2));
+    p.forward_bytes = 256 + (size_t)(p.units - p.whole) * p.parts * p.per_tile *
+                                (a.head_dim * sizeof(float) + sizeof(float2));
     plan_attention_backward(a, &p);
     return p;
 }
 
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* ws, hipStream_t s) {
-    const int64_t rows = (int64_t)a.q_items.start[a.batch] * a.heads;
-    if (rows == 0) return hipSuccess;
+    if (p.units == 0) return hipSuccess;
     FwdArgs f;
     f.a = a;
     f.group = group_of(a);
-    cut_items(a.q_items, a.batch, f.group.size, kRows, &f.tiles);
-    f.splits = p.splits;
+    cut_items(a.q_items, a.batch, f.group.size, p.per_tile, &f.tiles);
+    f.whole = p.whole;
+    f.parts = p.parts;
+    const int tail = p.units - p.whole;
     f.part_o = static_cast<float*>(ws);
-    f.part_ml = reinterpret_cast<float2*>(static_cast<float*>(ws) +
-                                          (int64_t)p.splits * rows * a.head_dim);
-    const int tiles = f.tiles.start[a.batch];
-    hipError_t e = a.head_dim <= 64   ? forward_as<64>(f, p, tiles, s)
-                   : a.head_dim <= 96 ? forward_as<96>(f, p, tiles, s)
-                                      : forward_as<128>(f, p, tiles, s);
-    if (e != hipSuccess || p.splits == 1) return e;
-    combine_kernel<<<dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s>>>(f, rows);
+    f.part_ml = reinterpret_cast<float2*>(f.part_o +
+                                          (int64_t)tail * p.parts * p.per_tile * a.head_dim);
+    const int blocks = p.whole + tail * p.parts;
+    const hipError_t e = a.head_dim <= 64   ? forward_as<64>(f, p, blocks, s)
+                         : a.head_dim <= 96 ? forward_as<96>(f, p, blocks, s)
+                                            : forward_as<128>(f, p, blocks, s);
+    if (e != hipSuccess || tail == 0) return e;
+    combine_kernel<<<dim3((unsigned)(tail * (p.per_tile / 4))), dim3(256), 0, s>>>(f, p.per_tile);
     return hipGetLastError();
 }
 

@@ -169,13 +169,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
         tile_barrier();
         if (key + kWalk < end) fetch(buf ^ 1, key + kWalk);
         const bool masked = key + kWalk > all_see;
+        const uint32_t k_at = T::row_base(kt[buf], lane), v_at = T::row_base(vt[buf], lane);
+        const uint32_t k_tr = T::tr_base(kt[buf], lane);
 #pragma unroll
         for (int b = 0; b < kWalk / 32; ++b) {
             f32x16 s = zero16(), dp = zero16();
 #pragma unroll
             for (int k = 0; k < T::kSteps; ++k) {
-                s = mfma(T::row_frag(kt[buf], 32 * b, lane, k), q[k], s);
-                dp = mfma(T::row_frag(vt[buf], 32 * b, lane, k), dout[k], dp);
+                s = mfma(T::row_frag(k_at, 32 * b, k), q[k], s);
+                dp = mfma(T::row_frag(v_at, 32 * b, k), dout[k], dp);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
                 const bf16x8_t ds = acc_frag(s, t);
 #pragma unroll
                 for (int d = 0; d < T::kBlocks; ++d)
-                    dq[d] = mfma(T::tr_frag(kt[buf], 32 * b + 16 * t, lane, d), ds, dq[d]);
+                    dq[d] = mfma(T::tr_frag(k_tr, 32 * b + 16 * t, d), ds, dq[d]);
             }
         }
     }
@@ -312,13 +314,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
         const bool masked = row < all_from || row + kWalk > end;
 #pragma unroll
         for (int b = 0; b < kWalk / 32; ++b) {
-            int l = lane;
-            asm volatile("" : "+v"(l));
+            const uint32_t q_at = T::row_base(qt[buf], lane), o_at = T::row_base(ot[buf], lane);
             f32x16 s = zero16(), dp = zero16();
 #pragma unroll
             for (int k = 0; k < T::kSteps; ++k) {
-                s = mfma(T::row_frag(qt[buf], 32 * b, l, k), kf[k], s);
-                dp = mfma(T::row_frag(ot[buf], 32 * b, l, k), vf[k], dp);
+                s = mfma(T::row_frag(q_at, 32 * b, k), kf[k], s);
+                dp = mfma(T::row_frag(o_at, 32 * b, k), vf[k], dp);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -342,14 +343,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            asm volatile("" : "+v"(l));
+            const uint32_t q_tr = T::tr_base(qt[buf], lane), o_tr = T::tr_base(ot[buf], lane);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const bf16x8_t p = acc_frag(s, t), ds = acc_frag(dp, t);
 #pragma unroll
                 for (int d = 0; d < T::kBlocks; ++d) {
-                    dv[d] = mfma(T::tr_frag(ot[buf], 32 * b + 16 * t, l, d), p, dv[d]);
-                    dk[d] = mfma(T::tr_frag(qt[buf], 32 * b + 16 * t, l, d), ds, dk[d]);
+                    dv[d] = mfma(T::tr_frag(o_tr, 32 * b + 16 * t, d), p, dv[d]);
+                    dk[d] = mfma(T::tr_frag(q_tr, 32 * b + 16 * t, d), ds, dk[d]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);

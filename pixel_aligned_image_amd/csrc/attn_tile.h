@@ -71,6 +71,14 @@ __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
                  : "memory");
 }
 
+// The same from a uniform base and a 32-bit offset per lane.
+__device__ __forceinline__ void dma16_from(const void* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
@@ -110,18 +118,64 @@ struct Tile {
         }
     }
 
+    // The same for rows a fixed `pitch` of bytes apart, from `first` on, none of
+    // them past the end: a scalar base per instruction and one 32-bit offset
+    // per lane, which `lane_offset` makes once (pitch at most kMaxPitch).
+    static constexpr int64_t kMaxPitch = int64_t(1) << 28;
+    static __device__ __forceinline__ int lane_chunk(int wave, int lane) {
+        // (a row's swizzle is the same for all of the lane's rows)
+        return (lane % kChunks) ^ swizzle(wave * (64 / kChunks) + lane / kChunks);
+    }
+    static __device__ __forceinline__ uint32_t lane_offset(int wave, int lane, int64_t pitch) {
+        return (uint32_t)(lane / kChunks * pitch) + lane_chunk(wave, lane) * 16;
+    }
+    template <int Rows, int Waves>
+    static __device__ __forceinline__ void load_rows(uint4* tile, int wave, const void* first,
+                                                     int64_t pitch, uint32_t lane_off, bool on) {
+        constexpr int kPer = 64 / kChunks;
+        static_assert(Rows % (kPer * Waves) == 0 && (Waves * kPer) % 16 == 0, "rows per wave");
+        const uint32_t at = lds_offset(tile);
+#pragma unroll
+        for (int i = 0; i < Rows / (kPer * Waves); ++i) {
+            const int row0 = (i * Waves + wave) * kPer;
+            if (on)
+                dma16_from(static_cast<const char*>(first) + row0 * pitch, lane_off,
+                           at + row0 * kChunks * 16);
+        }
+    }
+
     // Zeros in the chunks of a tile's rows that load() leaves as they are.
     static __device__ __forceinline__ void clear(uint4* tile, int rows, int threads, int tid) {
         for (int i = tid; i < rows * kChunks; i += threads) tile[i] = make_uint4(0, 0, 0, 0);
     }
 
+    // LDS byte addresses that a lane's fragments of a tile start from: one
+    // register each per tile. The chunk of a contraction step or of a block of
+    // columns is an exclusive or on it and rows are immediate offsets. The
+    // value is opaque to the compiler, which would otherwise keep an address
+    // per fragment (32 registers and as many additions per tile).
+    static __device__ __forceinline__ uint32_t row_base(const uint4* tile, int lane) {
+        const int r = lane & 31;
+        uint32_t at = lds_offset(tile) + (r * kChunks + ((lane >> 5) ^ swizzle(r))) * 16;
+        asm volatile("" : "+v"(at));
+        return at;
+    }
+    static __device__ __forceinline__ uint32_t tr_base(const uint4* tile, int lane) {
+        const int i2 = (lane >> 2) & 3, h = lane >> 5;
+        const int f = kChunks == 16 ? i2 << 2 : (i2 & 2) << 1;
+        const int chunk = ((((lane >> 4) & 1) << 1) | ((lane >> 1) & 1)) ^ f ^ h;
+        uint32_t at = lds_offset(tile) + ((4 * h + i2) * kChunks + chunk) * 16 + (lane & 1) * 8;
+        asm volatile("" : "+v"(at));
+        return at;
+    }
+
+    typedef const __attribute__((address_space(3))) char lds_char;
+
     // Rows row0 .. row0 + 31 (a multiple of 32) as operand A, contraction
     // step s of the head.
-    static __device__ __forceinline__ bf16x8_t row_frag(const uint4* tile, int row0, int lane,
-                                                        int s) {
-        const int r = lane & 31;
-        const int b = (lane >> 5) ^ swizzle(r);
-        return __builtin_bit_cast(bf16x8_t, tile[(row0 + r) * kChunks + (b ^ (2 * s))]);
+    static __device__ __forceinline__ bf16x8_t row_frag(uint32_t base, int row0, int s) {
+        lds_char* p = (lds_char*)(uintptr_t)(base ^ (32 * s));
+        return *(const __attribute__((address_space(3))) bf16x8_t*)(p + row0 * kChunks * 16);
     }
 
     // Columns 32 db .. 32 db + 31 of the head as the rows of operand A, the
@@ -129,19 +183,13 @@ struct Tile {
     // transposing reads of 4 rows each. In a transposing read the 16 lanes of
     // a group address 4 rows x 16 columns, 4 columns a lane, and each gets
     // one column's 4 values.
-    static __device__ __forceinline__ bf16x8_t tr_frag(const uint4* tile, int row0, int lane,
-                                                       int db) {
-        const int i2 = (lane >> 2) & 3, h = lane >> 5;
-        const int f = kChunks == 16 ? i2 << 2 : (i2 & 2) << 1;
-        const int b = ((((lane >> 4) & 1) << 1) | ((lane >> 1) & 1)) ^ f ^ h;
-        const char* base = reinterpret_cast<const char*>(tile) +
-                           ((row0 + 4 * h + i2) * kChunks) * 16 + (lane & 1) * 8;
+    static __device__ __forceinline__ bf16x8_t tr_frag(uint32_t base, int row0, int db) {
         s16x8 v;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const char* p = base + 8 * e * kChunks * 16 + ((b ^ (4 * db) ^ (2 * e)) * 16);
+            lds_char* p = (lds_char*)(uintptr_t)(base ^ (64 * db) ^ (32 * e));
             const s16x4 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)p);
+                (__attribute__((address_space(3))) s16x4*)(p + (row0 + 8 * e) * kChunks * 16));
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[4 * e + j] = q[j];
         }

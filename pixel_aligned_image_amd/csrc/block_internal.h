@@ -61,6 +61,17 @@ __device__ __forceinline__ float lane_sum(float v) {
     return v;
 }
 
+__device__ __forceinline__ float lane_max(float v) {
+    float a;
+    v = fmaxf(v, dpp<0xB1>(v));
+    v = fmaxf(v, dpp<0x4E>(v));
+    v = fmaxf(v, dpp<0x141>(v));
+    v = fmaxf(v, dpp<0x140>(v));
+    { const float b = other_row16(v, a); v = fmaxf(a, b); }
+    { const float b = other_half(v, a); v = fmaxf(a, b); }
+    return v;
+}
+
 // ---------------------------------------------------------------------------
 // 16-byte vectors of elements as floats: 8 bf16 or 4 binary32.
 // ---------------------------------------------------------------------------
@@ -142,8 +153,10 @@ struct AttnArgs {
 
 // How a forward or backward launch is cut (host-only; sizes the workspace).
 struct AttnPlan {
-    int32_t splits;             // parts of the keys that a forward row tile is cut into
     bool single;                // every item's rows fit one wave: the waves split the keys
+    int32_t per_tile;           // query rows of a tile
+    int32_t units;              // row tiles x key heads
+    int32_t whole, parts;       // units run whole; parts of the keys of every later one
     int32_t dq_splits, dk_splits; // backward: parts of the keys for dq, of the rows for dk, dv
     size_t forward_bytes, backward_bytes;
 };
