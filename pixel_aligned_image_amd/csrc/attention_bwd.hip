@@ -36,12 +36,13 @@ struct BwdArgs {
     ItemTable tiles;                     // first tile of every item, of rows or keys
     Group group;
     int splits;
-    float *lse2, *delta;                 // [kv_heads][nq * group]
+    float *minus_lse, *minus_d;          // [heads][nq]
     float *part, *part2;                 // [splits][n * heads][head_dim]: dq, or dk and dv
 };
 
-// D and lse2 of every row; 32 lanes per (token, head), 4 columns a lane. lse2
-// of a row that sees no key is +inf, so its P is exp2(-inf) = 0.
+// What the score and dP products of every row start from: -lse / scale, so that
+// P = exp2(scale log2(e) (S - lse / scale)), and -D. 32 lanes per (token, head),
+// 4 columns a lane. A row that sees no key starts from -inf: its P is 0.
 __global__ __launch_bounds__(256) void rows_kernel(BwdArgs f, int64_t rows) {
     const AttnArgs& a = f.a;
     const int d = (threadIdx.x & 31) * 4;
@@ -62,12 +63,10 @@ __global__ __launch_bounds__(256) void rows_kernel(BwdArgs f, int64_t rows) {
         }
         s = lane_sum<32>(s);
         if (d) continue;
-        const int kv_head = head / (int)f.group.size;
-        const int64_t at = (rows / a.heads * kv_head + token) * f.group.size + head -
-                           kv_head * (int)f.group.size;
+        const int64_t at = rows / a.heads * head + token;
         const float l = a.lse_in[row];
-        f.delta[at] = s;
-        f.lse2[at] = l == -INFINITY ? INFINITY : l * kLog2e;
+        f.minus_d[at] = -s;
+        f.minus_lse[at] = l == -INFINITY ? -INFINITY : -l / a.scale;
     }
 }
 
@@ -85,6 +84,39 @@ __device__ __forceinline__ void store_sums(const f32x16 (&o)[Tile<HD>::kBlocks],
                 *reinterpret_cast<float4*>(out + d) = make_float4(
                     o[b][4 * j], o[b][4 * j + 1], o[b][4 * j + 2], o[b][4 * j + 3]);
         }
+}
+
+// Issue orders. The two products of `Steps` steps: `Ahead` + 4 LDS reads, then
+// a matrix instruction and a read in turn.
+template <int Steps, int Ahead>
+__device__ __forceinline__ void products_in_turn() {
+    __builtin_amdgcn_sched_group_barrier(0x100, Ahead + 4, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * Steps; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Two sets of `N` matrix instructions on transposed fragments, each set behind
+// its half of `2 Vector` vector instructions: the second half goes under the
+// first set.
+template <int N, int Vector>
+__device__ __forceinline__ void sums_in_turn() {
+    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, Vector, 0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, (Vector + N - 1) / N, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
 }
 
 template <int HD>
@@ -122,9 +154,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
                                                   (int64_t)(q0 + (int)token) * a.dout_stride +
                                                   head * a.head_dim),
                    live, chunks, lane);
-    const int64_t stat = ((int64_t)a.q_items.start[a.batch] * kv_head + q0) * f.group.size + row;
-    const float lse2 = live ? f.lse2[stat] : INFINITY;
-    const float delta = live ? f.delta[stat] : 0.f;
+    const int64_t stat = (int64_t)a.q_items.start[a.batch] * head + q0 + (int)token;
+    const float c = a.scale * kLog2e;
+    const float minus_lse2 = live ? f.minus_lse[stat] * c : -INFINITY;
+    const float minus_d = live ? f.minus_d[stat] : 0.f;
 
     int part = (nk + f.splits - 1) / f.splits;
     part = (part + kWalk - 1) / kWalk * kWalk;
@@ -138,7 +171,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
         end = min(end, (int)last + nk - nq + 1);
     }
     const int all_see = __builtin_amdgcn_readfirstlane(limit);
-    const float c = a.scale * kLog2e;
 
     f32x16 dq[T::kBlocks];
 #pragma unroll
@@ -164,37 +196,45 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
         });
     };
     if (begin < end) fetch(0, begin);
-    int buf = 0;
-    for (int key = begin; key < end; key += kWalk, buf ^= 1) {
-        tile_barrier();
-        if (key + kWalk < end) fetch(buf ^ 1, key + kWalk);
-        const bool masked = key + kWalk > all_see;
-        const uint32_t k_at = T::row_base(kt[buf], lane), v_at = T::row_base(vt[buf], lane);
-        const uint32_t k_tr = T::tr_base(kt[buf], lane);
+    auto walk = [&](bool masked, int buf, int key) {
 #pragma unroll
         for (int b = 0; b < kWalk / 32; ++b) {
+            const uint32_t k_at = T::row_base(kt[buf], lane), v_at = T::row_base(vt[buf], lane);
             f32x16 s = zero16(), dp = zero16();
 #pragma unroll
             for (int k = 0; k < T::kSteps; ++k) {
                 s = mfma(T::row_frag(k_at, 32 * b, k), q[k], s);
                 dp = mfma(T::row_frag(v_at, 32 * b, k), dout[k], dp);
             }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[i] = __builtin_amdgcn_exp2f(s[i] * c - lse2) * (dp[i] - delta);
+            products_in_turn<T::kSteps, 0>();
             if (masked) {
+                const int left = limit - key - 4 * h;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (key + 32 * b + acc_row(i, h) >= limit) s[i] = 0.f;
+                    if (32 * b + acc_row(i, 0) >= left) s[i] = -INFINITY;
             }
+            // dS^T, the half of the keys that the first matrix instructions
+            // need and then, under them, the other
+            const uint32_t k_tr = T::tr_base(kt[buf], lane);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int i = 8 * t; i < 8 * t + 8; ++i)
+                    s[i] = __builtin_amdgcn_exp2f(s[i] * c + minus_lse2) * (dp[i] + minus_d);
                 const bf16x8_t ds = acc_frag(s, t);
 #pragma unroll
                 for (int d = 0; d < T::kBlocks; ++d)
                     dq[d] = mfma(T::tr_frag(k_tr, 32 * b + 16 * t, d), ds, dq[d]);
             }
+            sums_in_turn<T::kBlocks, 36>();
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    int buf = 0;
+    for (int key = begin; key < end; key += kWalk, buf ^= 1) {
+        tile_barrier();
+        if (key + kWalk < end) fetch(buf ^ 1, key + kWalk);
+        walk(key + kWalk > all_see, buf, key);
     }
 
     const int64_t out_row = (int64_t)(q0 + (int)token) * a.heads + head;
@@ -206,8 +246,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
         return;
     }
     tile_barrier();
-    // a row that sees nothing has dS = 0 * (...): its dq is 0 by definition
-    const float by = lse2 == INFINITY ? 0.f : a.scale;
+    const float by = a.scale;
     uint4* stage = wave < 2 ? kt[wave] : vt[wave - 2];
     store_rows<HD>(dq, by, stage, chunks, lane, [&](int r) -> uint4* {
         const uint32_t at = row0 + 32 * wave + r;
@@ -220,12 +259,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
     });
 }
 
+// Walks the rows of one key head's query heads, head by head, in tiles of 64
+// tokens: every tile is a run of tokens of one head, loaded as it lies.
 template <int HD>
 __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     using T = Tile<HD>;
-    __shared__ uint4 qt[2][kWalk * T::kChunks];
-    __shared__ uint4 ot[2][kWalk * T::kChunks];
-    __shared__ alignas(16) float stats[2][2][kWalk];     // [buffer][lse2, delta]
+    __shared__ uint4 tiles[2][2 * kWalk * T::kChunks];   // [buffer][q rows, dout rows]
+    __shared__ alignas(16) float stats[2][2][kWalk];     // [buffer][-lse / scale, -D]
     const AttnArgs& a = f.a;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -237,7 +277,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     const int q0 = a.q_items.start[item], nq = a.q_items.start[item + 1] - q0;
     const int k0 = a.k_items.start[item], nk = a.k_items.start[item + 1] - k0;
     const int group = f.group.size;
-    const int rows = nq * group;
 
     const int key = key0 + 32 * wave + (lane & 31);
     const bool live = key < nk;
@@ -253,125 +292,142 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
                                                   kv_head * a.head_dim),
                    live, chunks, lane);
 
-    // rows of this part; the first that see this workgroup's and this lane's
-    // keys (a causal row's token sees key j from token j - (nk - nq) on)
-    int part = (int)(((int64_t)rows + f.splits - 1) / f.splits);
-    part = (part + kWalk - 1) / kWalk * kWalk;
-    int begin = (int)min((int64_t)blockIdx.y * part, (int64_t)rows);
-    const int end = (int)min((int64_t)begin + part, (int64_t)rows);
-    int from = 0, all_from = 0;
+    // Tokens from `from` on see this lane's key, from `all_from` on all of the
+    // wave's, and none before the first tile sees any of the workgroup's.
+    int first = 0, from = 0, all_from = 0;
     if (a.causal) {
-        const int64_t r = (int64_t)(key - (nk - nq)) * group;
-        from = (int)min(max(r, (int64_t)0), (int64_t)rows);
-        all_from = (int)min(
-            max((int64_t)(key0 + 32 * wave + 31 - (nk - nq)) * group, (int64_t)0), (int64_t)rows);
-        const int64_t first = (int64_t)(key0 - (nk - nq)) * group;
-        if (first > begin) begin += (int)((min(first, (int64_t)end) - begin) / kWalk * kWalk);
+        from = min(max(key - (nk - nq), 0), nq);
+        all_from = min(max(key0 + 32 * wave + 31 - (nk - nq), 0), nq);
+        first = min(max(key0 - (nk - nq), 0), nq) / kWalk;
     }
+    // this part's tiles, counted over (head, token tile)
+    const int per_head = (nq + kWalk - 1) / kWalk - first;
+    const int64_t all = (int64_t)per_head * group;
+    const int begin = (int)(all * blockIdx.y / f.splits);
+    const int end = (int)(all * (blockIdx.y + 1) / f.splits);
     const float c = a.scale * kLog2e;
 
     f32x16 dk[T::kBlocks], dv[T::kBlocks];
 #pragma unroll
     for (int b = 0; b < T::kBlocks; ++b) dk[b] = dv[b] = zero16();
     if (chunks < T::kChunks) {
-        for (int i = 0; i < 2; ++i) {
-            T::clear(qt[i], kWalk, 64 * kWaves, threadIdx.x);
-            T::clear(ot[i], kWalk, 64 * kWaves, threadIdx.x);
-        }
+        for (int i = 0; i < 2; ++i) T::clear(tiles[i], 2 * kWalk, 64 * kWaves, threadIdx.x);
         __syncthreads();
     }
     const uint16_t* qb = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)q0 * a.q_stride +
                          kv_head * group * a.head_dim;
     const uint16_t* ob = reinterpret_cast<const uint16_t*>(a.dout) + (int64_t)q0 * a.dout_stride +
                          kv_head * group * a.head_dim;
-    const int64_t stat = ((int64_t)a.q_items.start[a.batch] * kv_head + q0) * group;
-    // rows past the last repeat it; their P and dS are 0
+    const int64_t stat = (int64_t)kv_head * group * a.q_items.start[a.batch] + q0;
+    const int64_t q_pitch = a.q_stride * 2, o_pitch = a.dout_stride * 2;
+    const bool near = max(q_pitch, o_pitch) <= T::kMaxPitch;
+    const uint32_t q_off = T::lane_offset(wave, lane, q_pitch);
+    const uint32_t o_off = T::lane_offset(wave, lane, o_pitch);
+    const bool on = T::lane_chunk(wave, lane) < chunks;
+
+    // The next tile to load, and its row sums on their way to LDS. Tokens past
+    // the item's last repeat it and start from -inf, so their P is 0.
+    int member = per_head > 0 ? begin / per_head : 0;
+    int token = (first + begin - member * per_head) * kWalk;
     float stat_next = 0.f;
-    auto fetch = [&](int buf, int row) {
+    auto fetch = [&](int buf) {
+        const uint16_t* qm = qb + member * a.head_dim;
+        const uint16_t* om = ob + member * a.head_dim;
+        uint4* qt = tiles[buf];
+        uint4* ot = tiles[buf] + kWalk * T::kChunks;
         if (threadIdx.x < 2 * kWalk) {
-            const int64_t at = stat + min(row + (int)(threadIdx.x % kWalk), rows - 1);
-            stat_next = threadIdx.x < kWalk ? f.lse2[at] : f.delta[at];
+            const int t = token + (int)(threadIdx.x % kWalk);
+            const int64_t at = stat + (int64_t)member * a.q_items.start[a.batch] + min(t, nq - 1);
+            stat_next = threadIdx.x >= kWalk ? f.minus_d[at] : t < nq ? f.minus_lse[at] : -INFINITY;
         }
-        T::template load<kWalk, kWaves>(qt[buf], wave, lane, chunks, [&](int r) {
-            uint32_t t, m;
-            f.group.split(min(row + r, rows - 1), t, m);
-            return reinterpret_cast<const uint4*>(qb + (int64_t)t * a.q_stride + m * a.head_dim);
-        });
-        T::template load<kWalk, kWaves>(ot[buf], wave, lane, chunks, [&](int r) {
-            uint32_t t, m;
-            f.group.split(min(row + r, rows - 1), t, m);
-            return reinterpret_cast<const uint4*>(ob + (int64_t)t * a.dout_stride +
-                                                  m * a.head_dim);
-        });
+        if (near && token + kWalk <= nq) {
+            T::template load_rows<kWalk, kWaves>(qt, wave, qm + (int64_t)token * a.q_stride,
+                                                 q_pitch, q_off, on);
+            T::template load_rows<kWalk, kWaves>(ot, wave, om + (int64_t)token * a.dout_stride,
+                                                 o_pitch, o_off, on);
+        } else {
+            T::template load<kWalk, kWaves>(qt, wave, lane, chunks, [&](int r) {
+                return reinterpret_cast<const uint4*>(qm +
+                                                      (int64_t)min(token + r, nq - 1) * a.q_stride);
+            });
+            T::template load<kWalk, kWaves>(ot, wave, lane, chunks, [&](int r) {
+                return reinterpret_cast<const uint4*>(
+                    om + (int64_t)min(token + r, nq - 1) * a.dout_stride);
+            });
+        }
     };
-    if (begin < end) fetch(0, begin);
-    auto walk = [&](auto which, int row) {
-        constexpr int buf = decltype(which)::value;
-        if (threadIdx.x < 2 * kWalk) stats[buf][threadIdx.x / kWalk][threadIdx.x % kWalk] = stat_next;
-        tile_barrier();
-        if (row + kWalk < end) fetch(buf ^ 1, row + kWalk);
-        __builtin_amdgcn_sched_barrier(0);
-        const bool masked = row < all_from || row + kWalk > end;
+    if (begin < end) fetch(0);
+    auto walk = [&](bool masked, int buf, int row) {
 #pragma unroll
         for (int b = 0; b < kWalk / 32; ++b) {
-            const uint32_t q_at = T::row_base(qt[buf], lane), o_at = T::row_base(ot[buf], lane);
-            f32x16 s = zero16(), dp = zero16();
-#pragma unroll
-            for (int k = 0; k < T::kSteps; ++k) {
-                s = mfma(T::row_frag(q_at, 32 * b, k), kf[k], s);
-                dp = mfma(T::row_frag(o_at, 32 * b, k), vf[k], dp);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            const uint32_t at = T::row_base(tiles[buf], lane);
+            f32x16 s, dp;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float4 l4 =
+                const float4 l =
                     *reinterpret_cast<const float4*>(&stats[buf][0][32 * b + 8 * j + 4 * h]);
-                const float4 d4 =
+                const float4 d =
                     *reinterpret_cast<const float4*>(&stats[buf][1][32 * b + 8 * j + 4 * h]);
-                const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[4 * j + i] = __builtin_amdgcn_exp2f(s[4 * j + i] * c - ls[i]);
-                    dp[4 * j + i] = s[4 * j + i] * (dp[4 * j + i] - ds[i]);
-                }
+                s[4 * j] = l.x, s[4 * j + 1] = l.y, s[4 * j + 2] = l.z, s[4 * j + 3] = l.w;
+                dp[4 * j] = d.x, dp[4 * j + 1] = d.y, dp[4 * j + 2] = d.z, dp[4 * j + 3] = d.w;
             }
+#pragma unroll
+            for (int k = 0; k < T::kSteps; ++k) {
+                s = mfma(T::row_frag(at, 32 * b, k), kf[k], s);
+                dp = mfma(T::row_frag(at, kWalk + 32 * b, k), vf[k], dp);
+            }
+            products_in_turn<T::kSteps, 8>();
             if (masked) {
+                const int before = from - row - 4 * h;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int at = row + 32 * b + acc_row(i, h);
-                    if (at < from || at >= end) s[i] = dp[i] = 0.f;
-                }
+                for (int i = 0; i < 16; ++i)
+                    if (32 * b + acc_row(i, 0) < before) s[i] = -INFINITY;
             }
-            __builtin_amdgcn_sched_barrier(0);
-            const uint32_t q_tr = T::tr_base(qt[buf], lane), o_tr = T::tr_base(ot[buf], lane);
+            const uint32_t tr = T::tr_base(tiles[buf], lane);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int i = 8 * t; i < 8 * t + 8; ++i) {
+                    s[i] = __builtin_amdgcn_exp2f(s[i] * c);
+                    dp[i] *= s[i];
+                }
                 const bf16x8_t p = acc_frag(s, t), ds = acc_frag(dp, t);
 #pragma unroll
                 for (int d = 0; d < T::kBlocks; ++d) {
-                    dv[d] = mfma(T::tr_frag(o_tr, 32 * b + 16 * t, d), p, dv[d]);
-                    dk[d] = mfma(T::tr_frag(q_tr, 32 * b + 16 * t, d), ds, dk[d]);
+                    dv[d] = mfma(T::tr_frag(tr, kWalk + 32 * b + 16 * t, d), p, dv[d]);
+                    dk[d] = mfma(T::tr_frag(tr, 32 * b + 16 * t, d), ds, dk[d]);
                 }
             }
+            sums_in_turn<2 * T::kBlocks, 32>();
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    for (int row = begin; row < end; row += 2 * kWalk) {
-        walk(std::integral_constant<int, 0>{}, row);
-        if (row + kWalk < end) walk(std::integral_constant<int, 1>{}, row + kWalk);
+    int buf = 0;
+    for (int nth = begin; nth < end; ++nth, buf ^= 1) {
+        const int row = token;                           // of the tile in `buf`
+        if (threadIdx.x < 2 * kWalk)
+            stats[buf][threadIdx.x / kWalk][threadIdx.x % kWalk] = stat_next;
+        tile_barrier();
+        token += kWalk;
+        if (token >= nq) {
+            token = first * kWalk;
+            ++member;
+        }
+        if (nth + 1 < end) fetch(buf ^ 1);
+        walk(row < all_from, buf, row);
     }
 
     if (f.splits > 1) {
         if (!live) return;
-        const int64_t all = (int64_t)a.k_items.start[a.batch] * a.kv_heads;
-        const int64_t at = (blockIdx.y * all + (int64_t)(k0 + key) * a.kv_heads + kv_head) *
+        const int64_t rows = (int64_t)a.k_items.start[a.batch] * a.kv_heads;
+        const int64_t at = (blockIdx.y * rows + (int64_t)(k0 + key) * a.kv_heads + kv_head) *
                            a.head_dim;
         store_sums<HD>(dk, f.part + at, a.head_dim, lane);
         store_sums<HD>(dv, f.part2 + at, a.head_dim, lane);
         return;
     }
     tile_barrier();
-    uint4* stage = wave < 2 ? qt[wave] : ot[wave - 2];
+    uint4* stage = tiles[0] + wave * 32 * T::kChunks;
     auto to = [&](void* base, int64_t stride) {
         return [=](int r) -> uint4* {
             const int at = key0 + 32 * wave + r;
@@ -488,9 +544,9 @@ hipError_t launch_attention_backward(const AttnArgs& a, const AttnPlan& p, void*
     f.a = a;
     f.group = group_of(a);
     char* at = static_cast<char*>(ws);
-    f.lse2 = reinterpret_cast<float*>(at);
+    f.minus_lse = reinterpret_cast<float*>(at);
     at += padded(q_rows * sizeof(float));
-    f.delta = reinterpret_cast<float*>(at);
+    f.minus_d = reinterpret_cast<float*>(at);
     at += padded(q_rows * sizeof(float));
     f.part = reinterpret_cast<float*>(at);
     if (q_rows > 0) {

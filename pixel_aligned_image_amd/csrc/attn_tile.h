@@ -72,7 +72,10 @@ __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
 }
 
 // The same from a uniform base and a 32-bit offset per lane.
-__device__ __forceinline__ void dma16_from(const void* base, uint32_t offset, uint32_t lds) {
+__device__ __forceinline__ void dma16_from(const void* from, uint32_t offset, uint32_t lds) {
+    const uint64_t at = (uint64_t)(uintptr_t)from;
+    const uint64_t base = ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32) |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
