@@ -94,6 +94,8 @@ struct Softmax {
     __device__ __forceinline__ void scores(f32x16 (&s)[2], const bf16x8_t (&q)[T::kSteps],
                                            const uint4* kt, int lane) const {
         const uint32_t at = T::row_base(kt, lane);
+        // (ahead of the CU's other waves, whose vector work then fills in)
+        __builtin_amdgcn_s_setprio(1);
         s[0] = s[1] = zero16();
 #pragma unroll
         for (int k = 0; k < T::kSteps; ++k)
@@ -106,6 +108,7 @@ struct Softmax {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
+        __builtin_amdgcn_s_setprio(0);
     }
 
     // Keys at or past `limit` are not seen.
@@ -275,6 +278,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(FwdArgs f) {
                                                   (int64_t)(q0 + (int)token) * a.q_stride +
                                                   head * a.head_dim),
                    live, chunks, lane);
+    settle(q);
 
     // keys of this part, and those this workgroup and this lane see
     const int parts = which < 0 ? 1 : f.parts;
@@ -420,6 +424,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
                                                   (int64_t)(q0 + (int)token) * a.q_stride +
                                                   head * a.head_dim),
                    live, chunks, lane);
+    settle(q);
     const int parts = which < 0 ? 1 : f.parts;
     int share = (nk + parts - 1) / parts;
     share = (share + kSingleKeys - 1) / kSingleKeys * kSingleKeys;

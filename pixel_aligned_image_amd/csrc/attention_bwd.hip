@@ -36,7 +36,7 @@ struct BwdArgs {
     ItemTable tiles;                     // first tile of every item, of rows or keys
     Group group;
     int splits;
-    float *minus_lse, *minus_d;          // [heads][nq]
+    float *minus_lse, *minus_d;          // [heads][nq], then -inf and 0
     float *part, *part2;                 // [splits][n * heads][head_dim]: dq, or dk and dv
 };
 
@@ -45,6 +45,10 @@ struct BwdArgs {
 // 4 columns a lane. A row that sees no key starts from -inf: its P is 0.
 __global__ __launch_bounds__(256) void rows_kernel(BwdArgs f, int64_t rows) {
     const AttnArgs& a = f.a;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        f.minus_lse[rows] = -INFINITY;
+        f.minus_d[rows] = 0.f;
+    }
     const int d = (threadIdx.x & 31) * 4;
     for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows;
          row += (int64_t)gridDim.x * 8) {
@@ -156,8 +160,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
                    live, chunks, lane);
     const int64_t stat = (int64_t)a.q_items.start[a.batch] * head + q0 + (int)token;
     const float c = a.scale * kLog2e;
-    const float minus_lse2 = live ? f.minus_lse[stat] * c : -INFINITY;
-    const float minus_d = live ? f.minus_d[stat] : 0.f;
+    float minus_lse2 = live ? f.minus_lse[stat] * c : -INFINITY;
+    float minus_d = live ? f.minus_d[stat] : 0.f;
+    settle(q);
+    settle(dout);
+    asm volatile("" : "+v"(minus_lse2), "+v"(minus_d));
 
     int part = (nk + f.splits - 1) / f.splits;
     part = (part + kWalk - 1) / kWalk * kWalk;
@@ -196,39 +203,66 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
         });
     };
     if (begin < end) fetch(0, begin);
-    auto walk = [&](bool masked, int buf, int key) {
+    auto products = [&](f32x16& s, f32x16& dp, uint32_t k_at, uint32_t v_at, int b) {
+        s = zero16();
+        dp = zero16();
 #pragma unroll
-        for (int b = 0; b < kWalk / 32; ++b) {
-            const uint32_t k_at = T::row_base(kt[buf], lane), v_at = T::row_base(vt[buf], lane);
-            f32x16 s = zero16(), dp = zero16();
-#pragma unroll
-            for (int k = 0; k < T::kSteps; ++k) {
-                s = mfma(T::row_frag(k_at, 32 * b, k), q[k], s);
-                dp = mfma(T::row_frag(v_at, 32 * b, k), dout[k], dp);
-            }
-            products_in_turn<T::kSteps, 0>();
-            if (masked) {
-                const int left = limit - key - 4 * h;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (32 * b + acc_row(i, 0) >= left) s[i] = -INFINITY;
-            }
-            // dS^T, the half of the keys that the first matrix instructions
-            // need and then, under them, the other
-            const uint32_t k_tr = T::tr_base(kt[buf], lane);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int i = 8 * t; i < 8 * t + 8; ++i)
-                    s[i] = __builtin_amdgcn_exp2f(s[i] * c + minus_lse2) * (dp[i] + minus_d);
-                const bf16x8_t ds = acc_frag(s, t);
-#pragma unroll
-                for (int d = 0; d < T::kBlocks; ++d)
-                    dq[d] = mfma(T::tr_frag(k_tr, 32 * b + 16 * t, d), ds, dq[d]);
-            }
-            sums_in_turn<T::kBlocks, 36>();
-            __builtin_amdgcn_sched_barrier(0);
+        for (int k = 0; k < T::kSteps; ++k) {
+            s = mfma(T::row_frag(k_at, 32 * b, k), q[k], s);
+            dp = mfma(T::row_frag(v_at, 32 * b, k), dout[k], dp);
         }
+    };
+    auto mask = [&](f32x16& s, int key) {
+        const int left = limit - key - 4 * h;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (acc_row(i, 0) >= left) s[i] = -INFINITY;
+    };
+    auto gradient = [&](f32x16& s, const f32x16& dp) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            s[i] = __builtin_amdgcn_exp2f(s[i] * c + minus_lse2) * (dp[i] + minus_d);
+    };
+    auto walk = [&](bool masked, int buf, int key) {
+        const uint32_t k_at = T::row_base(kt[buf], lane), v_at = T::row_base(vt[buf], lane);
+        f32x16 s0, dp0, s1, dp1;
+        __builtin_amdgcn_s_setprio(1);       // (as in the forward kernel)
+        products(s0, dp0, k_at, v_at, 0);
+        products_in_turn<T::kSteps, 4>();
+        __builtin_amdgcn_s_setprio(0);
+        if (masked) mask(s0, key);
+        // the second block's products under the first one's exponentials
+        products(s1, dp1, k_at, v_at, 1);
+        gradient(s0, dp0);
+        bf16x8_t ds[4];
+        ds[0] = acc_frag(s0, 0);
+        ds[1] = acc_frag(s0, 1);
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * T::kSteps; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 72 / (2 * T::kSteps) + 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (masked) mask(s1, key + 32);
+        const uint32_t k_tr = T::tr_base(kt[buf], lane);
+        gradient(s1, dp1);
+        ds[2] = acc_frag(s1, 0);
+        ds[3] = acc_frag(s1, 1);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int d = 0; d < T::kBlocks; ++d)
+                dq[d] = mfma(T::tr_frag(k_tr, 16 * t, d), ds[t], dq[d]);
+        __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+        for (int i = 0; i < 4 * T::kBlocks; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 72 / (2 * T::kBlocks) + 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
     };
     int buf = 0;
     for (int key = begin; key < end; key += kWalk, buf ^= 1) {
@@ -291,6 +325,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
                                                   (int64_t)(k0 + (live ? key : 0)) * a.v_stride +
                                                   kv_head * a.head_dim),
                    live, chunks, lane);
+    settle(kf);
+    settle(vf);
 
     // Tokens from `from` on see this lane's key, from `all_from` on all of the
     // wave's, and none before the first tile sees any of the workgroup's.
@@ -325,20 +361,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     const uint32_t o_off = T::lane_offset(wave, lane, o_pitch);
     const bool on = T::lane_chunk(wave, lane) < chunks;
 
-    // The next tile to load, and its row sums on their way to LDS. Tokens past
-    // the item's last repeat it and start from -inf, so their P is 0.
+    // The next tile to load. Tokens past the item's last repeat it and start
+    // from the -inf behind the last row's value, so their P is 0.
     int member = per_head > 0 ? begin / per_head : 0;
     int token = (first + begin - member * per_head) * kWalk;
-    float stat_next = 0.f;
+    const int64_t past = (int64_t)a.heads * a.q_items.start[a.batch];
     auto fetch = [&](int buf) {
         const uint16_t* qm = qb + member * a.head_dim;
         const uint16_t* om = ob + member * a.head_dim;
         uint4* qt = tiles[buf];
         uint4* ot = tiles[buf] + kWalk * T::kChunks;
-        if (threadIdx.x < 2 * kWalk) {
-            const int t = token + (int)(threadIdx.x % kWalk);
-            const int64_t at = stat + (int64_t)member * a.q_items.start[a.batch] + min(t, nq - 1);
-            stat_next = threadIdx.x >= kWalk ? f.minus_d[at] : t < nq ? f.minus_lse[at] : -INFINITY;
+        if (wave < 2) {
+            const int t = token + lane;
+            const int64_t at = t < nq ? stat + (int64_t)member * a.q_items.start[a.batch] + t
+                                      : past;
+            dma4((wave ? f.minus_d : f.minus_lse) + at, lds_offset(stats[buf][wave]));
         }
         if (near && token + kWalk <= nq) {
             T::template load_rows<kWalk, kWaves>(qt, wave, qm + (int64_t)token * a.q_stride,
@@ -405,8 +442,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     int buf = 0;
     for (int nth = begin; nth < end; ++nth, buf ^= 1) {
         const int row = token;                           // of the tile in `buf`
-        if (threadIdx.x < 2 * kWalk)
-            stats[buf][threadIdx.x / kWalk][threadIdx.x % kWalk] = stat_next;
         tile_barrier();
         token += kWalk;
         if (token >= nq) {
@@ -533,7 +568,7 @@ void plan_attention_backward(const AttnArgs& a, AttnPlan* p) {
     const size_t k_rows = (size_t)a.k_items.start[a.batch] * a.kv_heads;
     const size_t dq = p->dq_splits > 1 ? p->dq_splits * q_rows : 0;
     const size_t dk = p->dk_splits > 1 ? 2 * p->dk_splits * k_rows : 0;
-    p->backward_bytes = 256 + 2 * padded(q_rows * sizeof(float)) +
+    p->backward_bytes = 256 + 2 * padded((q_rows + 1) * sizeof(float)) +
                         std::max(dq, dk) * a.head_dim * sizeof(float);
 }
 
@@ -545,9 +580,9 @@ hipError_t launch_attention_backward(const AttnArgs& a, const AttnPlan& p, void*
     f.group = group_of(a);
     char* at = static_cast<char*>(ws);
     f.minus_lse = reinterpret_cast<float*>(at);
-    at += padded(q_rows * sizeof(float));
+    at += padded((q_rows + 1) * sizeof(float));
     f.minus_d = reinterpret_cast<float*>(at);
-    at += padded(q_rows * sizeof(float));
+    at += padded((q_rows + 1) * sizeof(float));
     f.part = reinterpret_cast<float*>(at);
     if (q_rows > 0) {
         // (a launch holds under 2^32 threads)

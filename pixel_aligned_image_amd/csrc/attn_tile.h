@@ -71,7 +71,15 @@ __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
                  : "memory");
 }
 
-// The same from a uniform base and a 32-bit offset per lane.
+// 64 lanes x 4 bytes into 256 bytes of LDS, lane l at 4 l.
+__device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
+                 : "memory");
+}
+
+// dma16 from a uniform base and a 32-bit offset per lane.
 __device__ __forceinline__ void dma16_from(const void* from, uint32_t offset, uint32_t lds) {
     const uint64_t at = (uint64_t)(uintptr_t)from;
     const uint64_t base = ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32) |
@@ -247,6 +255,15 @@ __device__ __forceinline__ void load_query(bf16x8_t (&q)[Tile<HD>::kSteps], cons
         const uint4 v = live && chunk < chunks ? row[chunk] : make_uint4(0, 0, 0, 0);
         q[k] = __builtin_bit_cast(bf16x8_t, v);
     }
+}
+
+// The values are there: the compiler's wait for their loads stands here and
+// not at their first use inside a loop, where it would also wait for the tile
+// loads in flight, which it does not know of.
+template <int N>
+__device__ __forceinline__ void settle(bf16x8_t (&q)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) asm volatile("" : "+v"(q[k]));
 }
 
 // A finished tile's rows through LDS (32 rows of the tile layout) so that
