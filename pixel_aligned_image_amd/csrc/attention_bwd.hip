@@ -293,13 +293,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
     });
 }
 
-// Walks the rows of one key head's query heads, head by head, in tiles of 64
+// Walks the rows of one key head's query heads, head by head, in tiles of 32
 // tokens: every tile is a run of tokens of one head, loaded as it lies.
+//
+// The wave's two sums take 128 registers for heads of 128 and its keys 32. Its
+// values stay in LDS: 32 registers more would leave two waves a SIMD nothing
+// to read fragments ahead into, and every matrix instruction would wait for
+// LDS (one wave a SIMD, with registers to spare, is held up by its own issue).
 template <int HD>
 __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     using T = Tile<HD>;
-    __shared__ uint4 tiles[2][2 * kWalk * T::kChunks];   // [buffer][q rows, dout rows]
-    __shared__ alignas(16) float stats[2][2][kWalk];     // [buffer][-lse / scale, -D]
+    constexpr int kRows = 32;
+    __shared__ uint4 tiles[2][2 * kRows * T::kChunks];   // [buffer][q rows, dout rows]
+    __shared__ uint4 values[kHeld * T::kChunks];
+    __shared__ alignas(16) float stats[2][2][64];        // [buffer][-lse / scale, -D]
     const AttnArgs& a = f.a;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -312,21 +319,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     const int k0 = a.k_items.start[item], nk = a.k_items.start[item + 1] - k0;
     const int group = f.group.size;
 
+    if (chunks < T::kChunks) {
+        for (int i = 0; i < 2; ++i) T::clear(tiles[i], 2 * kRows, 64 * kWaves, threadIdx.x);
+        T::clear(values, kHeld, 64 * kWaves, threadIdx.x);
+        __syncthreads();
+    }
     const int key = key0 + 32 * wave + (lane & 31);
     const bool live = key < nk;
-    bf16x8_t kf[T::kSteps], vf[T::kSteps];
+    bf16x8_t kf[T::kSteps];
     load_query<HD>(kf,
                    reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.k) +
                                                   (int64_t)(k0 + (live ? key : 0)) * a.k_stride +
                                                   kv_head * a.head_dim),
                    live, chunks, lane);
-    load_query<HD>(vf,
-                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.v) +
-                                                  (int64_t)(k0 + (live ? key : 0)) * a.v_stride +
-                                                  kv_head * a.head_dim),
-                   live, chunks, lane);
+    // (keys past the item's last repeat it; their sums are not stored)
+    T::template load<kHeld, kWaves>(values, wave, lane, chunks, [&](int r) {
+        return reinterpret_cast<const uint4*>(
+            reinterpret_cast<const uint16_t*>(a.v) +
+            (int64_t)(k0 + min(key0 + r, nk - 1)) * a.v_stride + kv_head * a.head_dim);
+    });
     settle(kf);
-    settle(vf);
 
     // Tokens from `from` on see this lane's key, from `all_from` on all of the
     // wave's, and none before the first tile sees any of the workgroup's.
@@ -334,14 +346,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     if (a.causal) {
         from = min(max(key - (nk - nq), 0), nq);
         all_from = min(max(key0 + 32 * wave + 31 - (nk - nq), 0), nq);
-        first = min(max(key0 - (nk - nq), 0), nq) / kWalk;
+        first = min(max(key0 - (nk - nq), 0), nq) / kRows;
     }
     // This part of the tiles, numbered over (head, token tile), is the same
     // for every workgroup of the key head, and is walked from its end: they
     // read the same rows at the same time, from their XCD's L2, whatever
     // their causal first tile is. (Walking up from it, 56 % of the reads of
     // 12,289 tokens missed L2.)
-    const int per_head = (nq + kWalk - 1) / kWalk;
+    const int per_head = (nq + kRows - 1) / kRows;
     const int64_t all = (int64_t)per_head * group;
     const int low = (int)(all * blockIdx.y / f.splits);
     const int high = (int)(all * (blockIdx.y + 1) / f.splits);
@@ -360,15 +372,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     f32x16 dk[T::kBlocks], dv[T::kBlocks];
 #pragma unroll
     for (int b = 0; b < T::kBlocks; ++b) dk[b] = dv[b] = zero16();
-    if (chunks < T::kChunks) {
-        for (int i = 0; i < 2; ++i) T::clear(tiles[i], 2 * kWalk, 64 * kWaves, threadIdx.x);
-        __syncthreads();
-    }
     const uint16_t* qb = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)q0 * a.q_stride +
                          kv_head * group * a.head_dim;
     const uint16_t* ob = reinterpret_cast<const uint16_t*>(a.dout) + (int64_t)q0 * a.dout_stride +
                          kv_head * group * a.head_dim;
     const int64_t stat = (int64_t)kv_head * group * a.q_items.start[a.batch] + q0;
+    const int64_t past = (int64_t)a.heads * a.q_items.start[a.batch];
     const int64_t q_pitch = a.q_stride * 2, o_pitch = a.dout_stride * 2;
     const bool near = max(q_pitch, o_pitch) <= T::kMaxPitch;
     const uint32_t q_off = T::lane_offset(wave, lane, q_pitch);
@@ -377,84 +386,109 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
 
     // The next tile to load. Tokens past the item's last repeat it and start
     // from the -inf behind the last row's value, so their P is 0.
-    const int64_t past = (int64_t)a.heads * a.q_items.start[a.batch];
     auto fetch = [&](int buf) {
-        const int token = at_tile * kWalk;
+        const int token = at_tile * kRows;
         const uint16_t* qm = qb + member * a.head_dim;
         const uint16_t* om = ob + member * a.head_dim;
         uint4* qt = tiles[buf];
-        uint4* ot = tiles[buf] + kWalk * T::kChunks;
+        uint4* ot = tiles[buf] + kRows * T::kChunks;
         if (wave < 2) {
             const int t = token + lane;
             const int64_t at = t < nq ? stat + (int64_t)member * a.q_items.start[a.batch] + t
                                       : past;
             dma4((wave ? f.minus_d : f.minus_lse) + at, lds_offset(stats[buf][wave]));
         }
-        if (near && token + kWalk <= nq) {
-            T::template load_rows<kWalk, kWaves>(qt, wave, qm + (int64_t)token * a.q_stride,
+        if (near && token + kRows <= nq) {
+            T::template load_rows<kRows, kWaves>(qt, wave, qm + (int64_t)token * a.q_stride,
                                                  q_pitch, q_off, on);
-            T::template load_rows<kWalk, kWaves>(ot, wave, om + (int64_t)token * a.dout_stride,
+            T::template load_rows<kRows, kWaves>(ot, wave, om + (int64_t)token * a.dout_stride,
                                                  o_pitch, o_off, on);
         } else {
-            T::template load<kWalk, kWaves>(qt, wave, lane, chunks, [&](int r) {
+            T::template load<kRows, kWaves>(qt, wave, lane, chunks, [&](int r) {
                 return reinterpret_cast<const uint4*>(qm +
                                                       (int64_t)min(token + r, nq - 1) * a.q_stride);
             });
-            T::template load<kWalk, kWaves>(ot, wave, lane, chunks, [&](int r) {
+            T::template load<kRows, kWaves>(ot, wave, lane, chunks, [&](int r) {
                 return reinterpret_cast<const uint4*>(
                     om + (int64_t)min(token + r, nq - 1) * a.dout_stride);
             });
         }
     };
     if (member >= last_member) fetch(0);
+
+    // One tile. The issue order is the written one: a matrix instruction, the
+    // reads of the fragments a few matrix instructions on, and in the first
+    // half of the sums the exponentials that the second half needs.
     auto walk = [&](bool masked, int buf, int row) {
+        constexpr int kAhead = 3;
+        const uint32_t at = T::row_base(tiles[buf], lane);
+        const uint32_t v_at = T::row_base(values + 32 * wave * T::kChunks, lane);
+        f32x16 s, dp;
 #pragma unroll
-        for (int b = 0; b < kWalk / 32; ++b) {
-            const uint32_t at = T::row_base(tiles[buf], lane);
-            f32x16 s, dp;
+        for (int j = 0; j < 4; ++j) {
+            const float4 l = *reinterpret_cast<const float4*>(&stats[buf][0][8 * j + 4 * h]);
+            const float4 d = *reinterpret_cast<const float4*>(&stats[buf][1][8 * j + 4 * h]);
+            s[4 * j] = l.x, s[4 * j + 1] = l.y, s[4 * j + 2] = l.z, s[4 * j + 3] = l.w;
+            dp[4 * j] = d.x, dp[4 * j + 1] = d.y, dp[4 * j + 2] = d.z, dp[4 * j + 3] = d.w;
+        }
+        bf16x8_t qf[kAhead], of[kAhead], vf[kAhead];
+        auto read = [&](int k) {
+            qf[k % kAhead] = T::row_frag(at, 0, k);
+            of[k % kAhead] = T::row_frag(at, kRows, k);
+            vf[k % kAhead] = T::row_frag(v_at, 0, k);
+        };
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 l =
-                    *reinterpret_cast<const float4*>(&stats[buf][0][32 * b + 8 * j + 4 * h]);
-                const float4 d =
-                    *reinterpret_cast<const float4*>(&stats[buf][1][32 * b + 8 * j + 4 * h]);
-                s[4 * j] = l.x, s[4 * j + 1] = l.y, s[4 * j + 2] = l.z, s[4 * j + 3] = l.w;
-                dp[4 * j] = d.x, dp[4 * j + 1] = d.y, dp[4 * j + 2] = d.z, dp[4 * j + 3] = d.w;
-            }
+        for (int k = 0; k < kAhead; ++k) read(k);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int k = 0; k < T::kSteps; ++k) {
-                s = mfma(T::row_frag(at, 32 * b, k), kf[k], s);
-                dp = mfma(T::row_frag(at, kWalk + 32 * b, k), vf[k], dp);
-            }
-            products_in_turn<T::kSteps, 8>();
-            if (masked) {
-                const int before = from - row - 4 * h;
+        for (int k = 0; k < T::kSteps; ++k) {
+            s = mfma(qf[k % kAhead], kf[k], s);
+            dp = mfma(of[k % kAhead], vf[k % kAhead], dp);
+            if (k + kAhead < T::kSteps) read(k + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (masked) {
+            const int before = from - row - 4 * h;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (32 * b + acc_row(i, 0) < before) s[i] = -INFINITY;
-            }
-            const uint32_t tr = T::tr_base(tiles[buf], lane);
+            for (int i = 0; i < 16; ++i)
+                if (acc_row(i, 0) < before) s[i] = -INFINITY;
+        }
+        const uint32_t tr = T::tr_base(tiles[buf], lane);
+        constexpr int kSums = 4 * T::kBlocks, kTrAhead = 5;
+        bf16x8_t frag[kTrAhead];
+        auto read_tr = [&](int i) {          // (t, d, dv or dk)
+            const int t = i / (2 * T::kBlocks), d = i / 2 % T::kBlocks;
+            frag[i % kTrAhead] = T::tr_frag(tr, (i & 1 ? 0 : kRows) + 16 * t, d);
+        };
+        bf16x8_t p[2], ds[2];
+        auto element = [&](int e) {
+            s[e] = __builtin_amdgcn_exp2f(s[e] * c);
+            dp[e] *= s[e];
+            p[e >> 3][e & 7] = (__bf16)s[e];
+            ds[e >> 3][e & 7] = (__bf16)dp[e];
+        };
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+        for (int i = 0; i < kTrAhead; ++i) read_tr(i);
 #pragma unroll
-                for (int i = 8 * t; i < 8 * t + 8; ++i) {
-                    s[i] = __builtin_amdgcn_exp2f(s[i] * c);
-                    dp[i] *= s[i];
-                }
-                const bf16x8_t p = acc_frag(s, t), ds = acc_frag(dp, t);
+        for (int e = 0; e < 8; ++e) element(e);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int d = 0; d < T::kBlocks; ++d) {
-                    dv[d] = mfma(T::tr_frag(tr, kWalk + 32 * b + 16 * t, d), p, dv[d]);
-                    dk[d] = mfma(T::tr_frag(tr, 32 * b + 16 * t, d), ds, dk[d]);
-                }
-            }
-            sums_in_turn<2 * T::kBlocks, 32>();
+        for (int i = 0; i < kSums; ++i) {
+            const int t = i / (2 * T::kBlocks), d = i / 2 % T::kBlocks;
+            if (i & 1) dk[d] = mfma(frag[i % kTrAhead], ds[t], dk[d]);
+            else dv[d] = mfma(frag[i % kTrAhead], p[t], dv[d]);
+            if (i + kTrAhead < kSums) read_tr(i + kTrAhead);
+            if (t == 0)
+#pragma unroll
+                for (int e = 8 + 8 * i / (2 * T::kBlocks); e < 8 + 8 * (i + 1) / (2 * T::kBlocks);
+                     ++e)
+                    element(e);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     int buf = 0;
     while (member >= last_member) {
-        const int row = at_tile * kWalk;                 // of the tile in `buf`
+        const int row = at_tile * kRows;                 // of the tile in `buf`
         tile_barrier();
         --at_tile;
         settle_tile();
@@ -473,7 +507,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
         return;
     }
     tile_barrier();
-    uint4* stage = tiles[0] + wave * 32 * T::kChunks;
+    uint4* stage = values + wave * 32 * T::kChunks;
     auto to = [&](void* base, int64_t stride) {
         return [=](int r) -> uint4* {
             const int at = key0 + 32 * wave + r;
