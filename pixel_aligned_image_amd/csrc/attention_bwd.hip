@@ -312,7 +312,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int chunks = a.head_dim >> 3;
 
-    const int tile = blockIdx.x / a.kv_heads, kv_head = blockIdx.x - tile * a.kv_heads;
+    // Causal: the parts of the longest tiles first, so that the last ones to
+    // run are short (12,289 tokens: 961 -> 878 us). Otherwise part by part, so
+    // that neighbours walk the same rows (2 x 1029 keys: 104 -> 96 us).
+    const int units = gridDim.x / f.splits;
+    const int unit = a.causal ? blockIdx.x / f.splits : blockIdx.x % units;
+    const int part = a.causal ? blockIdx.x % f.splits : blockIdx.x / units;
+    const int tile = unit / a.kv_heads, kv_head = unit - tile * a.kv_heads;
     const int item = item_of_tile(f.tiles, a.batch, tile);
     const int key0 = (tile - f.tiles.start[item]) * kHeld;
     const int q0 = a.q_items.start[item], nq = a.q_items.start[item + 1] - q0;
@@ -355,8 +361,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     // 12,289 tokens missed L2.)
     const int per_head = (nq + kRows - 1) / kRows;
     const int64_t all = (int64_t)per_head * group;
-    const int low = (int)(all * blockIdx.y / f.splits);
-    const int high = (int)(all * (blockIdx.y + 1) / f.splits);
+    const int low = (int)(all * part / f.splits);
+    const int high = (int)(all * (part + 1) / f.splits);
     const int last_member = low < high ? low / per_head : 0;
     int member = low < high ? (high - 1) / per_head : -1;
     int at_tile = min(per_head, high - member * per_head) - 1;
@@ -500,7 +506,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     if (f.splits > 1) {
         if (!live) return;
         const int64_t rows = (int64_t)a.k_items.start[a.batch] * a.kv_heads;
-        const int64_t at = (blockIdx.y * rows + (int64_t)(k0 + key) * a.kv_heads + kv_head) *
+        const int64_t at = (part * rows + (int64_t)(k0 + key) * a.kv_heads + kv_head) *
                            a.head_dim;
         store_sums<HD>(dk, f.part + at, a.head_dim, lane);
         store_sums<HD>(dv, f.part2 + at, a.head_dim, lane);
@@ -569,7 +575,7 @@ hipError_t backward_as(BwdArgs& f, const AttnPlan& p, hipStream_t s) {
         cut_items(a.k_items, a.batch, 1, kHeld, &f.tiles);
         f.splits = p.dk_splits;
         f.part2 = f.part + f.splits * k_rows * a.head_dim;
-        dkv_kernel<HD><<<dim3((unsigned)f.tiles.start[a.batch] * a.kv_heads, (unsigned)f.splits),
+        dkv_kernel<HD><<<dim3((unsigned)(f.tiles.start[a.batch] * a.kv_heads * f.splits)),
                          dim3(64 * kWaves), 0, s>>>(f);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (f.splits > 1) {
