@@ -2,11 +2,20 @@
 // forward call's lse the probabilities are one exponential away from the
 // scores, P = exp(scale S - lse), so both kernels recompute them tile by tile:
 //
-//   rows kernel   D_i = dout_i . out_i and lse in the exponent's unit, once
+//   rows kernel   D_i = dout_i . out_i and lse in the scores' unit, once
 //   dq kernel     a wave holds 32 query rows and walks the keys:
 //                 dS^T = P^T (V dO^T - D),  dQ^T += K^T dS^T
-//   dkv kernel    a wave holds 32 keys and walks the query rows:
+//                 and on the way D_i = sum_j P_ij (dout_i . v_j)
+//   dkv kernel    a wave holds 32 keys and walks the query rows, with that D:
 //                 dV^T += dO^T P,  dK^T += Q^T dS
+//
+// A result is off by its own rounding to bf16, by that of dS (as large) and by
+// D's, which out's rounding and that of the forward call's P have moved: half
+// as large where a row sees some ten keys, and less as the root of their
+// number. All three make 1.57 times the first alone on items of 11 keys, 1.43
+// on long ones. Rows that see few keys therefore take dS as the sum of two bf16
+// factors (1.24 there; another product on fragments already read, 40 % more
+// time if every row did), and dk takes the D that the dq kernel sums up (1.42).
 //
 // Each product's second factor is the softmax tile as the first product left
 // it in registers (attn_tile.h). The scores are computed twice, once per
@@ -29,7 +38,8 @@ using namespace attn;
 
 constexpr int kWaves = 4;
 constexpr int kHeld = 32 * kWaves;       // rows (dq) or keys (dkv) held by a workgroup
-constexpr int kWalk = 64;                // keys (dq) or rows (dkv) of one walked tile
+constexpr int kWalk = 64;                // keys of a tile that the dq kernel walks
+constexpr int kFineKeys = 256;           // rows seeing so many take dS in two factors
 
 struct BwdArgs {
     AttnArgs a;
@@ -38,6 +48,7 @@ struct BwdArgs {
     int splits;
     float *minus_lse, *minus_d;          // [heads][nq], then -inf and 0
     float *part, *part2;                 // [splits][n * heads][head_dim]: dq, or dk and dv
+    float* part_d;                       // [splits][nq * heads]
 };
 
 // What the score and dP products of every row start from: -lse / scale, so that
@@ -218,12 +229,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
         for (int i = 0; i < 16; ++i)
             if (acc_row(i, 0) >= left) s[i] = -INFINITY;
     };
-    auto gradient = [&](f32x16& s, const f32x16& dp) {
+    // dS as a bf16 factor (fine: as the sum of two), and this lane's share of D
+    float sum_d = 0.f;
+    auto gradient = [&](auto fine, f32x16& s, const f32x16& dp, bf16x8_t* hi, bf16x8_t* lo) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            s[i] = __builtin_amdgcn_exp2f(s[i] * c + minus_lse2) * (dp[i] + minus_d);
+        for (int i = 0; i < 16; ++i) {
+            const float p = __builtin_amdgcn_exp2f(s[i] * c + minus_lse2);
+            sum_d += p * dp[i];
+            const float g = p * (dp[i] + minus_d);
+            hi[i >> 3][i & 7] = (__bf16)g;
+            if constexpr (decltype(fine)::value)
+                lo[i >> 3][i & 7] = (__bf16)(g - (float)hi[i >> 3][i & 7]);
+        }
     };
-    auto walk = [&](bool masked, int buf, int key) {
+    auto walk = [&](auto fine, bool masked, int buf, int key) {
+        constexpr bool kFine = decltype(fine)::value;
+        constexpr int kVector = kFine ? 136 : 88;        // vector instructions of gradient()
         const uint32_t k_at = T::row_base(kt[buf], lane), v_at = T::row_base(vt[buf], lane);
         f32x16 s0, dp0, s1, dp1;
         __builtin_amdgcn_s_setprio(1);       // (as in the forward kernel)
@@ -233,52 +254,65 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
         if (masked) mask(s0, key);
         // the second block's products under the first one's exponentials
         products(s1, dp1, k_at, v_at, 1);
-        gradient(s0, dp0);
-        bf16x8_t ds[4];
-        ds[0] = acc_frag(s0, 0);
-        ds[1] = acc_frag(s0, 1);
+        bf16x8_t hi[4], lo[4];
+        gradient(fine, s0, dp0, hi, lo);
         __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
         for (int i = 0; i < 2 * T::kSteps; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 72 / (2 * T::kSteps) + 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, kVector / (2 * T::kSteps) + 1, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
         if (masked) mask(s1, key + 32);
         const uint32_t k_tr = T::tr_base(kt[buf], lane);
-        gradient(s1, dp1);
-        ds[2] = acc_frag(s1, 0);
-        ds[3] = acc_frag(s1, 1);
+        gradient(fine, s1, dp1, hi + 2, lo + 2);
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t) {
+            bf16x8_t frag[T::kBlocks];
 #pragma unroll
-            for (int d = 0; d < T::kBlocks; ++d)
-                dq[d] = mfma(T::tr_frag(k_tr, 16 * t, d), ds[t], dq[d]);
+            for (int d = 0; d < T::kBlocks; ++d) frag[d] = T::tr_frag(k_tr, 16 * t, d);
+#pragma unroll
+            for (int d = 0; d < T::kBlocks; ++d) dq[d] = mfma(frag[d], hi[t], dq[d]);
+            if constexpr (kFine)
+#pragma unroll
+                for (int d = 0; d < T::kBlocks; ++d) dq[d] = mfma(frag[d], lo[t], dq[d]);
+        }
         __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
 #pragma unroll
-        for (int i = 0; i < 4 * T::kBlocks; ++i) {
+        for (int i = 0; i < (kFine ? 8 : 4) * T::kBlocks; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 72 / (2 * T::kBlocks) + 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, kFine ? 1 : 2, 0);
+            __builtin_amdgcn_sched_group_barrier(
+                0x002, kVector / ((kFine ? 4 : 2) * T::kBlocks) + 1, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    int buf = 0;
-    for (int key = begin; key < end; key += kWalk, buf ^= 1) {
-        tile_barrier();
-        if (key + kWalk < end) fetch(buf ^ 1, key + kWalk);
-        walk(key + kWalk > all_see, buf, key);
-    }
+    auto walk_all = [&](auto fine) {
+        int buf = 0;
+        for (int key = begin; key < end; key += kWalk, buf ^= 1) {
+            tile_barrier();
+            if (key + kWalk < end) fetch(buf ^ 1, key + kWalk);
+            walk(fine, key + kWalk > all_see, buf, key);
+        }
+    };
+    if (end <= kFineKeys) walk_all(std::true_type{});
+    else walk_all(std::false_type{});
 
+    float own;
+    const float other = other_half(sum_d, own);
+    sum_d = own + other;
     const int64_t out_row = (int64_t)(q0 + (int)token) * a.heads + head;
     if (f.splits > 1) {
         const int64_t all = (int64_t)a.q_items.start[a.batch] * a.heads;
-        if (live)
+        if (live) {
             store_sums<HD>(dq, f.part + (blockIdx.y * all + out_row) * a.head_dim, a.head_dim,
                            lane);
+            if (lane < 32) f.part_d[blockIdx.y * all + out_row] = sum_d;
+        }
         return;
     }
+    if (live && lane < 32) f.minus_d[stat] = -sum_d;
     tile_barrier();
     const float by = a.scale;
     uint4* stage = wave < 2 ? kt[wave] : vt[wave - 2];
@@ -527,10 +561,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     store_rows<HD>(dv, 1.0f, stage, chunks, lane, to(a.dv, a.dv_stride));
 }
 
-// Adds the parts of (token, head) rows in order: 32 lanes per row.
+// Adds the parts of (token, head) rows in order: 32 lanes per row. With
+// `part_d`, also those of D, into minus_d [heads][tokens].
 __global__ __launch_bounds__(256) void join_kernel(const float* part, int splits, int64_t rows,
                                                    int heads, int hd, float by, void* out,
-                                                   int64_t stride) {
+                                                   int64_t stride, const float* part_d,
+                                                   float* minus_d) {
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int d = (threadIdx.x & 31) * 4;
     if (row >= rows || d >= hd) return;
@@ -546,12 +582,18 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, int splits
     const int head = (int)(row - token * heads);
     *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + token * stride + head * hd + d) =
         make_uint2(pack_bf16x2(s.x * by, s.y * by), pack_bf16x2(s.z * by, s.w * by));
+    if (part_d && d == 0) {
+        float sum = 0.f;
+        for (int p = 0; p < splits; ++p) sum += part_d[p * rows + row];
+        minus_d[rows / heads * head + token] = -sum;
+    }
 }
 
 hipError_t join(const float* part, int splits, int64_t rows, int heads, int hd, float by,
-                void* out, int64_t stride, hipStream_t s) {
-    join_kernel<<<dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s>>>(part, splits, rows, heads,
-                                                                      hd, by, out, stride);
+                void* out, int64_t stride, hipStream_t s, const float* part_d = nullptr,
+                float* minus_d = nullptr) {
+    join_kernel<<<dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s>>>(
+        part, splits, rows, heads, hd, by, out, stride, part_d, minus_d);
     return hipGetLastError();
 }
 
@@ -564,11 +606,12 @@ hipError_t backward_as(BwdArgs& f, const AttnPlan& p, hipStream_t s) {
     if (q_rows > 0) {
         cut_items(a.q_items, a.batch, f.group.size, kHeld, &f.tiles);
         f.splits = p.dq_splits;
+        f.part_d = f.part + f.splits * q_rows * a.head_dim;
         dq_kernel<HD><<<dim3((unsigned)f.tiles.start[a.batch] * a.kv_heads, (unsigned)f.splits),
                         dim3(64 * kWaves), 0, s>>>(f);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (f.splits > 1 && (e = join(f.part, f.splits, q_rows, a.heads, a.head_dim, a.scale, a.dq,
-                                      a.dq_stride, s)) != hipSuccess)
+                                      a.dq_stride, s, f.part_d, f.minus_d)) != hipSuccess)
             return e;
     }
     if (k_rows > 0) {
@@ -617,10 +660,10 @@ void plan_attention_backward(const AttnArgs& a, AttnPlan* p) {
     p->dk_splits = parts((int64_t)kt.start[a.batch] * a.kv_heads, most_rows);
     const size_t q_rows = (size_t)a.q_items.start[a.batch] * a.heads;
     const size_t k_rows = (size_t)a.k_items.start[a.batch] * a.kv_heads;
-    const size_t dq = p->dq_splits > 1 ? p->dq_splits * q_rows : 0;
-    const size_t dk = p->dk_splits > 1 ? 2 * p->dk_splits * k_rows : 0;
+    const size_t dq = p->dq_splits > 1 ? p->dq_splits * q_rows * (a.head_dim + 1) : 0;
+    const size_t dk = p->dk_splits > 1 ? 2 * p->dk_splits * k_rows * a.head_dim : 0;
     p->backward_bytes = 256 + 2 * padded((q_rows + 1) * sizeof(float)) +
-                        std::max(dq, dk) * a.head_dim * sizeof(float);
+                        std::max(dq, dk) * sizeof(float);
 }
 
 hipError_t launch_attention_backward(const AttnArgs& a, const AttnPlan& p, void* ws,
