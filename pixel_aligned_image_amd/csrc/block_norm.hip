@@ -21,6 +21,21 @@
 
 namespace p3d {
 
+// About four workgroups per CU, and at least 16 rows each, so that the chunk
+// sums (12 bytes per column and chunk, written and read once) stay small
+// beside the rows.
+int64_t norm_chunks(int64_t n, int32_t batch, const ItemTable& items, ItemTable* chunks) {
+    const int64_t most = 4 * kComputeUnits;
+    const int64_t rpc = std::max<int64_t>((n + most - 1) / most, 16);
+    int32_t at = 0;
+    for (int32_t b = 0; b < batch; ++b) {
+        chunks->start[b] = at;
+        at += (int32_t)((items.start[b + 1] - items.start[b] + rpc - 1) / rpc);
+    }
+    for (int32_t b = batch; b <= P3D_MAX_BATCH; ++b) chunks->start[b] = at;
+    return rpc;
+}
+
 namespace {
 
 constexpr int kThreads = 256;
@@ -56,26 +71,24 @@ struct RowVec {
     static constexpr int N = Vec<T>::N;
     float f[VPT][N];
 
-    __device__ __forceinline__ void load(const void* base, int64_t row, int nv, int t) {
-        const uint4* p = reinterpret_cast<const uint4*>(base) + row * nv;
-        uint4 q[VPT];
-#pragma unroll
-        for (int u = 0; u < VPT; ++u) {
-            const int v = u * TPR + t;
-            q[u] = v < nv ? p[v] : make_uint4(0, 0, 0, 0);
-        }
+    __device__ __forceinline__ void widen(const uint4 (&q)[VPT]) {
 #pragma unroll
         for (int u = 0; u < VPT; ++u) Vec<T>::widen(q[u], f[u]);
     }
-    __device__ __forceinline__ void store(void* base, int64_t row, int nv, int t) const {
-        uint4* p = reinterpret_cast<uint4*>(base) + row * nv;
-#pragma unroll
-        for (int u = 0; u < VPT; ++u) {
-            const int v = u * TPR + t;
-            if (v < nv) p[v] = Vec<T>::narrow(f[u]);
-        }
-    }
 };
+
+// A row's vectors as they lie, zeros past its end (and where there is no
+// tensor).
+template <int VPT, int TPR>
+__device__ __forceinline__ void load_row(uint4 (&q)[VPT], const void* base, int64_t row, int nv,
+                                         int t) {
+    const uint4* p = reinterpret_cast<const uint4*>(base) + row * nv;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int v = u * TPR + t;
+        q[u] = base && v < nv ? p[v] : make_uint4(0, 0, 0, 0);
+    }
+}
 
 // One vector of a per-column parameter, `other` where it is absent.
 template <typename T>
@@ -87,6 +100,24 @@ __device__ __forceinline__ void param(const void* base, int64_t offset, int v, i
     } else {
 #pragma unroll
         for (int e = 0; e < Vec<T>::N; ++e) f[e] = other;
+    }
+}
+
+// One value of a per-column parameter, `other` where it is absent.
+template <typename T>
+__device__ __forceinline__ float column(const void* base, int64_t i, float other) {
+    if (!base) return other;
+    if constexpr (sizeof(T) == 4) return reinterpret_cast<const float*>(base)[i];
+    else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[i] << 16);
+}
+
+// What a vector's columns are multiplied or shifted by.
+template <int N>
+__device__ __forceinline__ void factors(const float* lds, int v, float (&f)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(lds + v * N + e);
+        f[e] = q.x, f[e + 1] = q.y, f[e + 2] = q.z, f[e + 3] = q.w;
     }
 }
 
@@ -125,7 +156,8 @@ __device__ __forceinline__ float normalise(RowVec<T, VPT, TPR>& v, int kind, int
 }
 
 // d <- the gradient of the norm's input from the gradient d of its output n:
-// rstd (d - n mean(d n) - mean(d)), the last term for LAYER only.
+// rstd (d - n mean(d n) - mean(d)), the last term for LAYER only (0 past the
+// row's end).
 template <typename T, int VPT, int TPR>
 __device__ __forceinline__ void normalise_backward(RowVec<T, VPT, TPR>& d,
                                                    const RowVec<T, VPT, TPR>& n, int kind,
@@ -144,13 +176,32 @@ __device__ __forceinline__ void normalise_backward(RowVec<T, VPT, TPR>& d,
     const float dot = row_sum<TPR>(q, red) * inv_dim;
     const float mean = kind == P3D_NORM_LAYER ? row_sum<TPR>(s, red) * inv_dim : 0.f;
 #pragma unroll
-    for (int u = 0; u < VPT; ++u)
+    for (int u = 0; u < VPT; ++u) {
+        const bool in = u * TPR + t < nv;
 #pragma unroll
-        for (int e = 0; e < N; ++e) d.f[u][e] = rstd * (d.f[u][e] - n.f[u][e] * dot - mean);
+        for (int e = 0; e < N; ++e)
+            d.f[u][e] = in ? rstd * (d.f[u][e] - n.f[u][e] * dot - mean) : 0.f;
+    }
+}
+
+// A row's vectors out; `nt`: past the caches.
+template <typename T, int VPT, int TPR>
+__device__ __forceinline__ void store_row(const RowVec<T, VPT, TPR>& r, void* base, int64_t row,
+                                          int nv, int t, bool nt) {
+    uint4* p = reinterpret_cast<uint4*>(base) + row * nv;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int v = u * TPR + t;
+        if (v >= nv) continue;
+        const uint4 q = Vec<T>::narrow(r.f[u]);
+        if (nt) store_nt16(p + v, q);
+        else p[v] = q;
+    }
 }
 
 template <typename T, int VPT, int TPR>
-__global__ __launch_bounds__(kThreads) void gated_norm_kernel(NormArgs a, ItemTable items) {
+__global__ __launch_bounds__(kThreads) void gated_norm_kernel(NormArgs a, ItemTable items,
+                                                              bool nt) {
     constexpr int N = Vec<T>::N;
     __shared__ float red[4];
     const int t = threadIdx.x % TPR;
@@ -160,11 +211,14 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(NormArgs a, ItemTa
     for (int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR; row < a.n;
          row += (int64_t)gridDim.x * (kThreads / TPR)) {
         const int64_t mod = item_of(items, a.batch, row) * (a.mod_stride / N);
+        uint4 raw_x[VPT], raw_y[VPT];
+        load_row<VPT, TPR>(raw_x, a.x, row, nv, t);
+        load_row<VPT, TPR>(raw_y, a.y, row, nv, t);
         RowVec<T, VPT, TPR> x;
-        x.load(a.x, row, nv, t);
+        x.widen(raw_x);
         if (a.y) {
             RowVec<T, VPT, TPR> y;
-            y.load(a.y, row, nv, t);
+            y.widen(raw_y);
             normalise(y, a.post, nv, t, inv_dim, a.eps, red);
 #pragma unroll
             for (int u = 0; u < VPT; ++u) {
@@ -176,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(NormArgs a, ItemTa
                 for (int e = 0; e < N; ++e) x.f[u][e] += a.res_scale * g[e] * (y.f[u][e] * w[e]);
             }
         }
-        if (a.r) x.store(a.r, row, nv, t);
+        if (a.r) store_row(x, a.r, row, nv, t, nt);
         normalise(x, a.pre, nv, t, inv_dim, a.eps, red);
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
@@ -190,24 +244,29 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(NormArgs a, ItemTa
             for (int e = 0; e < N; ++e)
                 x.f[u][e] = (x.f[u][e] * w[e] + b[e]) * (1.0f + sc[e]) + sh[e];
         }
-        x.store(a.h, row, nv, t);
+        store_row(x, a.h, row, nv, t, nt);
     }
 }
 
 // The three column sums that every parameter gradient is made of, per item:
 // A = sum dh n, S = sum dh, G = sum dr t^ (n, t^ the normalised r and y). A
-// workgroup walks one chunk of one item's rows with its sums in registers,
-// joins its row groups through LDS in a fixed order and writes [3][dim]
+// workgroup walks one chunk of one item's rows with its sums in registers and
+// what its columns are multiplied by in LDS, put together once; x and y of the
+// next row are loaded, still packed, while a row is worked on, dh and dr before
+// the statistics that come ahead of them. It joins its row groups through LDS in a fixed order and writes [3][dim]
 // binary32 values; no atomics, so the sums' order never changes.
 template <typename T, int VPT, int TPR>
-__global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(NormArgs a,
+__global__ __launch_bounds__(kThreads, VPT * Vec<T>::N <= 24 ? 2 : 1) void gated_norm_backward_kernel(NormArgs a,
                                                                        ItemTable items,
                                                                        ItemTable chunks,
-                                                                       int64_t rows_per_chunk) {
+                                                                       int64_t rows_per_chunk,
+                                                                       bool nt) {
     constexpr int N = Vec<T>::N;
     constexpr int R = kThreads / TPR;        // rows in flight
     __shared__ float red[4];
-    __shared__ float cols[R * TPR * VPT * N];
+    extern __shared__ float cols[];          // [2][dim], then [R][TPR * VPT * N]
+    float* mul = cols;                       // weight (1 + scale)
+    float* lift = cols + a.dim;              // res_scale gate post_weight
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int nv = a.dim / N;
     const float inv_dim = 1.0f / (float)a.dim;
@@ -215,7 +274,19 @@ __global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(NormArgs 
     const int64_t first = items.start[item] +
                           (int64_t)((int)blockIdx.x - chunks.start[item]) * rows_per_chunk;
     const int64_t end = min(first + rows_per_chunk, (int64_t)items.start[item + 1]);
-    const int64_t mod = item * (a.mod_stride / N);
+
+    // (a group past the last row repeats it, stores nothing and adds nothing)
+    int64_t row = first + group;
+    uint4 next_x[VPT], next_y[VPT];
+    load_row<VPT, TPR>(next_x, a.x, min(row, end - 1), nv, t);
+    load_row<VPT, TPR>(next_y, a.y, min(row, end - 1), nv, t);
+    const int64_t mod = item * a.mod_stride;
+    for (int c = threadIdx.x; c < a.dim; c += kThreads) {
+        mul[c] = column<T>(a.weight, c, 1.f) * (1.0f + column<T>(a.scale, mod + c, 0.f));
+        lift[c] = a.res_scale * column<T>(a.gate, mod + c, 1.f) *
+                  column<T>(a.post_weight, c, 1.f);
+    }
+    __syncthreads();
 
     float sums[3][VPT][N];
 #pragma unroll
@@ -225,68 +296,73 @@ __global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(NormArgs 
 #pragma unroll
             for (int e = 0; e < N; ++e) sums[k][u][e] = 0.f;
 
-    for (int64_t row = first + group; row < end; row += R) {
-        RowVec<T, VPT, TPR> x, y, d, dr;
-        x.load(a.x, row, nv, t);
-        if (a.y) y.load(a.y, row, nv, t);
-        d.load(a.dh, row, nv, t);
-        if (a.dr) dr.load(a.dr, row, nv, t);
+    // every thread takes the turns of the workgroup's first row
+    for (int64_t top = first; top < end; top += R, row += R) {
+        const bool live = row < end;
+        RowVec<T, VPT, TPR> x, y, d;
+        uint4 raw_d[VPT], raw_r[VPT];
+        load_row<VPT, TPR>(raw_d, a.dh, min(row, end - 1), nv, t);
+        load_row<VPT, TPR>(raw_r, a.dr, min(row, end - 1), nv, t);
+        x.widen(next_x);
+        if (a.y) y.widen(next_y);
+        load_row<VPT, TPR>(next_x, a.x, min(row + R, end - 1), nv, t);
+        load_row<VPT, TPR>(next_y, a.y, min(row + R, end - 1), nv, t);
         float y_rstd = 1.f;
         if (a.y) {
             y_rstd = normalise(y, a.post, nv, t, inv_dim, a.eps, red);
 #pragma unroll
             for (int u = 0; u < VPT; ++u) {
-                const int v = u * TPR + t;
-                float g[N], w[N];
-                param<T>(a.gate, mod, v, nv, 1.f, g);
-                param<T>(a.post_weight, 0, v, nv, 1.f, w);
+                float g[N];
+                factors<N>(lift, min(u * TPR + t, nv - 1), g);
 #pragma unroll
-                for (int e = 0; e < N; ++e) x.f[u][e] += a.res_scale * g[e] * (y.f[u][e] * w[e]);
+                for (int e = 0; e < N; ++e) x.f[u][e] += g[e] * y.f[u][e];
             }
         }
         const float rstd = normalise(x, a.pre, nv, t, inv_dim, a.eps, red);
+        d.widen(raw_d);
+        const float once = live ? 1.f : 0.f;
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
-            const int v = u * TPR + t;
-            float w[N], sc[N];
-            param<T>(a.weight, 0, v, nv, 1.f, w);
-            param<T>(a.scale, mod, v, nv, 0.f, sc);
+            float m[N];
+            factors<N>(mul, min(u * TPR + t, nv - 1), m);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                sums[0][u][e] += d.f[u][e] * x.f[u][e];
-                sums[1][u][e] += d.f[u][e];
-                d.f[u][e] *= (1.0f + sc[e]) * w[e];
+                sums[0][u][e] += once * d.f[u][e] * x.f[u][e];
+                sums[1][u][e] += once * d.f[u][e];
+                d.f[u][e] *= m[e];
             }
         }
         normalise_backward(d, x, a.pre, rstd, nv, t, inv_dim, red);
         if (a.dr) {
 #pragma unroll
-            for (int u = 0; u < VPT; ++u)
+            for (int u = 0; u < VPT; ++u) {
+                float f[N];
+                Vec<T>::widen(raw_r[u], f);
 #pragma unroll
-                for (int e = 0; e < N; ++e) d.f[u][e] += dr.f[u][e];
+                for (int e = 0; e < N; ++e) d.f[u][e] += f[e];
+            }
         }
-        d.store(a.dx, row, nv, t);
+        if (live) store_row(d, a.dx, row, nv, t, nt);
         if (a.y) {
 #pragma unroll
             for (int u = 0; u < VPT; ++u) {
-                const int v = u * TPR + t;
-                float g[N], w[N];
-                param<T>(a.gate, mod, v, nv, 1.f, g);
-                param<T>(a.post_weight, 0, v, nv, 1.f, w);
+                float g[N];
+                factors<N>(lift, min(u * TPR + t, nv - 1), g);
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    sums[2][u][e] += d.f[u][e] * y.f[u][e];
-                    d.f[u][e] *= a.res_scale * g[e] * w[e];
+                    sums[2][u][e] += once * d.f[u][e] * y.f[u][e];
+                    d.f[u][e] *= g[e];
                 }
             }
             if (a.dy) {
                 normalise_backward(d, y, a.post, y_rstd, nv, t, inv_dim, red);
-                d.store(a.dy, row, nv, t);
+                if (live) store_row(d, a.dy, row, nv, t, nt);
             }
         }
     }
 
     if (!a.partial) return;
+    float* joint = cols + 2 * a.dim;
     float* out = a.partial + (int64_t)blockIdx.x * 3 * a.dim;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
@@ -295,21 +371,14 @@ __global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(NormArgs 
         for (int u = 0; u < VPT; ++u)
 #pragma unroll
             for (int e = 0; e < N; ++e)
-                cols[(group * VPT * TPR + u * TPR + t) * N + e] = sums[k][u][e];
+                joint[(group * VPT * TPR + u * TPR + t) * N + e] = sums[k][u][e];
         __syncthreads();
         for (int c = threadIdx.x; c < a.dim; c += kThreads) {
             float s = 0.f;
-            for (int g = 0; g < R; ++g) s += cols[g * VPT * TPR * N + c];
+            for (int g = 0; g < R; ++g) s += joint[g * VPT * TPR * N + c];
             out[k * a.dim + c] = s;
         }
     }
-}
-
-template <typename T>
-__device__ __forceinline__ float column(const void* base, int64_t i, float other) {
-    if (!base) return other;
-    if constexpr (sizeof(T) == 4) return reinterpret_cast<const float*>(base)[i];
-    else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[i] << 16);
 }
 
 // Joins an item's chunks: 32 columns by 32 chunk lanes per workgroup, each
@@ -377,86 +446,72 @@ __global__ __launch_bounds__(kThreads) void norm_items_kernel(NormArgs a,
     if (a.dpost_weight) a.dpost_weight[c] = s[2];
 }
 
+// Results go past the caches where the call's tensors do not fit the 256 MB of
+// last-level cache anyway (100,000 rows of 1536 bf16: 260 -> 229 us); below
+// that the next call finds them there.
+bool past_caches(const NormArgs& a, int planes, int bytes) {
+    return a.n * a.dim * planes * bytes > (int64_t(256) << 20);
+}
+
 template <typename T, int VPT, int TPR>
 hipError_t forward_as(const NormArgs& a, const ItemTable& items, hipStream_t s) {
     const int64_t rows = kThreads / TPR;
     // (a launch holds under 2^32 threads)
     const int64_t blocks = std::min<int64_t>((a.n + rows - 1) / rows, int64_t(1) << 22);
-    gated_norm_kernel<T, VPT, TPR><<<dim3((unsigned)blocks), dim3(kThreads), 0, s>>>(a, items);
+    gated_norm_kernel<T, VPT, TPR><<<dim3((unsigned)blocks), dim3(kThreads), 0, s>>>(
+        a, items, past_caches(a, 4, 16 / Vec<T>::N));
     return hipGetLastError();
 }
 
 template <typename T, int VPT, int TPR>
 hipError_t backward_as(const NormArgs& a, const ItemTable& items, const ItemTable& chunks,
                        int64_t rows_per_chunk, hipStream_t s) {
+    const size_t lds = (2 * a.dim + kThreads * VPT * Vec<T>::N) * sizeof(float);
     gated_norm_backward_kernel<T, VPT, TPR>
-        <<<dim3((unsigned)chunks.start[a.batch]), dim3(kThreads), 0, s>>>(a, items, chunks,
-                                                                        rows_per_chunk);
+        <<<dim3((unsigned)chunks.start[a.batch]), dim3(kThreads), lds, s>>>(
+            a, items, chunks, rows_per_chunk, past_caches(a, 6, 16 / Vec<T>::N));
     return hipGetLastError();
 }
 
 // The group of threads of a row of `nv` vectors, and its vectors per thread:
-// the smallest group that needs at most 4 (bf16) or 8 (binary32, half as wide)
-// vectors per thread.
-#define P3D_NORM_SHAPES(T, CALL)                                                        \
-    if (nv <= 16) return CALL(T, 1, 16);                                                \
-    if (nv <= 32) return CALL(T, 1, 32);                                                \
-    if (nv <= 64) return CALL(T, 1, 64);                                                \
-    if (nv <= 128) return CALL(T, 2, 64);                                               \
-    if (nv <= 192) return CALL(T, 3, 64);                                               \
-    if (nv <= 256) return CALL(T, 4, 64);
-
+// the smallest group that keeps a row's values in registers (the backward call
+// also its three sums: 24 columns a thread), else the whole workgroup.
 template <typename T>
 hipError_t forward_of(const NormArgs& a, const ItemTable& items, hipStream_t s) {
     const int nv = a.dim / Vec<T>::N;
-#define CALL(T, V, P) forward_as<T, V, P>(a, items, s)
-    P3D_NORM_SHAPES(T, CALL)
+    if (nv <= 16) return forward_as<T, 1, 16>(a, items, s);
+    if (nv <= 32) return forward_as<T, 1, 32>(a, items, s);
+    if (nv <= 64) return forward_as<T, 1, 64>(a, items, s);
+    if (nv <= 128) return forward_as<T, 2, 64>(a, items, s);
+    if (nv <= 192) return forward_as<T, 3, 64>(a, items, s);
+    if (nv <= 256) return forward_as<T, 4, 64>(a, items, s);
     if constexpr (Vec<T>::N == 4) {
-        if (nv <= 384) return CALL(T, 6, 64);
-        if (nv <= 512) return CALL(T, 8, 64);
+        if (nv <= 384) return forward_as<T, 6, 64>(a, items, s);
+        if (nv > 1024) return forward_as<T, 8, 256>(a, items, s);
     }
-    if constexpr (Vec<T>::N == 4) {
-        if (nv > 1024) return CALL(T, 8, 256);
-    }
-    if (nv <= 512) return CALL(T, 2, 256);
-    return CALL(T, 4, 256);
-#undef CALL
+    if (nv <= 512) return forward_as<T, 2, 256>(a, items, s);
+    return forward_as<T, 4, 256>(a, items, s);
 }
 
 template <typename T>
 hipError_t backward_of(const NormArgs& a, const ItemTable& items, const ItemTable& chunks,
                        int64_t rpc, hipStream_t s) {
     const int nv = a.dim / Vec<T>::N;
-#define CALL(T, V, P) backward_as<T, V, P>(a, items, chunks, rpc, s)
-    P3D_NORM_SHAPES(T, CALL)
+    if (nv <= 16) return backward_as<T, 1, 16>(a, items, chunks, rpc, s);
+    if (nv <= 32) return backward_as<T, 1, 32>(a, items, chunks, rpc, s);
+    if (nv <= 64) return backward_as<T, 1, 64>(a, items, chunks, rpc, s);
+    if (nv <= 128) return backward_as<T, 2, 64>(a, items, chunks, rpc, s);
+    if (nv <= 192) return backward_as<T, 3, 64>(a, items, chunks, rpc, s);
     if constexpr (Vec<T>::N == 4) {
-        if (nv <= 384) return CALL(T, 6, 64);
-        if (nv <= 512) return CALL(T, 8, 64);
+        if (nv <= 256) return backward_as<T, 4, 64>(a, items, chunks, rpc, s);
+        if (nv > 1024) return backward_as<T, 8, 256>(a, items, chunks, rpc, s);
     }
-    if constexpr (Vec<T>::N == 4) {
-        if (nv > 1024) return CALL(T, 8, 256);
-    }
-    if (nv <= 512) return CALL(T, 2, 256);
-    return CALL(T, 4, 256);
-#undef CALL
+    if (nv <= 256) return backward_as<T, 1, 256>(a, items, chunks, rpc, s);
+    if (nv <= 512) return backward_as<T, 2, 256>(a, items, chunks, rpc, s);
+    return backward_as<T, 4, 256>(a, items, chunks, rpc, s);
 }
 
 }  // namespace
-
-// About four workgroups per CU, and at least 16 rows each, so that the chunk
-// sums (12 bytes per column and chunk, written and read once) stay small
-// beside the rows.
-int64_t norm_chunks(int64_t n, int32_t batch, const ItemTable& items, ItemTable* chunks) {
-    int64_t rpc = (n + 4 * kComputeUnits - 1) / (4 * kComputeUnits);
-    if (rpc < 16) rpc = 16;
-    int32_t at = 0;
-    for (int32_t b = 0; b < batch; ++b) {
-        chunks->start[b] = at;
-        at += (int32_t)((items.start[b + 1] - items.start[b] + rpc - 1) / rpc);
-    }
-    for (int32_t b = batch; b <= P3D_MAX_BATCH; ++b) chunks->start[b] = at;
-    return rpc;
-}
 
 hipError_t launch_gated_norm(const NormArgs& a, p3d_dtype dt, const ItemTable& items,
                              hipStream_t s) {

@@ -110,10 +110,13 @@ __device__ __forceinline__ uint4 load_vec(const void* base, int64_t element, boo
                 : make_uint4(0, 0, 0, 0);
 }
 
+// `nt`: past the caches.
 template <typename T>
-__device__ __forceinline__ void store_vec(void* base, int64_t element, uint4 v) {
+__device__ __forceinline__ void store_vec(void* base, int64_t element, uint4 v, bool nt) {
     constexpr int E = 16 / Vec<T>::N;
-    *reinterpret_cast<uint4*>(reinterpret_cast<char*>(base) + element * E) = v;
+    uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<char*>(base) + element * E);
+    if (nt) store_nt16(p, v);
+    else *p = v;
 }
 
 // The forward call, and (turn = -1, no gamma) the gradient of the rotation
@@ -122,7 +125,7 @@ __device__ __forceinline__ void store_vec(void* base, int64_t element, uint4 v) 
 // chip and a workgroup's worth when there are not.
 template <typename T, int P2>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int head_slots,
-                                                          float turn) {
+                                                          float turn, bool nt) {
     constexpr int N = Vec<T>::N;
     constexpr int kSlots = kThreads / P2;
     extern __shared__ float2 table[];                    // [tokens of the workgroup][P]
@@ -140,13 +143,21 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int head
         const bool live = t < a.n && v * N < a.head_dim;
         float C[N], S[N];
         coefficients<N>(a, table + mine * P, v, P, turn, C, S);
+        // the next head's vectors are on their way while one is turned
+        const int64_t row = t * a.x_stride + v * N;
+        uint4 next_x = load_vec<T>(a.x, row + (int64_t)h0 * a.head_dim, live && h0 < a.heads);
+        uint4 next_g = load_vec<T>(a.gamma, (int64_t)h0 * a.head_dim + v * N,
+                                   a.gamma && live && h0 < a.heads);
         for (int h = h0; h < a.heads; h += head_slots) {
-            const int64_t col = (int64_t)h * a.head_dim + v * N;
-            float x[N];
-            Vec<T>::widen(load_vec<T>(a.x, t * a.x_stride + col, live), x);
+            float x[N], g[N];
+            Vec<T>::widen(next_x, x);
+            Vec<T>::widen(next_g, g);
+            const int64_t ahead = (int64_t)(h + head_slots) * a.head_dim;
+            const bool more = live && h + head_slots < a.heads;
+            next_x = load_vec<T>(a.x, row + ahead, more);
+            next_g = load_vec<T>(a.gamma, ahead + v * N, a.gamma && more);
             if (a.gamma) {
-                float q = 0.f, g[N];
-                Vec<T>::widen(load_vec<T>(a.gamma, col, live), g);
+                float q = 0.f;
 #pragma unroll
                 for (int e = 0; e < N; ++e) q += x[e] * x[e];
                 const float rstd = 1.0f / sqrtf(lane_sum<P2>(q) * inv_dim + a.eps);
@@ -154,7 +165,9 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int head
                 for (int e = 0; e < N; ++e) x[e] *= rstd * g[e];
             }
             turn_pairs<N>(a, x, v, P, C, S, heads_lds + slot * P2 * N, live);
-            if (live) store_vec<T>(a.out, t * a.out_stride + col, Vec<T>::narrow(x));
+            if (live)
+                store_vec<T>(a.out, t * a.out_stride + (int64_t)h * a.head_dim + v * N,
+                             Vec<T>::narrow(x), nt);
         }
     }
 }
@@ -166,7 +179,8 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int head
 template <typename T, int P2>
 __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a, int head_slots,
                                                                    int token_lanes, int batch,
-                                                                   int64_t tokens_per_chunk) {
+                                                                   int64_t tokens_per_chunk,
+                                                                   bool nt) {
     constexpr int N = Vec<T>::N;
     constexpr int kSlots = kThreads / P2;
     extern __shared__ float2 table[];                    // [batch * token_lanes][P]
@@ -185,6 +199,27 @@ __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a,
 #pragma unroll
         for (int e = 0; e < N; ++e) acc[k][e] = 0.f;
 
+    // The heads' scales stay in registers, packed; the next token's vectors
+    // are on their way while one token is worked on.
+    const bool mine = lane_t < token_lanes && v * N < a.head_dim;
+    uint4 gamma[kKeep], next_d[kKeep], next_x[kKeep];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k) {
+            const int h = head0 + k * head_slots;
+            const int64_t col = (int64_t)h * a.head_dim + v * N;
+            const bool there = mine && h < a.heads && t < end;
+            next_d[k] = load_vec<T>(a.dout, t * a.dout_stride + col, there);
+            next_x[k] = load_vec<T>(a.x, t * a.x_stride + col, there);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+        const int h = head0 + k * head_slots;
+        gamma[k] = load_vec<T>(a.gamma, (int64_t)h * a.head_dim + v * N, mine && h < a.heads);
+    }
+    fetch(first + lane_t);
+
     for (int64_t b0 = first; b0 < end; b0 += batch * token_lanes) {
         __syncthreads();
         fill_phases(a, b0, batch * token_lanes, P, table);
@@ -192,34 +227,40 @@ __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a,
         for (int u = 0; u < batch; ++u) {
             const int at = u * token_lanes + lane_t;
             const int64_t t = b0 + at;
-            const bool here = lane_t < token_lanes && t < end && v * N < a.head_dim;
+            const bool here = mine && t < end;
             float C[N], S[N];
             coefficients<N>(a, table + (lane_t < token_lanes ? at : 0) * P, v, P, -1.f, C, S);
+            float d[kKeep][N], x[kKeep][N];
+#pragma unroll
+            for (int k = 0; k < kKeep; ++k) {
+                Vec<T>::widen(next_d[k], d[k]);
+                Vec<T>::widen(next_x[k], x[k]);
+            }
+            fetch(t + token_lanes);
 #pragma unroll
             for (int k = 0; k < kKeep; ++k) {
                 const int h = head0 + k * head_slots;
                 const bool live = here && h < a.heads;
-                const int64_t col = (int64_t)h * a.head_dim + v * N;
-                float d[N], x[N], g[N];
-                Vec<T>::widen(load_vec<T>(a.dout, t * a.dout_stride + col, live), d);
-                Vec<T>::widen(load_vec<T>(a.x, t * a.x_stride + col, live), x);
-                Vec<T>::widen(load_vec<T>(a.gamma, col, live), g);
-                turn_pairs<N>(a, d, v, P, C, S, heads_lds + slot * P2 * N, live);
+                float g[N];
+                Vec<T>::widen(gamma[k], g);
+                turn_pairs<N>(a, d[k], v, P, C, S, heads_lds + slot * P2 * N, live);
                 float q = 0.f, dot = 0.f;
 #pragma unroll
-                for (int e = 0; e < N; ++e) q += x[e] * x[e];
+                for (int e = 0; e < N; ++e) q += x[k][e] * x[k][e];
                 const float rstd = 1.0f / sqrtf(lane_sum<P2>(q) * inv_dim + a.eps);
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    x[e] *= rstd;
-                    acc[k][e] += d[e] * x[e];
-                    d[e] *= g[e];
-                    dot += d[e] * x[e];
+                    x[k][e] *= rstd;
+                    acc[k][e] += d[k][e] * x[k][e];
+                    d[k][e] *= g[e];
+                    dot += d[k][e] * x[k][e];
                 }
                 dot = lane_sum<P2>(dot) * inv_dim;
 #pragma unroll
-                for (int e = 0; e < N; ++e) d[e] = rstd * (d[e] - x[e] * dot);
-                if (live) store_vec<T>(a.out, t * a.out_stride + col, Vec<T>::narrow(d));
+                for (int e = 0; e < N; ++e) d[k][e] = rstd * (d[k][e] - x[k][e] * dot);
+                if (live)
+                    store_vec<T>(a.out, t * a.out_stride + (int64_t)h * a.head_dim + v * N,
+                                 Vec<T>::narrow(d[k]), nt);
             }
         }
     }
@@ -291,13 +332,19 @@ Cut backward_cut(int64_t n, int heads, int head_dim, int per_vector) {
     c.token_lanes = slots / c.head_slots;
     c.head_blocks = (heads + kKeep * c.head_slots - 1) / (kKeep * c.head_slots);
     c.batch = c.token_lanes >= 16 ? 1 : 16 / c.token_lanes;
-    // about four workgroups per CU, at least 16 tokens each
+    // about four workgroups per CU, at least 8 tokens each
     const int64_t most = 4 * kComputeUnits / c.head_blocks > 0 ? 4 * kComputeUnits / c.head_blocks
                                                                : 1;
     c.tokens_per_chunk = (n + most - 1) / most;
-    if (c.tokens_per_chunk < 16) c.tokens_per_chunk = 16;
+    if (c.tokens_per_chunk < 8) c.tokens_per_chunk = 8;
     c.chunks = (int)((n + c.tokens_per_chunk - 1) / c.tokens_per_chunk);
     return c;
+}
+
+// Results go past the caches where the call's tensors do not fit the 256 MB of
+// last-level cache anyway, as those of the gated norm do.
+bool past_caches(const RotaryArgs& a, int planes, int bytes) {
+    return a.n * a.heads * a.head_dim * planes * bytes > (int64_t(256) << 20);
 }
 
 template <typename T, int P2>
@@ -310,7 +357,8 @@ hipError_t forward_as(const RotaryArgs& a, float turn, hipStream_t s) {
     const size_t lds = (size_t)tokens * a.axes * a.pairs * sizeof(float2);
     // (a launch holds under 2^32 threads)
     const int64_t blocks = std::min<int64_t>((a.n + tokens - 1) / tokens, int64_t(1) << 22);
-    rotary_kernel<T, P2><<<dim3((unsigned)blocks), dim3(kThreads), lds, s>>>(a, head_slots, turn);
+    rotary_kernel<T, P2><<<dim3((unsigned)blocks), dim3(kThreads), lds, s>>>(
+        a, head_slots, turn, past_caches(a, 2, 16 / Vec<T>::N));
     return hipGetLastError();
 }
 
@@ -319,7 +367,8 @@ hipError_t backward_as(const RotaryArgs& a, const Cut& c, hipStream_t s) {
     const size_t lds = (size_t)c.batch * c.token_lanes * a.axes * a.pairs * sizeof(float2);
     rotary_backward_kernel<T, P2>
         <<<dim3((unsigned)c.chunks, (unsigned)c.head_blocks), dim3(kThreads), lds, s>>>(
-            a, c.head_slots, c.token_lanes, c.batch, c.tokens_per_chunk);
+            a, c.head_slots, c.token_lanes, c.batch, c.tokens_per_chunk,
+            past_caches(a, 3, 16 / Vec<T>::N));
     return hipGetLastError();
 }
 
