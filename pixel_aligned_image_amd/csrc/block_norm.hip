@@ -396,6 +396,7 @@ __global__ __launch_bounds__(kJoinCols* kJoinLanes) void norm_join_kernel(NormAr
     const int64_t D = a.dim;
     float s[3] = {0.f, 0.f, 0.f};
     if (c < D) {
+#pragma unroll 4
         for (int q = chunks.start[item] + lane; q < chunks.start[item + 1]; q += kJoinLanes) {
             const float* p = a.partial + q * 3 * D + c;
 #pragma unroll

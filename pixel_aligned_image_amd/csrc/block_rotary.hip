@@ -289,7 +289,7 @@ __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a,
     }
 }
 
-constexpr int kJoinCols = 32, kJoinLanes = 32;
+constexpr int kJoinCols = 16, kJoinLanes = 64;
 
 __global__ __launch_bounds__(kJoinCols* kJoinLanes) void rotary_join_kernel(const float* partial,
                                                                             int chunks,
@@ -300,6 +300,7 @@ __global__ __launch_bounds__(kJoinCols* kJoinLanes) void rotary_join_kernel(cons
     const int c = blockIdx.x * kJoinCols + col;
     float s = 0.f;
     if (c < width)
+#pragma unroll 4
         for (int q = lane; q < chunks; q += kJoinLanes) s += partial[(int64_t)q * width + c];
     part[lane][col] = s;
     __syncthreads();
@@ -332,11 +333,11 @@ Cut backward_cut(int64_t n, int heads, int head_dim, int per_vector) {
     c.token_lanes = slots / c.head_slots;
     c.head_blocks = (heads + kKeep * c.head_slots - 1) / (kKeep * c.head_slots);
     c.batch = c.token_lanes >= 16 ? 1 : 16 / c.token_lanes;
-    // about four workgroups per CU, at least 8 tokens each
+    // about four workgroups per CU, at least 16 tokens each
     const int64_t most = 4 * kComputeUnits / c.head_blocks > 0 ? 4 * kComputeUnits / c.head_blocks
                                                                : 1;
     c.tokens_per_chunk = (n + most - 1) / most;
-    if (c.tokens_per_chunk < 8) c.tokens_per_chunk = 8;
+    if (c.tokens_per_chunk < 16) c.tokens_per_chunk = 16;
     c.chunks = (int)((n + c.tokens_per_chunk - 1) / c.tokens_per_chunk);
     return c;
 }
