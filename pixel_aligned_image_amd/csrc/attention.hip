@@ -14,7 +14,8 @@
 //
 // Where the row tiles do not fill the chip's last round the keys of the last
 // ones are cut into parts, each of which leaves (m, l, O) in the workspace,
-// joined by combine_kernel.
+// joined by combine_kernel. Two cases have kernels of their own: items of few
+// rows (single tokens), and items of few keys (global tokens).
 #include <algorithm>
 #include <type_traits>
 
@@ -35,11 +36,12 @@ constexpr int kMostParts = 64;           // a wave joins them, one lane each
 
 struct FwdArgs {
     AttnArgs a;
-    ItemTable tiles;                     // first row tile of every item
+    ItemTable tiles;                     // first row tile (single: part) of every item
     Group group;
     int whole, parts;                    // units run whole; parts of every later one
-    float* part_o;                       // [(unit - whole) * parts + part][rows][head_dim]
-    float2* part_ml;                     // [(unit - whole) * parts + part][rows]
+    int share;                           // single: keys of a part
+    float* part_o;                       // [slot][rows of a tile][head_dim]
+    float2* part_ml;                     // [slot][rows of a tile]
 };
 
 // A unit of the launch: one row tile of one key head. Tiles of an item run
@@ -51,18 +53,26 @@ struct Unit {
     uint32_t row0, rows;                 // first row of the tile, rows of the item
 
     __device__ __forceinline__ Unit(const FwdArgs& f, int unit, int per_tile) {
-        const AttnArgs& a = f.a;
-        const int tile = unit / a.kv_heads;
-        kv_head = unit - tile * a.kv_heads;
-        item = item_of_tile(f.tiles, a.batch, tile);
-        const int tiles = f.tiles.start[item + 1] - f.tiles.start[item];
-        const int nth = tile - f.tiles.start[item];
-        row0 = (uint32_t)(a.causal ? tiles - 1 - nth : nth) * per_tile;
+        const int tile = unit / f.a.kv_heads;
+        const int it = item_of_tile(f.tiles, f.a.batch, tile);
+        const int tiles = f.tiles.start[it + 1] - f.tiles.start[it];
+        const int nth = tile - f.tiles.start[it];
+        set(f.a, it, unit - tile * f.a.kv_heads, f.group.size,
+            (uint32_t)(f.a.causal ? tiles - 1 - nth : nth) * per_tile);
+    }
+    __device__ __forceinline__ Unit(const AttnArgs& a, int it, int head, int group) {
+        set(a, it, head, group, 0);
+    }
+    __device__ __forceinline__ void set(const AttnArgs& a, int it, int head, int group,
+                                        uint32_t first) {
+        item = it;
+        kv_head = head;
+        row0 = first;
         q0 = a.q_items.start[item];
         nq = a.q_items.start[item + 1] - q0;
         k0 = a.k_items.start[item];
         nk = a.k_items.start[item + 1] - k0;
-        rows = (uint32_t)nq * f.group.size;
+        rows = (uint32_t)nq * group;
     }
 };
 
@@ -408,9 +418,12 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int chunks = a.head_dim >> 3;
-    int which;
-    const int unit = unit_of(f, blockIdx.x, which);
-    const Unit u(f, unit, kSingleRows);
+    // the same number of keys for every workgroup, however long the items are
+    const int nth = blockIdx.x / a.kv_heads;
+    const int item = item_of_tile(f.tiles, a.batch, nth);
+    const int which = nth - f.tiles.start[item];
+    const bool split = f.tiles.start[item + 1] - f.tiles.start[item] > 1;
+    const Unit u(a, item, blockIdx.x - nth * a.kv_heads, f.group.size);
     const int kv_head = u.kv_head, q0 = u.q0, nq = u.nq, k0 = u.k0, nk = u.nk;
     const uint32_t row = lane & 31, rows = u.rows;
     const bool live = row < rows;
@@ -425,11 +438,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
                                                   head * a.head_dim),
                    live, chunks, lane);
     settle(q);
-    const int parts = which < 0 ? 1 : f.parts;
-    int share = (nk + parts - 1) / parts;
-    share = (share + kSingleKeys - 1) / kSingleKeys * kSingleKeys;
-    const int begin = (int)min((int64_t)max(which, 0) * share, (int64_t)nk);
-    const int end = (int)min((int64_t)begin + share, (int64_t)nk);
+    const int begin = (int)min((int64_t)which * f.share, (int64_t)nk);
+    const int end = (int)min((int64_t)begin + f.share, (int64_t)nk);
     const int limit = a.causal && live ? min(end, (int)token + nk - nq + 1) : end;
     const int all_see = __builtin_amdgcn_readfirstlane(limit);
     const float c = a.scale * kLog2e;
@@ -511,9 +521,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
     st.m = m;
     const int64_t out_row = (int64_t)(q0 + (int)token) * a.heads + head;
     if (!live) return;
-    if (which >= 0) {
-        store_part<HD>(f, st,
-                       ((int64_t)(unit - f.whole) * f.parts + which) * kSingleRows + row, l, lane);
+    if (split) {
+        store_part<HD>(f, st, (int64_t)blockIdx.x * kSingleRows + row, l, lane);
         return;
     }
     if (a.lse && lane < 32)
@@ -534,35 +543,153 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
         }
 }
 
+// Items of at most 32 NB keys (global tokens): keys and values lie in LDS once,
+// and every wave takes row tiles of its own, each one's queries loaded under
+// the one before. Bound by q in and out out; no barrier stands in the loop, and
+// three workgroups share a CU (two with 64 keys).
+template <int HD, int NB>
+__global__ __launch_bounds__(64 * kWaves, NB == 1 ? 3 : 2) void attention_few_kernel(
+    FwdArgs f, int tiles_per_wave) {
+    using T = Tile<HD>;
+    __shared__ uint4 kt[32 * NB * T::kChunks];
+    __shared__ uint4 vt[32 * NB * T::kChunks];
+    __shared__ uint4 stages[kWaves][32 * T::kChunks];
+    const AttnArgs& a = f.a;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int chunks = a.head_dim >> 3;
+    const Unit u(f, blockIdx.x, kRows * tiles_per_wave);
+    const int kv_head = u.kv_head, q0 = u.q0, nq = u.nq, k0 = u.k0, nk = u.nk;
+
+    if (chunks < T::kChunks || nk == 0) {    // (without keys, zeros stand for them)
+        T::clear(kt, 32 * NB, 64 * kWaves, threadIdx.x);
+        T::clear(vt, 32 * NB, 64 * kWaves, threadIdx.x);
+        __syncthreads();
+    }
+    const uint16_t* kb = reinterpret_cast<const uint16_t*>(a.k) + (int64_t)k0 * a.k_stride +
+                         kv_head * a.head_dim;
+    const uint16_t* vb = reinterpret_cast<const uint16_t*>(a.v) + (int64_t)k0 * a.v_stride +
+                         kv_head * a.head_dim;
+    if (nk > 0) {
+        T::template load<32 * NB, kWaves>(kt, wave, lane, chunks, [&](int r) {
+            return reinterpret_cast<const uint4*>(kb + (int64_t)min(r, nk - 1) * a.k_stride);
+        });
+        T::template load<32 * NB, kWaves>(vt, wave, lane, chunks, [&](int r) {
+            return reinterpret_cast<const uint4*>(vb + (int64_t)min(r, nk - 1) * a.v_stride);
+        });
+    }
+    const float c = a.scale * kLog2e;
+    bf16x8_t next[T::kSteps];
+    auto fetch = [&](uint32_t row) {
+        const bool live = row < u.rows;
+        uint32_t token, member;
+        f.group.split(live ? row : 0, token, member);
+        load_query<HD>(next,
+                       reinterpret_cast<const uint4*>(
+                           reinterpret_cast<const uint16_t*>(a.q) +
+                           (int64_t)(q0 + (int)token) * a.q_stride +
+                           (kv_head * (int)f.group.size + (int)member) * a.head_dim),
+                       live, chunks, lane);
+    };
+    uint32_t row0 = u.row0 + 32 * wave;
+    const uint32_t past = min(u.row0 + kRows * tiles_per_wave, u.rows);
+    fetch(row0 + (lane & 31));
+    tile_barrier();
+    for (; row0 < past; row0 += kRows) {
+        bf16x8_t q[T::kSteps];
+#pragma unroll
+        for (int k = 0; k < T::kSteps; ++k) q[k] = next[k];
+        fetch(row0 + kRows < past ? row0 + kRows + (lane & 31) : u.rows);
+        const uint32_t row = row0 + (lane & 31);
+        const bool live = row < u.rows;
+        uint32_t token, member;
+        f.group.split(live ? row : 0, token, member);
+        const int limit = a.causal && live ? min(nk, (int)token + nk - nq + 1) : nk;
+
+        const uint32_t k_at = T::row_base(kt, lane);
+        f32x16 s[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) s[b] = zero16();
+#pragma unroll
+        for (int k = 0; k < T::kSteps; ++k)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) s[b] = mfma(T::row_frag(k_at, 32 * b, k), q[k], s[b]);
+        Softmax<HD> st;
+        st.init();
+        st.mask(s, 0, limit, lane);
+        const float top = st.top(s);
+        const float base = top == -INFINITY ? 0.f : top * c;
+        bf16x8_t p[2 * NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[b][i] = __builtin_amdgcn_exp2f(s[b][i] * c - base);
+                st.l += s[b][i];
+            }
+            p[2 * b] = acc_frag(s[b], 0);
+            p[2 * b + 1] = acc_frag(s[b], 1);
+        }
+        const uint32_t v_at = T::tr_base(vt, lane);
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t)
+#pragma unroll
+            for (int d = 0; d < T::kBlocks; ++d)
+                st.o[d] = mfma(T::tr_frag(v_at, 16 * t, d), p[t], st.o[d]);
+        float own;
+        const float other = other_half(st.l, own);
+        const float l = own + other;
+        if (a.lse && live && lane < 32)
+            a.lse[(int64_t)(q0 + (int)token) * a.heads + kv_head * (int)f.group.size + member] =
+                l == 0.f ? -INFINITY : top * a.scale + kLn2 * __builtin_amdgcn_logf(l);
+        store_rows<HD>(st.o, l == 0.f ? 0.f : 1.0f / l, stages[wave], chunks, lane,
+                       [&](int r) -> uint4* {
+            const uint32_t at = row0 + r;
+            if (at >= u.rows) return nullptr;
+            uint32_t t, m;
+            f.group.split(at, t, m);
+            return reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) +
+                                            (int64_t)(q0 + (int)t) * a.out_stride +
+                                            (kv_head * (int)f.group.size + (int)m) * a.head_dim);
+        });
+    }
+}
+
 // Joins the parts of a row, one wave per row: lane p weighs part p, then each
 // half adds every other part, 4 columns a lane.
-__global__ __launch_bounds__(256) void combine_kernel(FwdArgs f, int per_tile) {
+__global__ __launch_bounds__(256) void combine_kernel(FwdArgs f, int per_tile, bool single) {
     const AttnArgs& a = f.a;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tail = blockIdx.x * 4 / per_tile;
     const int r = (blockIdx.x * 4 + wave) % per_tile;
-    const Unit u(f, f.whole + tail, per_tile);
+    const Unit u = single ? Unit(a, tail / a.kv_heads, tail % a.kv_heads, f.group.size)
+                          : Unit(f, f.whole + tail, per_tile);
     const uint32_t row = u.row0 + r;
     if (row >= u.rows) return;
     const float c = a.scale * kLog2e;
-    const int64_t first = (int64_t)tail * f.parts * per_tile + r;
-    const float2 ml = lane < f.parts ? f.part_ml[first + (int64_t)lane * per_tile]
-                                     : make_float2(-INFINITY, 0.f);
+    // a part's slot: the parts of a unit in turn, or (single) of the key heads
+    const int before = f.tiles.start[u.item];
+    const int parts = single ? f.tiles.start[u.item + 1] - before : f.parts;
+    if (single && parts == 1) return;
+    const int64_t slot = single ? (int64_t)before * a.kv_heads + u.kv_head
+                                : (int64_t)tail * f.parts;
+    const int64_t first = slot * per_tile + r, step = (single ? a.kv_heads : 1) * per_tile;
+    const float2 ml = lane < parts ? f.part_ml[first + lane * step]
+                                   : make_float2(-INFINITY, 0.f);
     const float m = lane_max(ml.x);
     const float weight = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((ml.x - m) * c);
     const float l = lane_sum<64>(ml.y * weight);
     const int d = (lane & 31) * 4;
     const float* from = f.part_o + first * a.head_dim + (d < a.head_dim ? d : 0);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p = 0; p < f.parts; p += 8) {
+    for (int p = 0; p < parts; p += 8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {            // (four loads in flight)
-            const int mine = p + 2 * i + h, there = min(mine, f.parts - 1);
+            const int mine = p + 2 * i + h, there = min(mine, parts - 1);
             const float other = __shfl(weight, there);
-            const float w = mine < f.parts ? other : 0.f;
-            const float4 v = *reinterpret_cast<const float4*>(
-                from + (int64_t)there * per_tile * a.head_dim);
+            const float w = mine < parts ? other : 0.f;
+            const float4 v = *reinterpret_cast<const float4*>(from + there * step * a.head_dim);
             o.x += v.x * w;
             o.y += v.y * w;
             o.z += v.z * w;
@@ -590,11 +717,30 @@ __global__ __launch_bounds__(256) void combine_kernel(FwdArgs f, int per_tile) {
 
 template <int HD>
 hipError_t forward_as(const FwdArgs& f, const AttnPlan& p, int blocks, hipStream_t s) {
+    const dim3 grid((unsigned)blocks), threads(64 * kWaves);
     if (p.single)
-        attention_single_kernel<HD><<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(f);
+        attention_single_kernel<HD><<<grid, threads, 0, s>>>(f);
+    else if (p.few == 1)
+        attention_few_kernel<HD, 1><<<grid, threads, 0, s>>>(f, p.per_tile / kRows);
+    else if (p.few == 2)
+        attention_few_kernel<HD, 2><<<grid, threads, 0, s>>>(f, p.per_tile / kRows);
     else
-        attention_kernel<HD><<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(f);
+        attention_kernel<HD><<<grid, threads, 0, s>>>(f);
     return hipGetLastError();
+}
+
+// Parts of the single-token kernel, of `share` keys each: one per CU where the
+// keys are long enough (its tiles fill a CU's LDS), at least 256 keys.
+int single_parts(const AttnArgs& a, int64_t share, ItemTable* start) {
+    int64_t at = 0;
+    for (int b = 0; b < a.batch; ++b) {
+        start->start[b] = (int32_t)at;
+        const int64_t keys = a.k_items.start[b + 1] - a.k_items.start[b];
+        const bool rows = a.q_items.start[b + 1] > a.q_items.start[b];
+        at += rows ? std::max<int64_t>(1, (keys + share - 1) / share) : 0;
+    }
+    for (int b = a.batch; b <= P3D_MAX_BATCH; ++b) start->start[b] = (int32_t)at;
+    return (int)at;
 }
 
 }  // namespace
@@ -613,24 +759,46 @@ AttnPlan attention_plan(const AttnArgs& a) {
             most_rows, (int64_t)(a.q_items.start[b + 1] - a.q_items.start[b]) * group);
         most_keys = std::max<int64_t>(most_keys, a.k_items.start[b + 1] - a.k_items.start[b]);
     }
+    const size_t row_bytes = a.head_dim * sizeof(float) + sizeof(float2);
+    ItemTable tiles;
     p.single = most_rows <= kSingleRows;
     p.per_tile = p.single ? kSingleRows : kRows;
-    ItemTable tiles;
-    cut_items(a.q_items, a.batch, group, p.per_tile, &tiles);
-    p.units = tiles.start[a.batch] * a.kv_heads;
-    // workgroups a CU holds: by LDS (single), by LDS and registers
-    const int slots = kComputeUnits * (p.single ? 1 : a.head_dim <= 64 ? 3 : 2);
-    p.whole = a.causal && p.units >= slots ? p.units : p.units / slots * slots;
     p.parts = 1;
-    if (p.whole < p.units)
-        p.parts = (int32_t)std::min<int64_t>(
-            {slots / (p.units - p.whole), most_keys / 256, kMostParts});
-    if (p.parts <= 1) {
-        p.whole = p.units;
-        p.parts = 1;
+    p.forward_bytes = 256;
+    if (p.single) {
+        cut_items(a.q_items, a.batch, group, p.per_tile, &tiles);
+        p.units = tiles.start[a.batch] * a.kv_heads;
+        int64_t share = std::max<int64_t>(
+            256, ((int64_t)a.k_items.start[a.batch] * a.kv_heads / kComputeUnits + 127) / 128 * 128);
+        share = std::max(share, (most_keys / kMostParts + 128) / 128 * 128);
+        while (single_parts(a, share, &tiles) * a.kv_heads > std::max(p.units, kComputeUnits))
+            share += (share / 16 + 127) / 128 * 128;
+        p.share = (int32_t)share;
+        const int parts = single_parts(a, share, &tiles) * a.kv_heads;
+        p.whole = parts == p.units ? p.units : 0;
+        if (p.whole == 0) p.forward_bytes += (size_t)parts * p.per_tile * row_bytes;
+    } else {
+        cut_items(a.q_items, a.batch, group, p.per_tile, &tiles);
+        if (most_keys <= 64) {
+            // about four rounds of workgroups
+            p.few = most_keys <= 32 ? 1 : 2;
+            const int64_t all = (int64_t)tiles.start[a.batch] * a.kv_heads;
+            p.per_tile *= (int32_t)std::max<int64_t>(1, all / (12 * kComputeUnits));
+            cut_items(a.q_items, a.batch, group, p.per_tile, &tiles);
+        }
+        p.units = tiles.start[a.batch] * a.kv_heads;
+        // workgroups a CU holds, by LDS and registers
+        const int slots = kComputeUnits * (a.head_dim <= 64 ? 3 : 2);
+        p.whole = p.few || (a.causal && p.units >= slots) ? p.units : p.units / slots * slots;
+        if (p.whole < p.units)
+            p.parts = (int32_t)std::min<int64_t>(
+                {slots / (p.units - p.whole), most_keys / 256, kMostParts});
+        if (p.parts <= 1) {
+            p.whole = p.units;
+            p.parts = 1;
+        }
+        p.forward_bytes += (size_t)(p.units - p.whole) * p.parts * p.per_tile * row_bytes;
     }
-    p.forward_bytes = 256 + (size_t)(p.units - p.whole) * p.parts * p.per_tile *
-                                (a.head_dim * sizeof(float) + sizeof(float2));
     plan_attention_backward(a, &p);
     return p;
 }
@@ -640,19 +808,23 @@ hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* ws, hipS
     FwdArgs f;
     f.a = a;
     f.group = group_of(a);
-    cut_items(a.q_items, a.batch, f.group.size, p.per_tile, &f.tiles);
     f.whole = p.whole;
     f.parts = p.parts;
+    f.share = p.share;
     const int tail = p.units - p.whole;
+    int slots = tail * p.parts;
+    if (p.single) slots = single_parts(a, p.share, &f.tiles) * a.kv_heads;
+    else cut_items(a.q_items, a.batch, f.group.size, p.per_tile, &f.tiles);
     f.part_o = static_cast<float*>(ws);
-    f.part_ml = reinterpret_cast<float2*>(f.part_o +
-                                          (int64_t)tail * p.parts * p.per_tile * a.head_dim);
-    const int blocks = p.whole + tail * p.parts;
+    f.part_ml = reinterpret_cast<float2*>(f.part_o + (int64_t)slots * p.per_tile * a.head_dim);
+    const int blocks = p.single ? slots : p.whole + slots;
     const hipError_t e = a.head_dim <= 64   ? forward_as<64>(f, p, blocks, s)
                          : a.head_dim <= 96 ? forward_as<96>(f, p, blocks, s)
                                             : forward_as<128>(f, p, blocks, s);
     if (e != hipSuccess || tail == 0) return e;
-    combine_kernel<<<dim3((unsigned)(tail * (p.per_tile / 4))), dim3(256), 0, s>>>(f, p.per_tile);
+    const int joined = p.single ? a.batch * a.kv_heads : tail;
+    combine_kernel<<<dim3((unsigned)(joined * (p.per_tile / 4))), dim3(256), 0, s>>>(
+        f, p.per_tile, p.single);
     return hipGetLastError();
 }
 

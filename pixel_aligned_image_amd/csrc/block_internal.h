@@ -154,6 +154,8 @@ struct AttnArgs {
 // How a forward or backward launch is cut (host-only; sizes the workspace).
 struct AttnPlan {
     bool single;                // every item's rows fit one wave: the waves split the keys
+    int32_t share;              // single: keys of a part
+    int32_t few;                // every item has at most 32 few keys (1 or 2): they stay in LDS
     int32_t per_tile;           // query rows of a tile
     int32_t units;              // row tiles x key heads
     int32_t whole, parts;       // units run whole; parts of the keys of every later one
