@@ -543,27 +543,31 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
         }
 }
 
-// Items of at most 32 NB keys (global tokens): keys and values lie in LDS once,
-// and every wave takes row tiles of its own, each one's queries loaded under
-// the one before. Bound by q in and out out; no barrier stands in the loop, and
-// three workgroups share a CU (two with 64 keys).
+// Items of at most 32 NB keys (global tokens): no loop at all. Bound by q in
+// and out out, which both go through the wave's LDS tile in whole rows: with 16
+// bytes of every row per instruction, as the operands lie, the lines of 32 rows
+// do not survive in L1 (100,000 tokens of 12 heads over 5 keys: 156 us, and 121
+// through LDS). Several row tiles per wave, the next one's queries loaded under
+// one, were slower (129 us with 3, 144 with 6) than more workgroups.
 template <int HD, int NB>
-__global__ __launch_bounds__(64 * kWaves, NB == 1 ? 3 : 2) void attention_few_kernel(
-    FwdArgs f, int tiles_per_wave) {
+__global__ __launch_bounds__(64 * kWaves, NB == 1 ? 3 : 2) void attention_few_kernel(FwdArgs f,
+                                                                                     bool nt) {
     using T = Tile<HD>;
     __shared__ uint4 kt[32 * NB * T::kChunks];
     __shared__ uint4 vt[32 * NB * T::kChunks];
-    __shared__ uint4 stages[kWaves][32 * T::kChunks];
+    __shared__ uint4 rows_lds[kWaves][32 * T::kChunks];
     const AttnArgs& a = f.a;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int chunks = a.head_dim >> 3;
-    const Unit u(f, blockIdx.x, kRows * tiles_per_wave);
+    const Unit u(f, blockIdx.x, kRows);
     const int kv_head = u.kv_head, q0 = u.q0, nq = u.nq, k0 = u.k0, nk = u.nk;
+    const int head0 = kv_head * (int)f.group.size;
 
     if (chunks < T::kChunks || nk == 0) {    // (without keys, zeros stand for them)
         T::clear(kt, 32 * NB, 64 * kWaves, threadIdx.x);
         T::clear(vt, 32 * NB, 64 * kWaves, threadIdx.x);
+        T::clear(rows_lds[0], 32 * kWaves, 64 * kWaves, threadIdx.x);
         __syncthreads();
     }
     const uint16_t* kb = reinterpret_cast<const uint16_t*>(a.k) + (int64_t)k0 * a.k_stride +
@@ -579,80 +583,74 @@ __global__ __launch_bounds__(64 * kWaves, NB == 1 ? 3 : 2) void attention_few_ke
         });
     }
     const float c = a.scale * kLog2e;
-    bf16x8_t next[T::kSteps];
-    auto fetch = [&](uint32_t row) {
-        const bool live = row < u.rows;
+    // an element's place in q or out by its row
+    auto place = [&](uint32_t row, int64_t stride) {
         uint32_t token, member;
-        f.group.split(live ? row : 0, token, member);
-        load_query<HD>(next,
-                       reinterpret_cast<const uint4*>(
-                           reinterpret_cast<const uint16_t*>(a.q) +
-                           (int64_t)(q0 + (int)token) * a.q_stride +
-                           (kv_head * (int)f.group.size + (int)member) * a.head_dim),
-                       live, chunks, lane);
+        f.group.split(row, token, member);
+        return (int64_t)(q0 + (int)token) * stride + (head0 + (int)member) * a.head_dim;
     };
-    uint32_t row0 = u.row0 + 32 * wave;
-    const uint32_t past = min(u.row0 + kRows * tiles_per_wave, u.rows);
-    fetch(row0 + (lane & 31));
-    tile_barrier();
-    for (; row0 < past; row0 += kRows) {
-        bf16x8_t q[T::kSteps];
-#pragma unroll
-        for (int k = 0; k < T::kSteps; ++k) q[k] = next[k];
-        fetch(row0 + kRows < past ? row0 + kRows + (lane & 31) : u.rows);
-        const uint32_t row = row0 + (lane & 31);
-        const bool live = row < u.rows;
-        uint32_t token, member;
-        f.group.split(live ? row : 0, token, member);
-        const int limit = a.causal && live ? min(nk, (int)token + nk - nq + 1) : nk;
-
-        const uint32_t k_at = T::row_base(kt, lane);
-        f32x16 s[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) s[b] = zero16();
-#pragma unroll
-        for (int k = 0; k < T::kSteps; ++k)
-#pragma unroll
-            for (int b = 0; b < NB; ++b) s[b] = mfma(T::row_frag(k_at, 32 * b, k), q[k], s[b]);
-        Softmax<HD> st;
-        st.init();
-        st.mask(s, 0, limit, lane);
-        const float top = st.top(s);
-        const float base = top == -INFINITY ? 0.f : top * c;
-        bf16x8_t p[2 * NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[b][i] = __builtin_amdgcn_exp2f(s[b][i] * c - base);
-                st.l += s[b][i];
-            }
-            p[2 * b] = acc_frag(s[b], 0);
-            p[2 * b + 1] = acc_frag(s[b], 1);
-        }
-        const uint32_t v_at = T::tr_base(vt, lane);
-#pragma unroll
-        for (int t = 0; t < 2 * NB; ++t)
-#pragma unroll
-            for (int d = 0; d < T::kBlocks; ++d)
-                st.o[d] = mfma(T::tr_frag(v_at, 16 * t, d), p[t], st.o[d]);
-        float own;
-        const float other = other_half(st.l, own);
-        const float l = own + other;
-        if (a.lse && live && lane < 32)
-            a.lse[(int64_t)(q0 + (int)token) * a.heads + kv_head * (int)f.group.size + member] =
-                l == 0.f ? -INFINITY : top * a.scale + kLn2 * __builtin_amdgcn_logf(l);
-        store_rows<HD>(st.o, l == 0.f ? 0.f : 1.0f / l, stages[wave], chunks, lane,
-                       [&](int r) -> uint4* {
-            const uint32_t at = row0 + r;
-            if (at >= u.rows) return nullptr;
-            uint32_t t, m;
-            f.group.split(at, t, m);
-            return reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) +
-                                            (int64_t)(q0 + (int)t) * a.out_stride +
-                                            (kv_head * (int)f.group.size + (int)m) * a.head_dim);
+    const uint32_t row0 = u.row0 + 32 * wave;
+    uint4* tile = rows_lds[wave];
+    if (row0 < u.rows)                       // rows past the last repeat it
+        T::template load<32, 1>(tile, 0, lane, chunks, [&](int r) {
+            return reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
+                                                  place(min(row0 + r, u.rows - 1), a.q_stride));
         });
+    tile_barrier();
+    if (row0 >= u.rows) return;
+    const uint32_t q_at = T::row_base(tile, lane);
+    bf16x8_t q[T::kSteps];
+#pragma unroll
+    for (int k = 0; k < T::kSteps; ++k) q[k] = T::row_frag(q_at, 0, k);
+    const uint32_t row = row0 + (lane & 31);
+    const bool live = row < u.rows;
+    uint32_t token, member;
+    f.group.split(live ? row : 0, token, member);
+    const int limit = a.causal && live ? min(nk, (int)token + nk - nq + 1) : nk;
+
+    const uint32_t k_at = T::row_base(kt, lane);
+    f32x16 s[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) s[b] = zero16();
+#pragma unroll
+    for (int k = 0; k < T::kSteps; ++k)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) s[b] = mfma(T::row_frag(k_at, 32 * b, k), q[k], s[b]);
+    Softmax<HD> st;
+    st.init();
+    st.mask(s, 0, limit, lane);
+    const float top = st.top(s);
+    const float base = top == -INFINITY ? 0.f : top * c;
+    bf16x8_t p[2 * NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[b][i] = __builtin_amdgcn_exp2f(s[b][i] * c - base);
+            st.l += s[b][i];
+        }
+        p[2 * b] = acc_frag(s[b], 0);
+        p[2 * b + 1] = acc_frag(s[b], 1);
     }
+    const uint32_t v_at = T::tr_base(vt, lane);
+#pragma unroll
+    for (int t = 0; t < 2 * NB; ++t)
+#pragma unroll
+        for (int d = 0; d < T::kBlocks; ++d)
+            st.o[d] = mfma(T::tr_frag(v_at, 16 * t, d), p[t], st.o[d]);
+    float own;
+    const float other = other_half(st.l, own);
+    const float l = own + other;
+    stage_rows<HD>(st.o, l == 0.f ? 0.f : 1.0f / l, tile, chunks, lane);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (a.lse && live && lane < 32)
+        a.lse[(int64_t)(q0 + (int)token) * a.heads + head0 + member] =
+            l == 0.f ? -INFINITY : top * a.scale + kLn2 * __builtin_amdgcn_logf(l);
+    write_rows<HD>(tile, chunks, lane, [&](int r) -> uint4* {
+        if (row0 + r >= u.rows) return nullptr;
+        return reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) +
+                                        place(row0 + r, a.out_stride));
+    }, nt);
 }
 
 // Joins the parts of a row, one wave per row: lane p weighs part p, then each
@@ -718,12 +716,15 @@ __global__ __launch_bounds__(256) void combine_kernel(FwdArgs f, int per_tile, b
 template <int HD>
 hipError_t forward_as(const FwdArgs& f, const AttnPlan& p, int blocks, hipStream_t s) {
     const dim3 grid((unsigned)blocks), threads(64 * kWaves);
+    // where q and out do not fit the last-level cache anyway, out goes past it
+    const int64_t moved = (int64_t)f.a.q_items.start[f.a.batch] * f.a.heads * f.a.head_dim * 4;
+    const bool nt = moved > (int64_t(256) << 20);
     if (p.single)
         attention_single_kernel<HD><<<grid, threads, 0, s>>>(f);
     else if (p.few == 1)
-        attention_few_kernel<HD, 1><<<grid, threads, 0, s>>>(f, p.per_tile / kRows);
+        attention_few_kernel<HD, 1><<<grid, threads, 0, s>>>(f, nt);
     else if (p.few == 2)
-        attention_few_kernel<HD, 2><<<grid, threads, 0, s>>>(f, p.per_tile / kRows);
+        attention_few_kernel<HD, 2><<<grid, threads, 0, s>>>(f, nt);
     else
         attention_kernel<HD><<<grid, threads, 0, s>>>(f);
     return hipGetLastError();
@@ -779,13 +780,7 @@ AttnPlan attention_plan(const AttnArgs& a) {
         if (p.whole == 0) p.forward_bytes += (size_t)parts * p.per_tile * row_bytes;
     } else {
         cut_items(a.q_items, a.batch, group, p.per_tile, &tiles);
-        if (most_keys <= 64) {
-            // about four rounds of workgroups
-            p.few = most_keys <= 32 ? 1 : 2;
-            const int64_t all = (int64_t)tiles.start[a.batch] * a.kv_heads;
-            p.per_tile *= (int32_t)std::max<int64_t>(1, all / (12 * kComputeUnits));
-            cut_items(a.q_items, a.batch, group, p.per_tile, &tiles);
-        }
+        p.few = most_keys <= 32 ? 1 : most_keys <= 64 ? 2 : 0;
         p.units = tiles.start[a.batch] * a.kv_heads;
         // workgroups a CU holds, by LDS and registers
         const int slots = kComputeUnits * (a.head_dim <= 64 ? 3 : 2);

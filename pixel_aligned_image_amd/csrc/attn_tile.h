@@ -266,11 +266,12 @@ __device__ __forceinline__ void settle(bf16x8_t (&q)[N]) {
     for (int k = 0; k < N; ++k) asm volatile("" : "+v"(q[k]));
 }
 
-// A finished tile's rows through LDS (32 rows of the tile layout) so that
-// whole rows go out in 16-byte pieces.
-template <int HD, typename Dst>
-__device__ __forceinline__ void store_rows(const f32x16 (&o)[Tile<HD>::kBlocks], float by,
-                                           uint4* stage, int chunks, int lane, Dst dst) {
+// A finished tile's rows go out through LDS (32 rows of the tile layout) so
+// that whole rows leave in 16-byte pieces: into LDS, and from there, row r to
+// dst(r) where that is not null (`nt`: past the caches).
+template <int HD>
+__device__ __forceinline__ void stage_rows(const f32x16 (&o)[Tile<HD>::kBlocks], float by,
+                                           uint4* stage, int chunks, int lane) {
     using T = Tile<HD>;
     const int r = lane & 31, h = lane >> 5;
     uint2* stage2 = reinterpret_cast<uint2*>(stage);
@@ -278,19 +279,37 @@ __device__ __forceinline__ void store_rows(const f32x16 (&o)[Tile<HD>::kBlocks],
     for (int b = 0; b < T::kBlocks; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            if (4 * b + j >= chunks) continue;
             uint2 v;
             v.x = pack_bf16x2(o[b][4 * j] * by, o[b][4 * j + 1] * by);
             v.y = pack_bf16x2(o[b][4 * j + 2] * by, o[b][4 * j + 3] * by);
             stage2[(r * T::kChunks + ((4 * b + j) ^ T::swizzle(r))) * 2 + h] = v;
         }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
+template <int HD, typename Dst>
+__device__ __forceinline__ void write_rows(const uint4* stage, int chunks, int lane, Dst dst,
+                                           bool nt = false) {
+    using T = Tile<HD>;
 #pragma unroll
     for (int i = 0; i < 32 * T::kChunks / 64; ++i) {
         const int at = i * 64 + lane;
         const int row = at / T::kChunks, c = at % T::kChunks;
         uint4* p = dst(row);
-        if (p && c < chunks) p[c] = stage[row * T::kChunks + (c ^ T::swizzle(row))];
+        if (p && c < chunks) {
+            const uint4 v = stage[row * T::kChunks + (c ^ T::swizzle(row))];
+            if (nt) store_nt16(p + c, v);
+            else p[c] = v;
+        }
     }
+}
+
+template <int HD, typename Dst>
+__device__ __forceinline__ void store_rows(const f32x16 (&o)[Tile<HD>::kBlocks], float by,
+                                           uint4* stage, int chunks, int lane, Dst dst) {
+    stage_rows<HD>(o, by, stage, chunks, lane);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    write_rows<HD>(stage, chunks, lane, dst);
 }
 
 // The group of query heads that share a key head.
