@@ -2,10 +2,10 @@
 // forward call's lse the probabilities are one exponential away from the
 // scores, P = exp(scale S - lse), so both kernels recompute them tile by tile:
 //
-//   rows kernel   D_i = dout_i . out_i and lse in the scores' unit, once
 //   dq kernel     a wave holds 32 query rows and walks the keys:
 //                 dS^T = P^T (V dO^T - D),  dQ^T += K^T dS^T
-//                 and on the way D_i = sum_j P_ij (dout_i . v_j)
+//                 with D_i = dout_i . out_i, and on the way sums up
+//                 D_i = sum_j P_ij (dout_i . v_j)
 //   dkv kernel    a wave holds 32 keys and walks the query rows, with that D:
 //                 dV^T += dO^T P,  dK^T += Q^T dS
 //
@@ -50,40 +50,6 @@ struct BwdArgs {
     float *part, *part2;                 // [splits][n * heads][head_dim]: dq, or dk and dv
     float* part_d;                       // [splits][nq * heads]
 };
-
-// What the score and dP products of every row start from: -lse / scale, so that
-// P = exp2(scale log2(e) (S - lse / scale)), and -D. 32 lanes per (token, head),
-// 4 columns a lane. A row that sees no key starts from -inf: its P is 0.
-__global__ __launch_bounds__(256) void rows_kernel(BwdArgs f, int64_t rows) {
-    const AttnArgs& a = f.a;
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        f.minus_lse[rows] = -INFINITY;
-        f.minus_d[rows] = 0.f;
-    }
-    const int d = (threadIdx.x & 31) * 4;
-    for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows;
-         row += (int64_t)gridDim.x * 8) {
-        const int64_t token = row / a.heads;
-        const int head = (int)(row - token * a.heads);
-        float s = 0.f;
-        if (d < a.head_dim) {
-            const uint2 x = *reinterpret_cast<const uint2*>(
-                reinterpret_cast<const uint16_t*>(a.dout) + token * a.dout_stride +
-                head * a.head_dim + d);
-            const uint2 y = *reinterpret_cast<const uint2*>(
-                reinterpret_cast<const uint16_t*>(a.out_in) + token * a.out_stride +
-                head * a.head_dim + d);
-            s = bf16lo(x.x) * bf16lo(y.x) + bf16hi(x.x) * bf16hi(y.x) +
-                bf16lo(x.y) * bf16lo(y.y) + bf16hi(x.y) * bf16hi(y.y);
-        }
-        s = lane_sum<32>(s);
-        if (d) continue;
-        const int64_t at = rows / a.heads * head + token;
-        const float l = a.lse_in[row];
-        f.minus_d[at] = -s;
-        f.minus_lse[at] = l == -INFINITY ? -INFINITY : -l / a.scale;
-    }
-}
 
 // A held tile's binary32 sums to the workspace; `row` counts (token, head).
 template <int HD>
@@ -169,10 +135,41 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
                                                   (int64_t)(q0 + (int)token) * a.dout_stride +
                                                   head * a.head_dim),
                    live, chunks, lane);
-    const int64_t stat = (int64_t)a.q_items.start[a.batch] * head + q0 + (int)token;
+    // What the score and dP products of the row start from in the dkv kernel:
+    // -lse / scale, so that P = exp2(scale log2(e) (S - lse / scale)), and -D. A
+    // row that sees no key starts from -inf: its P is 0. Here D = dout . out.
     const float c = a.scale * kLog2e;
-    float minus_lse2 = live ? f.minus_lse[stat] * c : -INFINITY;
-    float minus_d = live ? f.minus_d[stat] : 0.f;
+    const int64_t stat = (int64_t)a.q_items.start[a.batch] * head + q0 + (int)token;
+    float lse = -INFINITY, minus_d = 0.f;
+    if (live) {
+        lse = a.lse_in[(int64_t)(q0 + (int)token) * a.heads + head];
+        const uint4* o = reinterpret_cast<const uint4*>(
+            reinterpret_cast<const uint16_t*>(a.out_in) + (int64_t)(q0 + (int)token) * a.out_stride +
+            head * a.head_dim);
+#pragma unroll
+        for (int k = 0; k < T::kSteps; ++k) {
+            const int chunk = 2 * k + h;
+            if (chunk >= chunks) continue;
+            float x[8], y[8];
+            Vec<Bf16>::widen(o[chunk], x);
+            Vec<Bf16>::widen(__builtin_bit_cast(uint4, dout[k]), y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) minus_d -= x[e] * y[e];
+        }
+    }
+    {
+        float own;
+        const float other = other_half(minus_d, own);
+        minus_d = own + other;
+    }
+    float minus_lse2 = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    if (live && lane < 32 && blockIdx.y == 0)
+        f.minus_lse[stat] = lse == -INFINITY ? -INFINITY : -lse / a.scale;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+        const int64_t past = (int64_t)a.heads * a.q_items.start[a.batch];
+        f.minus_lse[past] = -INFINITY;
+        f.minus_d[past] = 0.f;
+    }
     settle(q);
     settle(dout);
     asm volatile("" : "+v"(minus_lse2), "+v"(minus_d));
@@ -678,13 +675,6 @@ hipError_t launch_attention_backward(const AttnArgs& a, const AttnPlan& p, void*
     f.minus_d = reinterpret_cast<float*>(at);
     at += padded((q_rows + 1) * sizeof(float));
     f.part = reinterpret_cast<float*>(at);
-    if (q_rows > 0) {
-        // (a launch holds under 2^32 threads)
-        const int64_t blocks = std::min<int64_t>((q_rows + 7) / 8, int64_t(1) << 22);
-        rows_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(f, q_rows);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
     return a.head_dim <= 64   ? backward_as<64>(f, p, s)
            : a.head_dim <= 96 ? backward_as<96>(f, p, s)
                               : backward_as<128>(f, p, s);
