@@ -77,16 +77,17 @@ struct RowVec {
     }
 };
 
-// A row's vectors as they lie, zeros past its end (and where there is no
-// tensor).
+// A row's vectors as they lie, zeros past its end and where there is no
+// tensor or (`live`) no row.
 template <int VPT, int TPR>
 __device__ __forceinline__ void load_row(uint4 (&q)[VPT], const void* base, int64_t row, int nv,
-                                         int t) {
+                                         int t, bool live = true) {
     const uint4* p = reinterpret_cast<const uint4*>(base) + row * nv;
+    const int vectors = base && live ? nv : 0;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
         const int v = u * TPR + t;
-        q[u] = base && v < nv ? p[v] : make_uint4(0, 0, 0, 0);
+        q[u] = v < vectors ? p[v] : make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -253,14 +254,12 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(NormArgs a, ItemTa
 // workgroup walks one chunk of one item's rows with its sums in registers and
 // what its columns are multiplied by in LDS, put together once; x and y of the
 // next row are loaded, still packed, while a row is worked on, dh and dr before
-// the statistics that come ahead of them. It joins its row groups through LDS in a fixed order and writes [3][dim]
-// binary32 values; no atomics, so the sums' order never changes.
+// the statistics that come ahead of them. It joins its row groups through LDS
+// in a fixed order and writes [3][dim] binary32 values; no atomics, so the
+// sums' order never changes.
 template <typename T, int VPT, int TPR>
-__global__ __launch_bounds__(kThreads, VPT * Vec<T>::N <= 24 ? 2 : 1) void gated_norm_backward_kernel(NormArgs a,
-                                                                       ItemTable items,
-                                                                       ItemTable chunks,
-                                                                       int64_t rows_per_chunk,
-                                                                       bool nt) {
+__global__ __launch_bounds__(kThreads, VPT* Vec<T>::N <= 24 ? 2 : 1) void gated_norm_backward_kernel(
+    NormArgs a, ItemTable items, ItemTable chunks, int64_t rows_per_chunk, bool nt) {
     constexpr int N = Vec<T>::N;
     constexpr int R = kThreads / TPR;        // rows in flight
     __shared__ float red[4];
@@ -275,11 +274,12 @@ __global__ __launch_bounds__(kThreads, VPT * Vec<T>::N <= 24 ? 2 : 1) void gated
                           (int64_t)((int)blockIdx.x - chunks.start[item]) * rows_per_chunk;
     const int64_t end = min(first + rows_per_chunk, (int64_t)items.start[item + 1]);
 
-    // (a group past the last row repeats it, stores nothing and adds nothing)
+    // (a group past the last row reads nothing, stores nothing and adds nothing:
+    // another group may have written that row's results over its inputs)
     int64_t row = first + group;
     uint4 next_x[VPT], next_y[VPT];
-    load_row<VPT, TPR>(next_x, a.x, min(row, end - 1), nv, t);
-    load_row<VPT, TPR>(next_y, a.y, min(row, end - 1), nv, t);
+    load_row<VPT, TPR>(next_x, a.x, row, nv, t, row < end);
+    load_row<VPT, TPR>(next_y, a.y, row, nv, t, row < end);
     const int64_t mod = item * a.mod_stride;
     for (int c = threadIdx.x; c < a.dim; c += kThreads) {
         mul[c] = column<T>(a.weight, c, 1.f) * (1.0f + column<T>(a.scale, mod + c, 0.f));
@@ -301,12 +301,12 @@ __global__ __launch_bounds__(kThreads, VPT * Vec<T>::N <= 24 ? 2 : 1) void gated
         const bool live = row < end;
         RowVec<T, VPT, TPR> x, y, d;
         uint4 raw_d[VPT], raw_r[VPT];
-        load_row<VPT, TPR>(raw_d, a.dh, min(row, end - 1), nv, t);
-        load_row<VPT, TPR>(raw_r, a.dr, min(row, end - 1), nv, t);
+        load_row<VPT, TPR>(raw_d, a.dh, row, nv, t, row < end);
+        load_row<VPT, TPR>(raw_r, a.dr, row, nv, t, row < end);
         x.widen(next_x);
         if (a.y) y.widen(next_y);
-        load_row<VPT, TPR>(next_x, a.x, min(row + R, end - 1), nv, t);
-        load_row<VPT, TPR>(next_y, a.y, min(row + R, end - 1), nv, t);
+        load_row<VPT, TPR>(next_x, a.x, row + R, nv, t, row + R < end);
+        load_row<VPT, TPR>(next_y, a.y, row + R, nv, t, row + R < end);
         float y_rstd = 1.f;
         if (a.y) {
             y_rstd = normalise(y, a.post, nv, t, inv_dim, a.eps, red);
@@ -320,15 +320,14 @@ __global__ __launch_bounds__(kThreads, VPT * Vec<T>::N <= 24 ? 2 : 1) void gated
         }
         const float rstd = normalise(x, a.pre, nv, t, inv_dim, a.eps, red);
         d.widen(raw_d);
-        const float once = live ? 1.f : 0.f;
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
             float m[N];
             factors<N>(mul, min(u * TPR + t, nv - 1), m);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                sums[0][u][e] += once * d.f[u][e] * x.f[u][e];
-                sums[1][u][e] += once * d.f[u][e];
+                sums[0][u][e] += live ? d.f[u][e] * x.f[u][e] : 0.f;
+                sums[1][u][e] += live ? d.f[u][e] : 0.f;
                 d.f[u][e] *= m[e];
             }
         }
@@ -350,7 +349,7 @@ __global__ __launch_bounds__(kThreads, VPT * Vec<T>::N <= 24 ? 2 : 1) void gated
                 factors<N>(lift, min(u * TPR + t, nv - 1), g);
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    sums[2][u][e] += once * d.f[u][e] * y.f[u][e];
+                    sums[2][u][e] += live ? d.f[u][e] * y.f[u][e] : 0.f;
                     d.f[u][e] *= g[e];
                 }
             }
