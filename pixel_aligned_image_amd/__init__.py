@@ -17,6 +17,8 @@ import sys
 
 import torch
 
+from ._streams import fresh as _fresh, lends as _lends
+
 __all__ = ["P3DError", "P3D_F32", "P3D_BF16", "P3D_MAX_BATCH", "lib", "p3d_version",
            "p3d_status_string", "p3d_last_error", "p3d_distance_from_fov", "p3d_make_camera",
            "p3d_project_points", "p3d_bilinear_sample", "p3d_proj_cond",
@@ -221,6 +223,7 @@ def _cams(cams):
 
 
 # -------------------------------------------------------------- entry points ---
+@_lends
 def p3d_project_points(coords, n, resolution, cams, height, width, grid=None, pixel=None,
                        frac=None, depth=None, mask=None, stream=None, points="cell_centres"):
     """Enqueue p3d_project_points (points="cell_centres") or
@@ -242,6 +245,7 @@ def p3d_project_points(coords, n, resolution, cams, height, width, grid=None, pi
                                          int(height), int(width), *args))
 
 
+@_lends
 def p3d_requantize_coords(src, src_resolution, grid, dst, mode="round_nodes", stream=None):
     """Enqueue p3d_requantize_coords: int32 [n, 4] (b, x, y, z) on a
     src_resolution grid -> dst int32 [n, 4] on `grid`; mode "round_nodes"
@@ -252,6 +256,7 @@ def p3d_requantize_coords(src, src_resolution, grid, dst, mode="round_nodes", st
                                      _dev(dst, "dst", torch.int32, (n, 4)), _stream(stream)))
 
 
+@_lends
 def p3d_bilinear_sample(feat, grid, out, batch_index=None, stream=None, order=None):
     """Enqueue p3d_bilinear_sample (p3d_bilinear_sample_ordered with an
     order, int32 [n] device tensor). feat: [B, H, W, C] float32/bfloat16;
@@ -299,6 +304,7 @@ def proj_cond_workspace(n, batch, feat, device="cuda"):
                        device=device)
 
 
+@_lends
 def p3d_proj_cond(coords, n, resolution, cams, feat, weight, out, bias=None, n_null=0,
                   mask=None, stream=None, points="cell_centres", workspace=None, noalloc=False,
                   order=None):
@@ -366,6 +372,7 @@ STAT_FIELDS = ("tokens", "inside", "sum0", "sum1", "sum_sq0", "sum_sq1", "cos_su
                "cos_count")        # the eight doubles of p3d_proj_stats, in order
 
 
+@_lends
 def p3d_projection_stats(coords, n, resolution, cams, feat, stats, points="cell_centres",
                          stream=None, order=None):
     """Enqueue p3d_projection_stats (p3d_projection_stats_ordered with an
@@ -449,6 +456,7 @@ def _maps(feat, batch):
     return feats, maps, dt
 
 
+@_lends
 def p3d_proj_sample(coords, n, resolution, cams, feat, S, mask=None, points="cell_centres",
                     stream=None, order=None):
     """Enqueue p3d_proj_sample (p3d_proj_sample_ordered with an order from
@@ -466,6 +474,7 @@ def p3d_proj_sample(coords, n, resolution, cams, feat, S, mask=None, points="cel
                                        _dev(mask, "mask", torch.uint8, (n,)), _stream(stream)))
 
 
+@_lends
 def p3d_stream_copy(src, dst, stream=None):
     """Enqueue p3d_stream_copy: dst[:] = src[:] (contiguous device tensors of
     equal byte size, a multiple of 16); a measurement helper, not a step of
@@ -485,6 +494,7 @@ def p3d_token_order_workspace_size(n, batch, key_height, key_width):
     return int(size)
 
 
+@_lends
 def p3d_token_order(coords, n, resolution, cams, key_height, key_width, order, workspace=None,
                     points="cell_centres", stream=None):
     """Enqueue p3d_token_order: order (int32 [n] device tensor) receives an
@@ -494,8 +504,8 @@ def p3d_token_order(coords, n, resolution, cams, key_height, key_width, order, w
     camarr, batch = _cams(cams)
     n = int(n)
     if workspace is None:
-        workspace = torch.empty(p3d_token_order_workspace_size(n, batch, key_height, key_width),
-                                dtype=torch.uint8, device="cuda")
+        workspace = _fresh(p3d_token_order_workspace_size(n, batch, key_height, key_width),
+                           "cuda", stream)
     _check(lib.p3d_token_order(_dev(coords, "coords", torch.int32, (n, 4)), n, int(resolution),
                                POINTS[points], camarr, batch, int(key_height), int(key_width),
                                _dev(order, "order", torch.int32, (n,)),
@@ -503,6 +513,7 @@ def p3d_token_order(coords, n, resolution, cams, key_height, key_width, order, w
                                _stream(stream)))
 
 
+@_lends
 def p3d_proj_linear_grouped(S, weights, outs, biases=None, accumulate=False, stream=None):
     """Enqueue p3d_proj_linear_grouped: for every block g, outs[g] = W_g S +
     b_g (accumulate: outs[g] += ...). S: bf16 [n, K]; weights: list of bf16

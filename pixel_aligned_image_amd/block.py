@@ -12,6 +12,8 @@ import ctypes
 
 import torch
 
+from ._streams import fresh as _fresh, lends as _lends
+
 __all__ = ["p3d_gated_norm", "p3d_gated_norm_backward", "p3d_gated_norm_workspace_size",
            "p3d_rotary", "p3d_rotary_backward", "p3d_rotary_workspace_size",
            "p3d_rotary_frequencies", "p3d_attention", "p3d_attention_backward",
@@ -90,17 +92,37 @@ def _dtype(t, name):
     return dt
 
 
+def _ptr(t, name, dtype, shape):
+    """Device pointer of an optional contiguous tensor. The smallest calls last
+    a few microseconds, as long as ten tensors' checks: one line passes what is
+    right, the package's own check words what is not."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
+    return _core._dev(t, name, dtype, shape)
+
+
+def _stream(stream):
+    """As the package's other calls: torch's current stream. Its handle alone
+    costs 0.4 us, a torch.cuda.Stream of it 2.8 us."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 def _sized(size):
     if size == 0:
         raise _core.P3DError(_core.P3D_ERR_INVALID_ARG, _core.p3d_last_error())
     return int(size)
 
 
-def _work(workspace, size, device):
+def _work(workspace, size, device, stream):
     """(pointer, bytes) of the caller's workspace, or of a fresh one. The
     tensor is returned too, so that it lives until the call is enqueued."""
     if workspace is None:
-        workspace = torch.empty(_sized(size()), dtype=torch.uint8, device=device)
+        workspace = _fresh(_sized(size()), device, stream)
     return workspace, _core._dev(workspace, "workspace", torch.uint8), workspace.numel()
 
 
@@ -109,11 +131,11 @@ def _heads(t, name, dtype, heads=None, head_dim=None, rows=None):
     tokens may be strided (a view of a packed projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s must be on the GPU, got %s" % (name, t.device))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != 3 or (heads is not None and tuple(t.shape) != (rows, heads, head_dim)):
+    if t.dim() != 3 or (heads is not None and t.shape != (rows, heads, head_dim)):
         raise ValueError("%s must be [%s, %s, %s], got %s" % (
             name, "n" if rows is None else rows, "heads" if heads is None else heads,
             "head_dim" if head_dim is None else head_dim, tuple(t.shape)))
@@ -128,7 +150,7 @@ def _heads(t, name, dtype, heads=None, head_dim=None, rows=None):
 def _norm(x, offsets, gate, scale, shift, pre, post, weight, bias, post_weight, res_scale, eps):
     if x.dim() != 2:
         raise ValueError("x must be [n, dim], got %s" % (tuple(x.shape),))
-    dev, dt = _core._dev, x.dtype
+    dt = x.dtype
     n, dim = x.shape
     off = make_offsets((0, n) if offsets is None else offsets)
     batch = len(off) - 1
@@ -139,9 +161,9 @@ def _norm(x, offsets, gate, scale, shift, pre, post, weight, bias, post_weight, 
         if t is None:
             continue
         # rows of a packed [batch, k, dim] modulation may be strided
-        if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.dtype != dt:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dt:
             raise TypeError("%s must be a %s tensor on the GPU" % (name, dt))
-        if tuple(t.shape) != (batch, dim) or (dim > 1 and t.stride(1) != 1):
+        if t.shape != (batch, dim) or (dim > 1 and t.stride(1) != 1):
             raise ValueError("%s must be [%d, %d] with contiguous rows, got %s, strides %s" % (
                 name, batch, dim, tuple(t.shape), t.stride()))
         if batch > 1:
@@ -152,12 +174,13 @@ def _norm(x, offsets, gate, scale, shift, pre, post, weight, bias, post_weight, 
         setattr(d, name, t.data_ptr())
     if stride is not None:
         d.mod_stride = stride
-    d.weight = dev(weight, "weight", dt, (dim,))
-    d.bias = dev(bias, "bias", dt, (dim,))
-    d.post_weight = dev(post_weight, "post_weight", dt, (dim,))
+    d.weight = _ptr(weight, "weight", dt, (dim,))
+    d.bias = _ptr(bias, "bias", dt, (dim,))
+    d.post_weight = _ptr(post_weight, "post_weight", dt, (dim,))
     return d, off
 
 
+@_lends
 def p3d_gated_norm(x, h, offsets=None, y=None, gate=None, scale=None, shift=None, r=None,
                    pre="layer", post="none", weight=None, bias=None, post_weight=None,
                    res_scale=1.0, eps=1e-6, stream=None):
@@ -168,10 +191,10 @@ def p3d_gated_norm(x, h, offsets=None, y=None, gate=None, scale=None, shift=None
     item)."""
     d, off = _norm(x, offsets, gate, scale, shift, pre, post, weight, bias, post_weight,
                    res_scale, eps)
-    dev, dt, shape = _core._dev, x.dtype, x.shape
-    _core._check(lib.p3d_gated_norm(d, dev(x, "x"), dev(y, "y", dt, shape),
-                                    dev(r, "r", dt, shape), dev(h, "h", dt, shape),
-                                    _core._stream(stream)))
+    dt, shape = x.dtype, x.shape
+    _core._check(lib.p3d_gated_norm(d, _ptr(x, "x", dt, shape), _ptr(y, "y", dt, shape),
+                                    _ptr(r, "r", dt, shape), _ptr(h, "h", dt, shape),
+                                    _stream(stream)))
 
 
 def p3d_gated_norm_workspace_size(x, offsets=None):
@@ -181,6 +204,7 @@ def p3d_gated_norm_workspace_size(x, offsets=None):
     return _sized(lib.p3d_gated_norm_workspace_size(d))
 
 
+@_lends
 def p3d_gated_norm_backward(dh, x, dx, offsets=None, dr=None, y=None, dy=None, gate=None,
                             scale=None, pre="layer", post="none", weight=None, bias=None,
                             post_weight=None, res_scale=1.0, eps=1e-6, dgate=None, dscale=None,
@@ -192,40 +216,42 @@ def p3d_gated_norm_backward(dh, x, dx, offsets=None, dr=None, y=None, dy=None, g
     dpost_weight [dim], each None where it is not wanted."""
     d, off = _norm(x, offsets, gate, scale, None, pre, post, weight, bias, post_weight,
                    res_scale, eps)
-    dev, dt, shape, f = _core._dev, x.dtype, x.shape, torch.float32
+    dev, dt, shape, f = _ptr, x.dtype, x.shape, torch.float32
     items, cols = (d.batch, d.dim), (d.dim,)
-    keep, ws, nbytes = _work(workspace, lambda: lib.p3d_gated_norm_workspace_size(d), x.device)
+    keep, ws, nbytes = _work(workspace, lambda: lib.p3d_gated_norm_workspace_size(d), x.device,
+                             stream)
     _core._check(lib.p3d_gated_norm_backward(
-        d, dev(dh, "dh", dt, shape), dev(dr, "dr", dt, shape), dev(x, "x"),
+        d, dev(dh, "dh", dt, shape), dev(dr, "dr", dt, shape), dev(x, "x", dt, shape),
         dev(y, "y", dt, shape), dev(dx, "dx", dt, shape), dev(dy, "dy", dt, shape),
         dev(dgate, "dgate", f, items), dev(dscale, "dscale", f, items),
         dev(dshift, "dshift", f, items), dev(dweight, "dweight", f, cols),
         dev(dbias, "dbias", f, cols), dev(dpost_weight, "dpost_weight", f, cols), ws, nbytes,
-        _core._stream(stream)))
+        _stream(stream)))
 
 
 # ------------------------------------------------------------------ rotary ---
 def _rotary(x, positions, freqs, layout, magnitude, gamma, eps):
-    dev = _core._dev
     n, heads, hd = x.shape
-    if not isinstance(positions, torch.Tensor) or positions.device.type != "cuda":
+    if not isinstance(positions, torch.Tensor) or not positions.is_cuda:
         raise TypeError("positions must be a torch.Tensor on the GPU")
-    if positions.dtype != torch.int32:
+    if positions.dtype is not torch.int32:
         raise TypeError("positions must be torch.int32, got %s" % positions.dtype)
     if positions.dim() != 2 or positions.shape[0] != n:
         raise ValueError("positions must be [%d, axes], got %s" % (n, tuple(positions.shape)))
     axes = positions.shape[1]
-    if axes > 1 and positions.stride(1) != 1:
-        raise ValueError("positions must have contiguous rows, got strides %s"
-                         % (positions.stride(),))
+    pos_stride = positions.stride()
+    if axes > 1 and pos_stride[1] != 1:
+        raise ValueError("positions must have contiguous rows, got strides %s" % (pos_stride,))
     if freqs.dim() != 1:
         raise ValueError("freqs must be [pairs], got %s" % (tuple(freqs.shape),))
-    return p3d_rotary_desc(n, heads, hd, _dtype(x, "x"), ROTARY_LAYOUT[layout], axes,
-                           freqs.shape[0], positions.stride(0) if n > 1 else axes, magnitude,
-                           eps, positions.data_ptr(), dev(freqs, "freqs", torch.float32),
-                           dev(gamma, "gamma", x.dtype, (heads, hd)))
+    pairs = freqs.shape[0]
+    return p3d_rotary_desc(n, heads, hd, _dtype(x, "x"), ROTARY_LAYOUT[layout], axes, pairs,
+                           pos_stride[0] if n > 1 else axes, magnitude, eps,
+                           positions.data_ptr(), _ptr(freqs, "freqs", torch.float32, (pairs,)),
+                           _ptr(gamma, "gamma", x.dtype, (heads, hd)))
 
 
+@_lends
 def p3d_rotary(x, positions, freqs, out, layout="interleaved", magnitude=1.0, gamma=None,
                eps=1e-6, stream=None):
     """Enqueue p3d_rotary: the heads of x [n, heads, head_dim] (float32 or
@@ -235,7 +261,7 @@ def p3d_rotary(x, positions, freqs, out, layout="interleaved", magnitude=1.0, ga
     xp, xs = _heads(x, "x", x.dtype)
     d = _rotary(x, positions, freqs, layout, magnitude, gamma, eps)
     op, os = _heads(out, "out", x.dtype, x.shape[1], x.shape[2], x.shape[0])
-    _core._check(lib.p3d_rotary(d, xp, xs, op, os, _core._stream(stream)))
+    _core._check(lib.p3d_rotary(d, xp, xs, op, os, _stream(stream)))
 
 
 def p3d_rotary_workspace_size(x, positions, freqs):
@@ -244,6 +270,7 @@ def p3d_rotary_workspace_size(x, positions, freqs):
         _rotary(x, positions, freqs, "interleaved", 1.0, None, 1e-6)))
 
 
+@_lends
 def p3d_rotary_backward(dout, positions, freqs, dx, layout="interleaved", magnitude=1.0,
                         gamma=None, eps=1e-6, x=None, dgamma=None, workspace=None, stream=None):
     """Enqueue p3d_rotary_backward: dx from dout [n, heads, head_dim]; with
@@ -256,10 +283,11 @@ def p3d_rotary_backward(dout, positions, freqs, dx, layout="interleaved", magnit
     op, os = _heads(dx, "dx", dout.dtype, heads, hd, n)
     keep, ws, nbytes = None, None, 0
     if dgamma is not None:
-        keep, ws, nbytes = _work(workspace, lambda: lib.p3d_rotary_workspace_size(d), dout.device)
+        keep, ws, nbytes = _work(workspace, lambda: lib.p3d_rotary_workspace_size(d), dout.device,
+                                 stream)
     _core._check(lib.p3d_rotary_backward(
-        d, dp, ds, xp, xs, op, os, _core._dev(dgamma, "dgamma", torch.float32, (heads, hd)), ws,
-        nbytes, _core._stream(stream)))
+        d, dp, ds, xp, xs, op, os, _ptr(dgamma, "dgamma", torch.float32, (heads, hd)), ws,
+        nbytes, _stream(stream)))
 
 
 def p3d_rotary_frequencies(base, pairs, scaling="plain", factor=1.0, trained=0.0):
@@ -297,6 +325,7 @@ def p3d_attention_workspace_size(q, k, q_offsets=None, k_offsets=None, causal=Fa
     return _sized(lib.p3d_attention_workspace_size(d))
 
 
+@_lends
 def p3d_attention(q, k, v, out, q_offsets=None, k_offsets=None, scale=None, causal=False,
                   lse=None, workspace=None, stream=None):
     """Enqueue p3d_attention: out [nq, heads, head_dim] from q, k, v ([n,
@@ -311,10 +340,11 @@ def p3d_attention(q, k, v, out, q_offsets=None, k_offsets=None, scale=None, caus
     kp, ks = _heads(k, "k", dt, kv_heads, hd, nk)
     vp, vs = _heads(v, "v", dt, kv_heads, hd, nk)
     op, os = _heads(out, "out", dt, heads, hd, nq)
-    keep, ws, nbytes = _work(workspace, lambda: lib.p3d_attention_workspace_size(d), q.device)
+    keep, ws, nbytes = _work(workspace, lambda: lib.p3d_attention_workspace_size(d), q.device,
+                             stream)
     _core._check(lib.p3d_attention(d, qp, qs, kp, ks, vp, vs, op, os,
-                                   _core._dev(lse, "lse", torch.float32, (nq, heads)), ws,
-                                   nbytes, _core._stream(stream)))
+                                   _ptr(lse, "lse", torch.float32, (nq, heads)), ws,
+                                   nbytes, _stream(stream)))
 
 
 def p3d_attention_backward_workspace_size(q, k, q_offsets=None, k_offsets=None, causal=False):
@@ -323,6 +353,7 @@ def p3d_attention_backward_workspace_size(q, k, q_offsets=None, k_offsets=None, 
     return _sized(lib.p3d_attention_backward_workspace_size(d))
 
 
+@_lends
 def p3d_attention_backward(dout, q, k, v, out, lse, dq, dk, dv, q_offsets=None, k_offsets=None,
                            scale=None, causal=False, workspace=None, stream=None):
     """Enqueue p3d_attention_backward: dq, dk, dv (like q, k, v) from dout,
@@ -335,10 +366,10 @@ def p3d_attention_backward(dout, q, k, v, out, lse, dq, dk, dv, q_offsets=None, 
     for name, t, n, h in (("dout", dout, nq, heads), ("q", q, nq, heads), ("k", k, nk, kv_heads),
                           ("v", v, nk, kv_heads), ("out", out, nq, heads)):
         args += _heads(t, name, dt, h, hd, n)
-    args.append(_core._dev(lse, "lse", torch.float32, (nq, heads)))
+    args.append(_ptr(lse, "lse", torch.float32, (nq, heads)))
     for name, t, n, h in (("dq", dq, nq, heads), ("dk", dk, nk, kv_heads),
                           ("dv", dv, nk, kv_heads)):
         args += _heads(t, name, dt, h, hd, n)
     keep, ws, nbytes = _work(workspace, lambda: lib.p3d_attention_backward_workspace_size(d),
-                             q.device)
-    _core._check(lib.p3d_attention_backward(d, *args, ws, nbytes, _core._stream(stream)))
+                             q.device, stream)
+    _core._check(lib.p3d_attention_backward(d, *args, ws, nbytes, _stream(stream)))

@@ -1,0 +1,66 @@
+"""Calls on a stream of their own: a tensor that the caller drops while the
+call still waits for its turn is not handed out again before it has run."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import pixel_aligned_image_amd as p3d
+
+N, DIM = 4096, 512
+SPIN = 20_000_000
+
+
+def gated_norm(s):
+    x = torch.randn(N, DIM, device="cuda")
+    p3d.p3d_gated_norm(x, torch.empty_like(x), stream=s)
+
+
+def norm_backward(s):
+    x = torch.randn(N, DIM, device="cuda")
+    p3d.p3d_gated_norm_backward(x, x, torch.empty_like(x), stream=s,
+                                dweight=torch.empty(DIM, device="cuda"))
+
+
+def rotary(s):
+    x = torch.randn(N, 4, 128, device="cuda")
+    p3d.p3d_rotary(x, torch.zeros(N, 1, dtype=torch.int32, device="cuda"),
+                   torch.ones(64, device="cuda"), torch.empty_like(x), stream=s)
+
+
+def attention(s):
+    q = torch.randn(N, 8, 128, device="cuda").bfloat16()
+    k = torch.randn(8 * N, 1, 128, device="cuda").bfloat16()
+    p3d.p3d_attention(q[:8], k, k, torch.empty_like(q[:8]), stream=s)
+
+
+def sample(s):
+    feat = torch.randn(1, 32, 32, DIM, device="cuda")
+    p3d.p3d_bilinear_sample(feat, torch.zeros(N, 2, device="cuda"),
+                            torch.empty(N, DIM, device="cuda"), stream=s)
+
+
+def token_order(s):
+    coords = torch.zeros(N, 4, dtype=torch.int32, device="cuda")
+    p3d.p3d_token_order(coords, N, 64, [(1.0, 2.0)], 32, 32,
+                        torch.empty(N, dtype=torch.int32, device="cuda"), stream=s)
+
+
+@pytest.mark.parametrize("call", [gated_norm, norm_backward, rotary, attention, sample,
+                                  token_order], ids=lambda f: f.__name__)
+def test_dropped_tensors_wait_for_the_stream(call):
+    own = torch.cuda.Stream()
+    call(own)                                # kernels loaded, workspaces' sizes cached
+    torch.cuda.synchronize()
+    with torch.cuda.stream(own):
+        torch.cuda._sleep(SPIN)
+    own.wait_stream(torch.cuda.current_stream())
+    call(own)
+    assert not own.query()
+    # whatever the allocator gives out now keeps its values
+    taken = [torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+             for size in (512, 1 << 12, 1 << 14, 1 << 16, 1 << 18, 1 << 20, N * DIM * 2,
+                          N * DIM * 4) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(bool((t == 7).all()) for t in taken)
