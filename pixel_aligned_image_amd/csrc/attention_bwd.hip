@@ -124,6 +124,42 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
     uint32_t token, member;
     f.group.split(live ? row : 0, token, member);
     const int head = kv_head * f.group.size + member;
+    int part = (nk + f.splits - 1) / f.splits;
+    part = (part + kWalk - 1) / kWalk * kWalk;
+    const int begin = (int)min((int64_t)blockIdx.y * part, (int64_t)nk);
+    int end = (int)min((int64_t)begin + part, (int64_t)nk);
+    int limit = end;
+    if (a.causal) {
+        limit = min(end, live ? (int)token + nk - nq + 1 : end);
+        uint32_t last, m;
+        f.group.split(min(row0 + kHeld, rows) - 1, last, m);
+        end = min(end, (int)last + nk - nq + 1);
+    }
+    const int all_see = __builtin_amdgcn_readfirstlane(limit);
+
+    // the first tile travels while the rows' own values are loaded
+    if (chunks < T::kChunks) {
+        for (int i = 0; i < 2; ++i) {
+            T::clear(kt[i], kWalk, 64 * kWaves, threadIdx.x);
+            T::clear(vt[i], kWalk, 64 * kWaves, threadIdx.x);
+        }
+        __syncthreads();
+    }
+    const uint16_t* kb = reinterpret_cast<const uint16_t*>(a.k) + (int64_t)k0 * a.k_stride +
+                         kv_head * a.head_dim;
+    const uint16_t* vb = reinterpret_cast<const uint16_t*>(a.v) + (int64_t)k0 * a.v_stride +
+                         kv_head * a.head_dim;
+    // rows past the item's last key repeat it; their dS is 0
+    auto fetch = [&](int buf, int key) {
+        T::template load<kWalk, kWaves>(kt[buf], wave, lane, chunks, [&](int r) {
+            return reinterpret_cast<const uint4*>(kb + (int64_t)min(key + r, nk - 1) * a.k_stride);
+        });
+        T::template load<kWalk, kWaves>(vt[buf], wave, lane, chunks, [&](int r) {
+            return reinterpret_cast<const uint4*>(vb + (int64_t)min(key + r, nk - 1) * a.v_stride);
+        });
+    };
+    if (begin < end) fetch(0, begin);
+
     bf16x8_t q[T::kSteps], dout[T::kSteps];
     load_query<HD>(q,
                    reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
@@ -174,43 +210,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
     settle(dout);
     asm volatile("" : "+v"(minus_lse2), "+v"(minus_d));
 
-    int part = (nk + f.splits - 1) / f.splits;
-    part = (part + kWalk - 1) / kWalk * kWalk;
-    const int begin = (int)min((int64_t)blockIdx.y * part, (int64_t)nk);
-    int end = (int)min((int64_t)begin + part, (int64_t)nk);
-    int limit = end;
-    if (a.causal) {
-        limit = min(end, live ? (int)token + nk - nq + 1 : end);
-        uint32_t last, m;
-        f.group.split(min(row0 + kHeld, rows) - 1, last, m);
-        end = min(end, (int)last + nk - nq + 1);
-    }
-    const int all_see = __builtin_amdgcn_readfirstlane(limit);
-
     f32x16 dq[T::kBlocks];
 #pragma unroll
     for (int b = 0; b < T::kBlocks; ++b) dq[b] = zero16();
-    if (chunks < T::kChunks) {
-        for (int i = 0; i < 2; ++i) {
-            T::clear(kt[i], kWalk, 64 * kWaves, threadIdx.x);
-            T::clear(vt[i], kWalk, 64 * kWaves, threadIdx.x);
-        }
-        __syncthreads();
-    }
-    const uint16_t* kb = reinterpret_cast<const uint16_t*>(a.k) + (int64_t)k0 * a.k_stride +
-                         kv_head * a.head_dim;
-    const uint16_t* vb = reinterpret_cast<const uint16_t*>(a.v) + (int64_t)k0 * a.v_stride +
-                         kv_head * a.head_dim;
-    // rows past the item's last key repeat it; their dS is 0
-    auto fetch = [&](int buf, int key) {
-        T::template load<kWalk, kWaves>(kt[buf], wave, lane, chunks, [&](int r) {
-            return reinterpret_cast<const uint4*>(kb + (int64_t)min(key + r, nk - 1) * a.k_stride);
-        });
-        T::template load<kWalk, kWaves>(vt[buf], wave, lane, chunks, [&](int r) {
-            return reinterpret_cast<const uint4*>(vb + (int64_t)min(key + r, nk - 1) * a.v_stride);
-        });
-    };
-    if (begin < end) fetch(0, begin);
     auto products = [&](f32x16& s, f32x16& dp, uint32_t k_at, uint32_t v_at, int b) {
         s = zero16();
         dp = zero16();
@@ -231,8 +233,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
     auto gradient = [&](auto fine, f32x16& s, const f32x16& dp, bf16x8_t* hi, bf16x8_t* lo) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float p = __builtin_amdgcn_exp2f(s[i] * c + minus_lse2);
-            sum_d += p * dp[i];
+            const float p = __builtin_amdgcn_exp2f(fmaf(s[i], c, minus_lse2));
+            sum_d = fmaf(p, dp[i], sum_d);
             const float g = p * (dp[i] + minus_d);
             hi[i >> 3][i & 7] = (__bf16)g;
             if constexpr (decltype(fine)::value)
@@ -325,16 +327,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
 }
 
 // Walks the rows of one key head's query heads, head by head, in tiles of 32
-// tokens: every tile is a run of tokens of one head, loaded as it lies.
+// tokens (64 for narrow heads: half the barriers): every tile is a run of
+// tokens of one head, loaded as it lies.
 //
 // The wave's two sums take 128 registers for heads of 128 and its keys 32. Its
 // values stay in LDS: 32 registers more would leave two waves a SIMD nothing
 // to read fragments ahead into, and every matrix instruction would wait for
 // LDS (one wave a SIMD, with registers to spare, is held up by its own issue).
 template <int HD>
-__global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
+__global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dkv_kernel(BwdArgs f) {
     using T = Tile<HD>;
-    constexpr int kRows = 32;
+    constexpr int kRows = HD <= 64 ? 64 : 32;
     __shared__ uint4 tiles[2][2 * kRows * T::kChunks];   // [buffer][q rows, dout rows]
     __shared__ uint4 values[kHeld * T::kChunks];
     __shared__ alignas(16) float stats[2][2][64];        // [buffer][-lse / scale, -D]
@@ -363,20 +366,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     }
     const int key = key0 + 32 * wave + (lane & 31);
     const bool live = key < nk;
-    bf16x8_t kf[T::kSteps];
-    load_query<HD>(kf,
-                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.k) +
-                                                  (int64_t)(k0 + (live ? key : 0)) * a.k_stride +
-                                                  kv_head * a.head_dim),
-                   live, chunks, lane);
-    // (keys past the item's last repeat it; their sums are not stored)
-    T::template load<kHeld, kWaves>(values, wave, lane, chunks, [&](int r) {
-        return reinterpret_cast<const uint4*>(
-            reinterpret_cast<const uint16_t*>(a.v) +
-            (int64_t)(k0 + min(key0 + r, nk - 1)) * a.v_stride + kv_head * a.head_dim);
-    });
-    settle(kf);
-
     // Tokens from `from` on see this lane's key, from `all_from` on all of the
     // wave's, and none before the first tile sees any of the workgroup's.
     int first = 0, from = 0, all_from = 0;
@@ -451,20 +440,35 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
             });
         }
     };
+    // the first tile travels while the keys and values are loaded
     if (member >= last_member) fetch(0);
+    bf16x8_t kf[T::kSteps];
+    load_query<HD>(kf,
+                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.k) +
+                                                  (int64_t)(k0 + (live ? key : 0)) * a.k_stride +
+                                                  kv_head * a.head_dim),
+                   live, chunks, lane);
+    // (keys past the item's last repeat it; their sums are not stored)
+    T::template load<kHeld, kWaves>(values, wave, lane, chunks, [&](int r) {
+        return reinterpret_cast<const uint4*>(
+            reinterpret_cast<const uint16_t*>(a.v) +
+            (int64_t)(k0 + min(key0 + r, nk - 1)) * a.v_stride + kv_head * a.head_dim);
+    });
+    settle(kf);
 
-    // One tile. The issue order is the written one: a matrix instruction, the
+    // 32 rows of a tile, from row `sub` on. The issue order is the written one: a matrix instruction, the
     // reads of the fragments a few matrix instructions on, and in the first
     // half of the sums the exponentials that the second half needs.
-    auto walk = [&](bool masked, int buf, int row) {
+    auto walk = [&](bool masked, int buf, int sub, int row) {
         constexpr int kAhead = 3;
-        const uint32_t at = T::row_base(tiles[buf], lane);
+        const uint4* rows = tiles[buf] + sub * T::kChunks;
+        const uint32_t at = T::row_base(rows, lane);
         const uint32_t v_at = T::row_base(values + 32 * wave * T::kChunks, lane);
         f32x16 s, dp;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float4 l = *reinterpret_cast<const float4*>(&stats[buf][0][8 * j + 4 * h]);
-            const float4 d = *reinterpret_cast<const float4*>(&stats[buf][1][8 * j + 4 * h]);
+            const float4 l = *reinterpret_cast<const float4*>(&stats[buf][0][sub + 8 * j + 4 * h]);
+            const float4 d = *reinterpret_cast<const float4*>(&stats[buf][1][sub + 8 * j + 4 * h]);
             s[4 * j] = l.x, s[4 * j + 1] = l.y, s[4 * j + 2] = l.z, s[4 * j + 3] = l.w;
             dp[4 * j] = d.x, dp[4 * j + 1] = d.y, dp[4 * j + 2] = d.z, dp[4 * j + 3] = d.w;
         }
@@ -490,7 +494,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
             for (int i = 0; i < 16; ++i)
                 if (acc_row(i, 0) < before) s[i] = -INFINITY;
         }
-        const uint32_t tr = T::tr_base(tiles[buf], lane);
+        const uint32_t tr = T::tr_base(rows, lane);
         constexpr int kSums = 4 * T::kBlocks, kTrAhead = 5;
         bf16x8_t frag[kTrAhead];
         auto read_tr = [&](int i) {          // (t, d, dv or dk)
@@ -530,7 +534,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
         --at_tile;
         settle_tile();
         if (member >= last_member) fetch(buf ^ 1);
-        walk(row < all_from, buf, row);
+#pragma unroll 1
+        for (int sub = 0; sub < kRows && row + sub < nq; sub += 32)
+            walk(row + sub < all_from, buf, sub, row + sub);
         buf ^= 1;
     }
 
@@ -558,18 +564,27 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dkv_kernel(BwdArgs f) {
     store_rows<HD>(dv, 1.0f, stage, chunks, lane, to(a.dv, a.dv_stride));
 }
 
-// Adds the parts of (token, head) rows in order: 32 lanes per row. With
-// `part_d`, also those of D, into minus_d [heads][tokens].
-__global__ __launch_bounds__(256) void join_kernel(const float* part, int splits, int64_t rows,
-                                                   int heads, int hd, float by, void* out,
-                                                   int64_t stride, const float* part_d,
-                                                   float* minus_d) {
+// What is joined into one result.
+struct Joint {
+    const float* part;
+    float by;
+    void* out;
+    int64_t stride;
+};
+
+// Adds the parts of (token, head) rows in order: 32 lanes per row, two results
+// side by side. With `part_d`, also those of D, into minus_d [heads][tokens].
+__global__ __launch_bounds__(256) void join_kernel(Joint first, Joint second, int splits,
+                                                   int64_t rows, int heads, int hd,
+                                                   const float* part_d, float* minus_d) {
+    const Joint& j = blockIdx.y ? second : first;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int d = (threadIdx.x & 31) * 4;
     if (row >= rows || d >= hd) return;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int p = 0; p < splits; ++p) {
-        const float4 v = *reinterpret_cast<const float4*>(part + (p * rows + row) * hd + d);
+        const float4 v = *reinterpret_cast<const float4*>(j.part + (p * rows + row) * hd + d);
         s.x += v.x;
         s.y += v.y;
         s.z += v.z;
@@ -577,21 +592,14 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, int splits
     }
     const int64_t token = row / heads;
     const int head = (int)(row - token * heads);
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + token * stride + head * hd + d) =
-        make_uint2(pack_bf16x2(s.x * by, s.y * by), pack_bf16x2(s.z * by, s.w * by));
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(j.out) + token * j.stride + head * hd +
+                              d) =
+        make_uint2(pack_bf16x2(s.x * j.by, s.y * j.by), pack_bf16x2(s.z * j.by, s.w * j.by));
     if (part_d && d == 0) {
         float sum = 0.f;
         for (int p = 0; p < splits; ++p) sum += part_d[p * rows + row];
         minus_d[rows / heads * head + token] = -sum;
     }
-}
-
-hipError_t join(const float* part, int splits, int64_t rows, int heads, int hd, float by,
-                void* out, int64_t stride, hipStream_t s, const float* part_d = nullptr,
-                float* minus_d = nullptr) {
-    join_kernel<<<dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s>>>(
-        part, splits, rows, heads, hd, by, out, stride, part_d, minus_d);
-    return hipGetLastError();
 }
 
 template <int HD>
@@ -607,9 +615,12 @@ hipError_t backward_as(BwdArgs& f, const AttnPlan& p, hipStream_t s) {
         dq_kernel<HD><<<dim3((unsigned)f.tiles.start[a.batch] * a.kv_heads, (unsigned)f.splits),
                         dim3(64 * kWaves), 0, s>>>(f);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        if (f.splits > 1 && (e = join(f.part, f.splits, q_rows, a.heads, a.head_dim, a.scale, a.dq,
-                                      a.dq_stride, s, f.part_d, f.minus_d)) != hipSuccess)
-            return e;
+        if (f.splits > 1) {
+            const Joint dq{f.part, a.scale, a.dq, a.dq_stride};
+            join_kernel<<<dim3((unsigned)((q_rows + 7) / 8)), dim3(256), 0, s>>>(
+                dq, dq, f.splits, q_rows, a.heads, a.head_dim, f.part_d, f.minus_d);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
     }
     if (k_rows > 0) {
         cut_items(a.k_items, a.batch, 1, kHeld, &f.tiles);
@@ -619,11 +630,10 @@ hipError_t backward_as(BwdArgs& f, const AttnPlan& p, hipStream_t s) {
                          dim3(64 * kWaves), 0, s>>>(f);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (f.splits > 1) {
-            if ((e = join(f.part, f.splits, k_rows, a.kv_heads, a.head_dim, a.scale, a.dk,
-                          a.dk_stride, s)) != hipSuccess)
-                return e;
-            return join(f.part2, f.splits, k_rows, a.kv_heads, a.head_dim, 1.0f, a.dv,
-                        a.dv_stride, s);
+            const Joint dk{f.part, a.scale, a.dk, a.dk_stride}, dv{f.part2, 1.0f, a.dv, a.dv_stride};
+            join_kernel<<<dim3((unsigned)((k_rows + 7) / 8), 2), dim3(256), 0, s>>>(
+                dk, dv, f.splits, k_rows, a.kv_heads, a.head_dim, nullptr, nullptr);
+            return hipGetLastError();
         }
     }
     return hipSuccess;
