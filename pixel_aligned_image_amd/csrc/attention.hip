@@ -173,7 +173,7 @@ struct Softmax {
             f32x16 e;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                e[i] = __builtin_amdgcn_exp2f(s[b][i] * c - base);
+                e[i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], c, -base));
                 sum += e[i];
             }
             p[2 * b] = acc_frag(e, 0);
@@ -200,13 +200,13 @@ struct Softmax {
         add(p, vt, lane);
         exponentials(s, next, c);
         // 8 transposed reads ahead, then per matrix instruction 2 reads and
-        // its share of the 128 vector instructions
+        // its share of the 112 vector instructions
         __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
 #pragma unroll
         for (int i = 0; i < 4 * T::kBlocks; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 32 / T::kBlocks, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 28 / T::kBlocks, 0);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[i] = next[i];
@@ -227,7 +227,7 @@ struct Softmax {
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            s[0][i] = __builtin_amdgcn_exp2f(s[0][i] * c - base);
+            s[0][i] = __builtin_amdgcn_exp2f(fmaf(s[0][i], c, -base));
             sum += s[0][i];
         }
         l += sum;
@@ -282,14 +282,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(FwdArgs f) {
     uint32_t token, member;
     f.group.split(live ? row : 0, token, member);
     const int head = kv_head * f.group.size + member;
-    bf16x8_t q[T::kSteps];
-    load_query<HD>(q,
-                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
-                                                  (int64_t)(q0 + (int)token) * a.q_stride +
-                                                  head * a.head_dim),
-                   live, chunks, lane);
-    settle(q);
-
     // keys of this part, and those this workgroup and this lane see
     const int parts = which < 0 ? 1 : f.parts;
     int share = (nk + parts - 1) / parts;
@@ -343,12 +335,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(FwdArgs f) {
                 vb + (int64_t)min(begin + key + r, nk - 1) * a.v_stride);
         });
     };
+    const int span = end - begin;
+    // the first tile travels while the queries are loaded
+    if (span > 0) fetch(0);
+    bf16x8_t q[T::kSteps];
+    load_query<HD>(q,
+                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
+                                                  (int64_t)(q0 + (int)token) * a.q_stride +
+                                                  head * a.head_dim),
+                   live, chunks, lane);
+    settle(q);
+
     // Tile by tile (`key` counts from `begin`): the scores of a tile, then
     // the second product of the tile before it in between this tile's
     // exponentials, so that the matrix cores run under them. V therefore
     // stays a tile longer than K (three buffers, two).
     bf16x8_t p[4];
-    const int span = end - begin;
     auto step = [&](auto first, int key) {
         tile_barrier();
         if (key + kKeys < span) fetch(key + kKeys);
@@ -369,7 +371,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(FwdArgs f) {
         else st.exponentials_and_add(sc, p, before, c, lane);
     };
     if (span > 0) {
-        fetch(0);
         step(std::true_type{}, 0);
         int key = kKeys;
         for (; key < span; key += kKeys) step(std::false_type{}, key);
@@ -431,13 +432,6 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
     f.group.split(live ? row : 0, token, member);
     const int head = kv_head * f.group.size + member;
 
-    bf16x8_t q[T::kSteps];
-    load_query<HD>(q,
-                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
-                                                  (int64_t)(q0 + (int)token) * a.q_stride +
-                                                  head * a.head_dim),
-                   live, chunks, lane);
-    settle(q);
     const int begin = (int)min((int64_t)which * f.share, (int64_t)nk);
     const int end = (int)min((int64_t)begin + f.share, (int64_t)nk);
     const int limit = a.causal && live ? min(end, (int)token + nk - nq + 1) : end;
@@ -464,7 +458,14 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
     };
     const int first = begin + wave * kSingleKeys;
     constexpr int kStep = kWaves * kSingleKeys;
-    if (first < end) fetch(0, first);
+    if (first < end) fetch(0, first);        // (ahead of the queries)
+    bf16x8_t q[T::kSteps];
+    load_query<HD>(q,
+                   reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
+                                                  (int64_t)(q0 + (int)token) * a.q_stride +
+                                                  head * a.head_dim),
+                   live, chunks, lane);
+    settle(q);
     int buf = 0;
     for (int key = first; key < end; key += kStep, buf ^= 1) {
         // the wave's reads of the other buffer are done before it is filled
@@ -626,7 +627,7 @@ __global__ __launch_bounds__(64 * kWaves, NB == 1 ? 3 : 2) void attention_few_ke
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            s[b][i] = __builtin_amdgcn_exp2f(s[b][i] * c - base);
+            s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], c, -base));
             st.l += s[b][i];
         }
         p[2 * b] = acc_frag(s[b], 0);
