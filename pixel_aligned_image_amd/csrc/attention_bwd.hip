@@ -25,6 +25,13 @@
 //
 // Where few tiles face a long axis the walked axis is cut into parts whose
 // binary32 sums go to the workspace and are joined by join_kernel.
+//
+// Bound by the matrix cores for heads of 128 (causal, 12,289 tokens, 12 heads
+// on 4: dq 0.67 ms, dkv 0.86 ms, 1.04 and 1.08 PFLOP/s of seen pairs) and by
+// the issue of vector next to matrix instructions for heads of 64 (7000
+// queries, 2 x 1029 keys, 16 heads: dq 78 us, dkv 84 and join 12; a SIMD's
+// vector and matrix units are busy 41 and 25 % of dq's time, 31 and 32 % of
+// dkv's).
 #include <algorithm>
 #include <type_traits>
 
@@ -334,6 +341,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
 // values stay in LDS: 32 registers more would leave two waves a SIMD nothing
 // to read fragments ahead into, and every matrix instruction would wait for
 // LDS (one wave a SIMD, with registers to spare, is held up by its own issue).
+// Heads of 64 leave room for three waves a SIMD (98 -> 89 us for 2 x 1029
+// keys, at the price of one register kept in memory outside the loop) and for
+// tiles of 64 rows (89 -> 85 us).
 template <int HD>
 __global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dkv_kernel(BwdArgs f) {
     using T = Tile<HD>;
@@ -347,8 +357,9 @@ __global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dkv_kernel(BwdA
     const int chunks = a.head_dim >> 3;
 
     // Causal: the parts of the longest tiles first, so that the last ones to
-    // run are short (12,289 tokens: 961 -> 878 us). Otherwise part by part, so
-    // that neighbours walk the same rows (2 x 1029 keys: 104 -> 96 us).
+    // run are short (12,289 tokens: 961 us the other way round, 878 this way).
+    // Otherwise part by part, so that neighbours walk the same rows (2 x 1029
+    // keys: 104 and 96 us).
     const int units = gridDim.x / f.splits;
     const int unit = a.causal ? blockIdx.x / f.splits : blockIdx.x % units;
     const int part = a.causal ? blockIdx.x % f.splits : blockIdx.x / units;

@@ -7,7 +7,10 @@
 // Both directions read every tensor once and keep a row in registers between
 // the read and the last write: the forward call moves 4 planes (x, y in; r, h
 // out), the backward call 6 (x, y, dh, dr in; dx, dy out), and nothing else
-// grows with the rows. Both are bound by memory. A row belongs to a group of
+// grows with the rows. Both are bound by memory: 100,000 rows of 1536 bf16
+// take 222 us forward (5.5 TB/s), 200,000 rows 448 us and backward 743 us (5.0
+// TB/s); 4096 rows of 1024 binary32, which stay in the caches, 14 and 24 us
+// with 5 us of sums; 5 rows 5 us, a launch. A row belongs to a group of
 // 16, 32, 64 or 256 threads, the smallest that holds it in at most VPT
 // 16-byte vectors each, so that its sums stay inside a wave wherever they can
 // (DPP, no LDS) and no lane idles on narrow rows.
@@ -23,7 +26,8 @@ namespace p3d {
 
 // About four workgroups per CU, and at least 16 rows each, so that the chunk
 // sums (12 bytes per column and chunk, written and read once) stay small
-// beside the rows.
+// beside the rows (4096 rows: 23 + 4.6 us with 16, 21 + 6.1 with 8, 26 + 9.4
+// with 4).
 int64_t norm_chunks(int64_t n, int32_t batch, const ItemTable& items, ItemTable* chunks) {
     const int64_t most = 4 * kComputeUnits;
     const int64_t rpc = std::max<int64_t>((n + most - 1) / most, 16);

@@ -5,7 +5,10 @@
 // element of its pair, C = m cos, S = -m sin for the first of the pair and
 // +m sin for the second; (C, S) = (1, 0) past the turned part. The gradient is
 // the same with S negated. Both directions read and write every element once
-// and are bound by memory.
+// and are bound by memory: 100,000 tokens of 24 bf16 heads of 128 take 220 us
+// (5.6 TB/s); 4096 tokens of binary32 heads, which stay in the caches, 14 us,
+// and 28 us backward with the gains' gradient, which is held up by the loads
+// of the few rows that a chunk has (4 us more for its sums).
 //
 // A group of P2 lanes (a power of two) holds one head, one 16-byte vector per
 // lane, so its rms sum stays inside a wave. The angles of a token do not
