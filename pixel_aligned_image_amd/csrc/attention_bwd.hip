@@ -9,13 +9,16 @@
 //   dkv kernel    a wave holds 32 keys and walks the query rows, with that D:
 //                 dV^T += dO^T P,  dK^T += Q^T dS
 //
-// A result is off by its own rounding to bf16, by that of dS (as large) and by
-// D's, which out's rounding and that of the forward call's P have moved: half
+// A result is off by its own rounding to bf16, by that of dS or P (as large) and
+// by D's, which out's rounding and that of the forward call's P have moved: half
 // as large where a row sees some ten keys, and less as the root of their
 // number. All three make 1.57 times the first alone on items of 11 keys, 1.43
 // on long ones. Rows that see few keys therefore take dS as the sum of two bf16
 // factors (1.24 there; another product on fragments already read, 40 % more
-// time if every row did), and dk takes the D that the dq kernel sums up (1.42).
+// time if every row did), items of a single tile of keys sum D up before dq uses
+// it (1.78 -> 1.0 on three keys), and dk takes the D that the dq kernel sums up
+// (1.42). dk and dv of a key that one or two rows see carry the rounding of
+// those rows' dS and P whole: 1.4 as a mean, up to 1.75 for a key alone.
 //
 // Each product's second factor is the softmax tile as the first product left
 // it in registers (attn_tile.h). The scores are computed twice, once per
@@ -108,7 +111,7 @@ __device__ __forceinline__ void sums_in_turn() {
 }
 
 template <int HD>
-__global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
+__global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dq_kernel(BwdArgs f) {
     using T = Tile<HD>;
     __shared__ uint4 kt[2][kWalk * T::kChunks];
     __shared__ uint4 vt[2][kWalk * T::kChunks];
@@ -302,8 +305,36 @@ __global__ __launch_bounds__(64 * kWaves, 2) void dq_kernel(BwdArgs f) {
             walk(fine, key + kWalk > all_see, buf, key);
         }
     };
+    // Rows of a single tile of keys are short enough for out's rounding to show
+    // in D (dq 1.78 times its own rounding off with three keys): they sum D up
+    // before they use it.
+    if (nk <= kWalk && begin < end) {
+        tile_barrier();
+        const uint32_t k_at = T::row_base(kt[0], lane), v_at = T::row_base(vt[0], lane);
+        float sum = 0.f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            f32x16 s, dp;
+            products(s, dp, k_at, v_at, b);
+            mask(s, 32 * b);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                sum = fmaf(__builtin_amdgcn_exp2f(fmaf(s[i], c, minus_lse2)), dp[i], sum);
+        }
+        float own;
+        const float other = other_half(sum, own);
+        minus_d = -(own + other);
+    }
     if (end <= kFineKeys) walk_all(std::true_type{});
     else walk_all(std::false_type{});
+
+    // A row that sees one key has P = 1 and dS = 0; P (dP - D) leaves a few
+    // 2^-24 of dP there, which would be all of dq.
+    if (live && (a.causal ? (int)token + nk - nq : nk - 1) == 0)
+#pragma unroll
+        for (int b = 0; b < T::kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dq[b][i] *= 0.f;
 
     float own;
     const float other = other_half(sum_d, own);
@@ -550,6 +581,12 @@ __global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dkv_kernel(BwdA
             walk(row + sub < all_from, buf, sub, row + sub);
         buf ^= 1;
     }
+
+    if (nk == 1)                             // (as in the dq kernel)
+#pragma unroll
+        for (int b = 0; b < T::kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dk[b][i] *= 0.f;
 
     if (f.splits > 1) {
         if (!live) return;

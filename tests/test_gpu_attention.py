@@ -98,6 +98,39 @@ def test_errors_on_the_whole():
             assert ref.rms_off(got[n], want[n]) < 2.0 ** -8, n
 
 
+@pytest.mark.parametrize("hd", [64, 96, 128])
+def test_errors_over_few_keys(hd):
+    """Rows of three keys: dq is off by its own rounding alone (dS is taken in
+    two factors, D from the same probabilities), 2^-8 / sqrt(3) at most, and
+    2^-6 of that for everything else."""
+    items = 60
+    q, k, v, dout = (t.cuda() for t in make(20 * items, 3 * items, 4, 4, hd, seed=hd))
+    off = [20 * b for b in range(items + 1)], [3 * b for b in range(items + 1)]
+    out, lse = forward(q, k, v, *off, hd ** -0.5, False)
+    got = backward(dout, q, k, v, out, lse, *off, hd ** -0.5, False)
+    want, _ = ref.attention_backward(ref.f64(dout), ref.f64(q), ref.f64(k), ref.f64(v), *off,
+                                     hd ** -0.5, False)
+    assert ref.rms_off(got["dq"], want["dq"]) < 2.0 ** -8 / 3 ** 0.5 * (1 + 2.0 ** -6)
+
+
+def test_rows_of_one_key():
+    """Their probability is 1 whatever the score: dq is 0, and dk of a key
+    that nothing else sees; also beside items that are cut into parts."""
+    for nq, nk, hd, causal in (([9], [1], 64, False), ([9], [1], 128, True),
+                               ([2, 700, 1], [1, 2500, 1], 128, False),
+                               ([1, 40], [1, 3000], 96, True)):
+        qo = [sum(nq[:b]) for b in range(len(nq) + 1)]
+        ko = [sum(nk[:b]) for b in range(len(nk) + 1)]
+        q, k, v, dout = (t.cuda() for t in make(qo[-1], ko[-1], 4, 2, hd, seed=hd))
+        out, lse = forward(q, k, v, qo, ko, 0.1, causal)
+        got = backward(dout, q, k, v, out, lse, qo, ko, 0.1, causal)
+        check_backward(got, dout, q, k, v, qo, ko, 0.1, causal)
+        for b, keys in enumerate(nk):
+            if keys == 1:
+                assert (got["dq"][qo[b]:qo[b + 1]] == 0).all()
+                assert (got["dk"][ko[b]:ko[b + 1]] == 0).all()
+
+
 def test_items_without_queries_or_keys():
     """Rows without keys give 0 and -inf, keys without queries gradient 0."""
     qo, ko = [0, 40, 40, 75, 90], [0, 0, 33, 70, 170]
