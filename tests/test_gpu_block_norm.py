@@ -215,3 +215,28 @@ def test_captured_in_a_graph():
         h.zero_()
         p3d.p3d_gated_norm(x, h, offsets=[0, 300, 700], r=r, **c)
         assert torch.equal(got, h)
+
+
+@pytest.mark.parametrize("over", ["x", "dh", "dr"])
+def test_in_place_gradient_of_ragged_chunks(over):
+    """dx over one of its inputs, chunks that do not fill their last turn, and
+    a last row whose dx is not finite: the columns' sums are those of the call
+    into a tensor of its own, and finite where dh and x are."""
+    for n, dim in ((17, 64), (33, 256), (18, 1024), (1041, 128)):
+        g = torch.Generator().manual_seed(n)
+        t = {k: torch.randn(n, dim, generator=g).cuda() for k in ("x", "dh", "dr")}
+        t["dr"][-1] = float("inf")
+
+        def call(dx, **kw):
+            sums = {k: torch.full((1, dim), float("nan"), device="cuda")
+                    for k in ("dscale", "dshift")}
+            a = t | kw
+            p3d.p3d_gated_norm_backward(a["dh"], a["x"], dx, dr=a["dr"], pre="rms", **sums)
+            return dx, sums
+
+        want, sums = call(torch.empty_like(t["x"]))
+        own = t[over].clone()
+        got, again = call(own, **{over: own})
+        assert torch.equal(got, want)
+        for k in sums:
+            assert torch.isfinite(sums[k]).all() and torch.equal(again[k], sums[k]), k
