@@ -479,7 +479,10 @@ hipError_t backward_as(const NormArgs& a, const ItemTable& items, const ItemTabl
 
 // The group of threads of a row of `nv` vectors, and its vectors per thread:
 // the smallest group that keeps a row's values in registers (the backward call
-// also its three sums: 24 columns a thread), else the whole workgroup.
+// also its three sums: 24 columns a thread), else the whole workgroup. Backward,
+// bf16 rows of 1536 take 755 us for 200,000 in a wave and 850 in a workgroup;
+// binary32 rows of 1536, whose packed vectors are twice as many registers, 991
+// us for 77,367 in a wave (71 registers spilled) and 600 in a workgroup.
 template <typename T>
 hipError_t forward_of(const NormArgs& a, const ItemTable& items, hipStream_t s) {
     const int nv = a.dim / Vec<T>::N;
