@@ -2,8 +2,9 @@
 
 torch hands a freed tensor's memory out again on its own stream at once. A
 call on a ``stream`` of its own may still be reading or writing it then, so
-such a call marks every tensor it is given (and a workspace it makes) as used
-on that stream. Calls on torch's current stream need none of this.
+such a call marks every tensor it is given as used on that stream, and a
+workspace that it makes is that stream's own. Calls on torch's current stream
+need none of this.
 """
 import functools
 import inspect
@@ -36,8 +37,12 @@ def lends(f):
 
 
 def fresh(nbytes, device, stream):
-    """A workspace of a call on ``stream`` (None: torch's current one)."""
-    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+    """A workspace of a call on ``stream`` (None: torch's current one). It is
+    allocated on that stream: a block of the current stream may be one that
+    was freed there while kernels which still use it are queued, and a call on
+    another stream does not wait for them. Freed, it goes back to the stream
+    that uses it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)

@@ -64,3 +64,45 @@ def test_dropped_tensors_wait_for_the_stream(call):
                           N * DIM * 4) for _ in range(8)]
     torch.cuda.synchronize()
     assert all(bool((t == 7).all()) for t in taken)
+
+
+def test_fresh_workspaces_are_no_blocks_in_use_elsewhere():
+    """Blocks freed on the current stream while work that writes them waits
+    there: a call on another stream, which does not wait for that work, gets
+    none of them as its workspace, and its results are those of a call alone."""
+    own = torch.cuda.Stream()
+    q = torch.randn(8, 8, 128, device="cuda").bfloat16()
+    k = torch.randn(8 * N, 1, 128, device="cuda").bfloat16()
+    x = torch.randn(N, DIM, device="cuda")
+    size = p3d.p3d_attention_workspace_size(q, k)
+    assert size > 1 << 20                    # the keys are split
+
+    def calls(stream):
+        out, dx, dw = torch.empty_like(q), torch.empty_like(x), torch.empty(DIM, device="cuda")
+        own.wait_stream(torch.cuda.current_stream())
+
+        def run():
+            p3d.p3d_attention(q, k, k, out, stream=stream)
+            p3d.p3d_gated_norm_backward(x, x, dx, dweight=dw, stream=stream)
+            return out, dx, dw
+
+        return run
+
+    alone = calls(None)()
+    torch.cuda.synchronize()
+    run = calls(own)                         # own waits for nothing after this
+    sizes = [size, p3d.p3d_gated_norm_workspace_size(x)]
+    taken = [torch.empty(s, dtype=torch.uint8, device="cuda") for s in sizes for _ in range(3)]
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in taken]
+    torch.cuda._sleep(SPIN // 10)
+    for _ in range(20):
+        for t in taken:
+            t.fill_(255)                     # NaN, were it read as sums
+    del taken, t
+    from pixel_aligned_image_amd import _streams
+    for s in sizes:
+        at = _streams.fresh(s, "cuda", own).data_ptr()
+        assert not any(a < at + s and at < b for a, b in spans)
+    got = run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(alone, got))
