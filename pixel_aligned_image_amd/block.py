@@ -79,8 +79,9 @@ def bind(core):
 
 # ----------------------------------------------------------------- helpers ---
 def make_offsets(offsets):
-    """ctypes int64 array of an item table (batch + 1 row numbers)."""
-    if isinstance(offsets, ctypes.Array):
+    """ctypes int64 array of an item table (batch + 1 row numbers). Only an
+    int64 array is passed on as it is: the library reads 8 bytes an entry."""
+    if isinstance(offsets, ctypes.Array) and offsets._type_ is _i64:
         return offsets
     return (_i64 * len(offsets))(*offsets)
 

@@ -327,3 +327,19 @@ def test_binding_checks(p3d):
         p3d.p3d_attention(h, h, h, h, [0, 4], [0, 2, 4])
     with pytest.raises(KeyError):
         p3d.p3d_gated_norm(x, x, pre="batch")
+
+
+def test_item_tables_of_other_types(p3d):
+    """The library reads int64 entries: an array of another type is converted,
+    one that holds no integers refused, an int64 array reused."""
+    table = offsets(0, 0, 4)
+    assert p3d.make_offsets(table) is table
+    for kind in (ctypes.c_int32, ctypes.c_uint32, ctypes.c_int16):
+        made = p3d.make_offsets((kind * 3)(0, 0, 4))
+        assert made._type_ is ctypes.c_int64 and list(made) == [0, 0, 4]
+    with pytest.raises(TypeError):
+        p3d.make_offsets((ctypes.c_double * 2)(0.0, 4.0))
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    # 12 bytes, of which int64 entries would be read past the end
+    assert p3d.p3d_gated_norm_workspace_size(x, (ctypes.c_int32 * 3)(0, 0, 4)) == \
+        p3d.p3d_gated_norm_workspace_size(x, [0, 0, 4])
