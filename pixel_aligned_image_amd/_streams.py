@@ -12,9 +12,18 @@ import inspect
 import torch
 
 
+def _as_torch(stream):
+    """What torch knows as the stream of a call: the calls take any object
+    with a ``cuda_stream`` handle."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream)
+
+
 def _mark(v, stream):
     if isinstance(v, torch.Tensor):
-        v.record_stream(stream)
+        if v.is_cuda:                        # (cameras may come as a CPU tensor)
+            v.record_stream(stream)
     elif isinstance(v, (list, tuple)):
         for x in v:
             _mark(x, stream)
@@ -26,8 +35,8 @@ def lends(f):
 
     @functools.wraps(f)
     def call(*args, **kw):
+        stream = _as_torch(kw.get("stream") if len(args) <= at else args[at])
         result = f(*args, **kw)
-        stream = kw.get("stream") if len(args) <= at else args[at]
         if stream is not None:
             _mark(args, stream)
             _mark(list(kw.values()), stream)
@@ -44,5 +53,5 @@ def fresh(nbytes, device, stream):
     that uses it."""
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_as_torch(stream)):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)

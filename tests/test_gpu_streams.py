@@ -106,3 +106,39 @@ def test_fresh_workspaces_are_no_blocks_in_use_elsewhere():
     got = run()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(alone, got))
+
+
+class Handle:
+    """A stream of another library: a handle and nothing else."""
+
+    def __init__(self, stream):
+        self.cuda_stream, self.keep = stream.cuda_stream, stream
+
+
+@pytest.mark.parametrize("call", [gated_norm, norm_backward, rotary, attention, sample,
+                                  token_order], ids=lambda f: f.__name__)
+def test_any_object_with_a_handle_is_a_stream(call):
+    """The calls read no more of a stream than its handle; tensors dropped
+    after such a call wait for it, too."""
+    own = torch.cuda.Stream()
+    call(Handle(own))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(own):
+        torch.cuda._sleep(SPIN)
+    own.wait_stream(torch.cuda.current_stream())
+    call(Handle(own))
+    assert not own.query()
+    taken = [torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+             for size in (512, 1 << 14, 1 << 18, N * DIM * 2, N * DIM * 4) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(bool((t == 7).all()) for t in taken)
+
+
+def test_cameras_as_a_cpu_tensor_on_a_stream():
+    coords = torch.zeros(N, 4, dtype=torch.int32, device="cuda")
+    order = torch.full((N,), -1, dtype=torch.int32, device="cuda")
+    own = torch.cuda.Stream()
+    own.wait_stream(torch.cuda.current_stream())
+    p3d.p3d_token_order(coords, N, 64, torch.tensor([[1.0, 2.0]]), 32, 32, order, stream=own)
+    torch.cuda.synchronize()
+    assert torch.equal(order.sort().values, torch.arange(N, dtype=torch.int32, device="cuda"))
