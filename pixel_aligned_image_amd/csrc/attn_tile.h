@@ -68,7 +68,7 @@ __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // 64 lanes x 4 bytes into 256 bytes of LDS, lane l at 4 l.
@@ -76,7 +76,7 @@ __device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // dma16 from a uniform base and a 32-bit offset per lane.
@@ -87,7 +87,7 @@ __device__ __forceinline__ void dma16_from(const void* from, uint32_t offset, ui
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {

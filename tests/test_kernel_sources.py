@@ -1,0 +1,35 @@
+"""Rules of the kernel sources that no run shows while they happen to hold.
+CPU only."""
+import glob
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SOURCES = sorted(glob.glob(os.path.join(ROOT, "pixel_aligned_image_amd", "csrc", "*")))
+
+
+def statements(text):
+    """The asm statements of a source: what stands in each one's brackets."""
+    text = re.sub(r"//[^\n]*", "", text)
+    for m in re.finditer(r"\basm\b\s*(?:volatile)?\s*\(", text):
+        depth, at = 1, m.end()
+        while depth:
+            depth += {"(": 1, ")": -1}.get(text[at], 0)
+            at += 1
+        yield text[m.end():at - 1]
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_assembly_names_the_registers_it_writes(path):
+    """m0 is no operand: the compiler learns of a write from the list only."""
+    for s in statements(open(path).read()):
+        if re.search(r"\b[sv]_\w+\s+m0\b", s):
+            assert re.search(r':[^:]*"m0"[^:]*$', s), s
+
+
+def test_the_rule_sees_a_write():
+    writes = list(statements('asm volatile("s_mov_b32 m0, %0" :: "s"(f(x)) : "memory");'))
+    assert len(writes) == 1 and re.search(r"\b[sv]_\w+\s+m0\b", writes[0])
+    assert not re.search(r':[^:]*"m0"[^:]*$', writes[0])
