@@ -269,8 +269,8 @@ __device__ __forceinline__ void store_part(const FwdArgs& f, const Softmax<HD>& 
 template <int HD>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(FwdArgs f) {
     using T = Tile<HD>;
-    __shared__ uint4 kt[2][kKeys * T::kChunks];
-    __shared__ uint4 vt[3][kKeys * T::kChunks];
+    __shared__ alignas(kTileAlign) uint4 kt[2][kKeys * T::kChunks];
+    __shared__ alignas(kTileAlign) uint4 vt[3][kKeys * T::kChunks];
     const AttnArgs& a = f.a;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -421,7 +421,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
     using T = Tile<HD>;
     constexpr int kTile = kSingleKeys * T::kChunks;
     constexpr int kLoads = 2 * kSingleKeys * T::kChunks / 64;
-    __shared__ uint4 tiles[kWaves][2][2][kTile];         // [wave][buffer][k, v]
+    __shared__ alignas(kTileAlign) uint4 tiles[kWaves][2][2][kTile];  // [wave][buffer][k, v]
     __shared__ float2 ml[kWaves][32];
     const AttnArgs& a = f.a;
     const int lane = threadIdx.x & 63;
@@ -563,9 +563,9 @@ template <int HD, int NB>
 __global__ __launch_bounds__(64 * kWaves, NB == 1 ? 3 : 2) void attention_few_kernel(FwdArgs f,
                                                                                      bool nt) {
     using T = Tile<HD>;
-    __shared__ uint4 kt[32 * NB * T::kChunks];
-    __shared__ uint4 vt[32 * NB * T::kChunks];
-    __shared__ uint4 rows_lds[kWaves][32 * T::kChunks];
+    __shared__ alignas(kTileAlign) uint4 kt[32 * NB * T::kChunks];
+    __shared__ alignas(kTileAlign) uint4 vt[32 * NB * T::kChunks];
+    __shared__ alignas(kTileAlign) uint4 rows_lds[kWaves][32 * T::kChunks];
     const AttnArgs& a = f.a;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -113,8 +113,8 @@ __device__ __forceinline__ void sums_in_turn() {
 template <int HD>
 __global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dq_kernel(BwdArgs f) {
     using T = Tile<HD>;
-    __shared__ uint4 kt[2][kWalk * T::kChunks];
-    __shared__ uint4 vt[2][kWalk * T::kChunks];
+    __shared__ alignas(kTileAlign) uint4 kt[2][kWalk * T::kChunks];
+    __shared__ alignas(kTileAlign) uint4 vt[2][kWalk * T::kChunks];
     const AttnArgs& a = f.a;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -379,8 +379,9 @@ template <int HD>
 __global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dkv_kernel(BwdArgs f) {
     using T = Tile<HD>;
     constexpr int kRows = HD <= 64 ? 64 : 32;
-    __shared__ uint4 tiles[2][2 * kRows * T::kChunks];   // [buffer][q rows, dout rows]
-    __shared__ uint4 values[kHeld * T::kChunks];
+    // [buffer][q rows, dout rows]
+    __shared__ alignas(kTileAlign) uint4 tiles[2][2 * kRows * T::kChunks];
+    __shared__ alignas(kTileAlign) uint4 values[kHeld * T::kChunks];
     __shared__ alignas(16) float stats[2][2][64];        // [buffer][-lse / scale, -D]
     const AttnArgs& a = f.a;
     const int lane = threadIdx.x & 63, h = lane >> 5;

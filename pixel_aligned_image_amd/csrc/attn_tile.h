@@ -98,7 +98,11 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // up to 128). Chunk c of row r sits at slot c ^ swizzle(r). Two kinds of read
 // have to spread over the banks (a 256-byte window): 16 consecutive rows at
 // one chunk (row fragments), and 4 consecutive rows at 4 neighbouring chunks
-// (transposed fragments); the swizzle separates both.
+// (transposed fragments); the swizzle separates both. A fragment's chunk is an
+// exclusive or on a byte address, so a tile starts on a whole row: its array is
+// declared with alignas(kTileAlign), and tiles inside it are whole rows apart.
+constexpr int kTileAlign = 256;
+
 template <int HD>
 struct Tile {
     static constexpr int kChunks = HD <= 64 ? 8 : 16;

@@ -33,3 +33,18 @@ def test_the_rule_sees_a_write():
     writes = list(statements('asm volatile("s_mov_b32 m0, %0" :: "s"(f(x)) : "memory");'))
     assert len(writes) == 1 and re.search(r"\b[sv]_\w+\s+m0\b", writes[0])
     assert not re.search(r':[^:]*"m0"[^:]*$', writes[0])
+
+
+def test_attention_tiles_start_on_whole_rows():
+    """Fragments reach a chunk by an exclusive or on the byte address."""
+    seen = 0
+    for path in SOURCES:
+        text = open(path).read()
+        if '#include "attn_tile.h"' not in text:
+            continue
+        for line in re.findall(r"^.*__shared__.*\buint4\b.*$", text, re.M):
+            assert "alignas(kTileAlign)" in line, (path, line)
+            seen += 1
+    assert seen >= 10
+    text = open(os.path.join(ROOT, "pixel_aligned_image_amd", "csrc", "attn_tile.h")).read()
+    assert int(re.search(r"kTileAlign = (\d+);", text).group(1)) == 256
