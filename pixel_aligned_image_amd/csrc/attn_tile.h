@@ -62,21 +62,22 @@ __device__ __forceinline__ void wave_wait() {
 // 64 lanes x 16 bytes from global memory into 1 KB of LDS at the uniform byte
 // offset `lds`, lane l at 16 l; lanes that are switched off write nothing. The
 // instruction is written out so that the compiler does not wait for it at the
-// next LDS read: the waits above are the only ones that cover it. (A write of
-// m0 needs one wait state before a load to LDS.)
+// next LDS read: the waits above are the only ones that cover it. The LDS
+// offset goes in m0, an operand, so the compiler writes it. (A write of m0
+// needs one wait state before a load to LDS.)
 __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
-                 : "memory", "m0");
+                 : "{m0}"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
+                 : "memory");
 }
 
 // 64 lanes x 4 bytes into 256 bytes of LDS, lane l at 4 l.
 __device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
-                 : "memory", "m0");
+                 : "{m0}"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
+                 : "memory");
 }
 
 // dma16 from a uniform base and a 32-bit offset per lane.
@@ -84,10 +85,10 @@ __device__ __forceinline__ void dma16_from(const void* from, uint32_t offset, ui
     const uint64_t at = (uint64_t)(uintptr_t)from;
     const uint64_t base = ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32) |
                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
-                 : "memory", "m0");
+                 : "{m0}"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {

@@ -23,10 +23,13 @@ def statements(text):
 
 @pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
 def test_assembly_names_the_registers_it_writes(path):
-    """m0 is no operand: the compiler learns of a write from the list only."""
+    """The compiler learns of a write to m0 from the list only; a load to LDS,
+    which reads it, takes it as an operand, so that the compiler writes it."""
     for s in statements(open(path).read()):
         if re.search(r"\b[sv]_\w+\s+m0\b", s):
             assert re.search(r':[^:]*"m0"[^:]*$', s), s
+        if "load_lds" in s:
+            assert '"{m0}"(' in s, s
 
 
 def test_the_rule_sees_a_write():
