@@ -218,7 +218,8 @@ p3d_status p3d_rotary_frequencies(double base, int32_t pairs, p3d_rotary_scaling
  *                nk the last entries of q_offsets and k_offsets; a token's
  *                heads are contiguous, tokens are *_stride elements apart (a
  *                multiple of 8), so views of a packed qkv need no copy;
- *                out may be q with equal strides
+ *                out may be q with equal strides, and must not overlap q
+ *                otherwise, nor k or v (checked as the gradients' tensors are)
  *   head_dim     a multiple of 8, 8..128; heads a multiple of kv_heads,
  *                heads <= 1024
  *   scale        finite, > 0
@@ -254,8 +255,10 @@ p3d_status p3d_attention(const p3d_attn_desc* desc, const void* q, int64_t q_str
  * queries that see at most 256 keys, for dq, as the sum of two bf16 numbers).
  * dk, and dq of items of at most 64 keys, take D_i as sum_j P_ij dout_i . v_j,
  * the same number without out's rounding. Rows that nothing reaches get 0, and
- * so does dq of a query that sees one key (its probability is 1). dq, dk and dv are strided like q, k and v, are
- * overwritten and must not overlap another tensor of the call. */
+ * so does dq of a query that sees one key (its probability is 1). dq, dk and dv
+ * are strided like q, k and v, are overwritten and must not overlap another
+ * tensor of the call (P3D_ERR_INVALID_ARG where the two have equal strides,
+ * one has a single row or both start at one place; not looked for otherwise). */
 size_t p3d_attention_backward_workspace_size(const p3d_attn_desc* desc);
 p3d_status p3d_attention_backward(const p3d_attn_desc* desc, const void* dout,
                                   int64_t dout_stride, const void* q, int64_t q_stride,

@@ -251,6 +251,46 @@ p3d_status check_attention(const char* fn, const p3d_attn_desc* d, AttnArgs* a) 
     return P3D_OK;
 }
 
+// The bytes of a [rows, width] tensor, rows `pitch` bytes apart.
+struct Rows {
+    const char* name;
+    const void* base;
+    int64_t rows, width, pitch;
+};
+
+int64_t floor_div(int64_t a, int64_t b) { return a >= 0 ? a / b : -((b - 1 - a) / b); }
+
+// Whether the single row `a` shares a byte with `b`: the first of b's rows that
+// ends behind a's start begins before a's end.
+bool row_meets(const Rows& a, const Rows& b) {
+    const int64_t at = static_cast<const char*>(a.base) - static_cast<const char*>(b.base);
+    const int64_t row = at < b.width ? 0 : floor_div(at - b.width, b.pitch) + 1;
+    return row < b.rows && row * b.pitch < at + a.width;
+}
+
+// Whether two tensors share a byte: decided where their rows are equally far
+// apart (views of one packed buffer), one of them has a single row, or both
+// start at one place.
+bool overlap(const Rows& a, const Rows& b) {
+    if (a.rows == 0 || b.rows == 0) return false;
+    if (a.base == b.base) return true;
+    if (a.rows == 1) return row_meets(a, b);
+    if (b.rows == 1) return row_meets(b, a);
+    if (a.pitch != b.pitch) return false;
+    // b's row 0 starts `column` bytes into row `down` of a's raster
+    const int64_t apart = static_cast<const char*>(b.base) - static_cast<const char*>(a.base);
+    const int64_t down = floor_div(apart, a.pitch), column = apart - down * a.pitch;
+    const auto meet = [&](int64_t by) { return by < a.rows && by + b.rows > 0; };
+    return (column < a.width && meet(down)) || (column + b.width > a.pitch && meet(down + 1));
+}
+
+p3d_status check_apart(const char* fn, const Rows& written, const Rows& other) {
+    if (overlap(written, other))
+        return set_error(P3D_ERR_INVALID_ARG, "%s: %s must not overlap %s", fn, written.name,
+                         other.name);
+    return P3D_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -475,6 +515,11 @@ p3d_status p3d_attention(const p3d_attn_desc* desc, const void* q, int64_t q_str
     const AttnPlan plan = attention_plan(a);
     P3D_TRY(check_workspace(fn, "p3d_attention_workspace_size", workspace, workspace_bytes,
                             (plan.forward_bytes + 255) / 256 * 256));
+    const int64_t nq = a.q_items.start[a.batch], nk = a.k_items.start[a.batch];
+    const Rows written{"out", out, nq, 2 * wq, 2 * out_stride};
+    P3D_TRY(check_apart(fn, written, {"k", k, nk, 2 * wk, 2 * k_stride}));
+    P3D_TRY(check_apart(fn, written, {"v", v, nk, 2 * wk, 2 * v_stride}));
+    if (out != q) P3D_TRY(check_apart(fn, written, {"q", q, nq, 2 * wq, 2 * q_stride}));
     a.q = q;
     a.k = k;
     a.v = v;
@@ -520,6 +565,18 @@ p3d_status p3d_attention_backward(const p3d_attn_desc* desc, const void* dout,
     const AttnPlan plan = attention_plan(a);
     P3D_TRY(check_workspace(fn, "p3d_attention_backward_workspace_size", workspace,
                             workspace_bytes, (plan.backward_bytes + 255) / 256 * 256));
+    const int64_t nq = a.q_items.start[a.batch], nk = a.k_items.start[a.batch];
+    const Rows tensors[] = {{"dq", dq, nq, 2 * wq, 2 * dq_stride},
+                            {"dk", dk, nk, 2 * wk, 2 * dk_stride},
+                            {"dv", dv, nk, 2 * wk, 2 * dv_stride},
+                            {"dout", dout, nq, 2 * wq, 2 * dout_stride},
+                            {"q", q, nq, 2 * wq, 2 * q_stride},
+                            {"k", k, nk, 2 * wk, 2 * k_stride},
+                            {"v", v, nk, 2 * wk, 2 * v_stride},
+                            {"out", out, nq, 2 * wq, 2 * out_stride},
+                            {"lse", lse, nq, 4 * (int64_t)a.heads, 4 * (int64_t)a.heads}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 9; ++j) P3D_TRY(check_apart(fn, tensors[i], tensors[j]));
     a.dout = dout;
     a.q = q;
     a.k = k;

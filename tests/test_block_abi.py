@@ -343,3 +343,65 @@ def test_item_tables_of_other_types(p3d):
     # 12 bytes, of which int64 entries would be read past the end
     assert p3d.p3d_gated_norm_workspace_size(x, (ctypes.c_int32 * 3)(0, 0, 4)) == \
         p3d.p3d_gated_norm_workspace_size(x, [0, 0, 4])
+
+
+def test_attention_results_do_not_overlap(p3d):
+    """Results over an input or over each other: equal tensors, views of one
+    packed buffer whose columns or rows meet, a single row inside another
+    tensor."""
+    lib, d = p3d.lib, attn_desc(p3d)         # 16 queries of 8 heads, 20 keys of 2, heads of 64
+    step = 1 << 20
+    fn = "p3d_attention_backward"
+    need = lib.p3d_attention_backward_workspace_size(d)
+    names = ["dout", "q", "k", "v", "out", "dq", "dk", "dv"]
+    wide = {"dout": 512, "q": 512, "k": 128, "v": 128, "out": 512, "dq": 512, "dk": 128,
+            "dv": 128}
+    apart = {n: FAKE + (i + 1) * step for i, n in enumerate(names)}
+    lse = FAKE + 20 * step
+
+    def back(d=d, need=need, lse=lse, stride=None, **at):
+        args = []
+        for n in names:
+            args += [at.get(n, apart[n]), stride or wide[n]]
+        return lib.p3d_attention_backward(d, *args[:10], lse, *args[10:], FAKE, need, None)
+
+    for n in ("dq", "dk", "dv"):
+        for other in names:
+            if n != other:
+                refused(p3d, back(**{n: apart[other]}), INVALID, "must not overlap", fn)
+        refused(p3d, back(**{n: lse}), INVALID, n + " must not overlap lse", fn)
+    # one packed buffer of 1600 columns: 2 * 128 of dk from column 512 on
+    base = FAKE + 64 * step
+    for at in (512 - 8, 512 + 8, 512, 512 - 120, 512 + 120):
+        refused(p3d, back(stride=1600, dk=base + 2 * 512, dv=base + 2 * at), INVALID,
+                "dk must not overlap dv", fn)
+    # a row further down, and one that runs on into the next row's first columns
+    refused(p3d, back(stride=1600, dk=base, dv=base + 2 * (1600 * 19 + 64)), INVALID,
+            "dk must not overlap dv", fn)
+    refused(p3d, back(stride=1600, dk=base, dv=base + 2 * (1600 - 64)), INVALID,
+            "dk must not overlap dv", fn)
+    refused(p3d, back(stride=1600, dv=base, dk=base + 2 * (1600 - 64)), INVALID,
+            "dk must not overlap dv", fn)
+    # one query's row of 512 over the keys' rows of 128: inside, from before, at the end
+    one = attn_desc(p3d, q=offsets(0, 1, 1))
+    need_one = lib.p3d_attention_backward_workspace_size(one)
+    for at in (128 * 3, -504, 128 * 20 - 8):
+        refused(p3d, back(d=one, need=need_one, dq=apart["dk"] + 2 * at), INVALID,
+                "dq must not overlap dk", fn)
+        refused(p3d, back(d=one, need=need_one, dk=apart["q"] - 2 * at), INVALID,
+                "dk must not overlap q", fn)
+
+    fn = "p3d_attention"
+    need_f = lib.p3d_attention_workspace_size(d)
+
+    def fwd(q=apart["q"], k=apart["k"], v=apart["v"], out=apart["out"], stride=None):
+        args = []
+        for n, p in (("q", q), ("k", k), ("v", v), ("out", out)):
+            args += [p, stride or wide[n]]
+        return lib.p3d_attention(d, *args, None, FAKE, need_f, None)
+
+    refused(p3d, fwd(out=apart["k"]), INVALID, "out must not overlap k", fn)
+    refused(p3d, fwd(out=apart["v"]), INVALID, "out must not overlap v", fn)
+    refused(p3d, fwd(stride=1600, q=base, out=base + 2 * 8), INVALID, "out must not overlap q", fn)
+    refused(p3d, fwd(stride=1600, q=base, out=base + 2 * 1600), INVALID, "out must not overlap q",
+            fn)
