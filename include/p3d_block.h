@@ -252,7 +252,9 @@ p3d_status p3d_attention(const p3d_attn_desc* desc, const void* q, int64_t q_str
  *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,
  *   dv_j = sum_i P_ij dout_i       (dk, dv: summed over the group's heads)
  * P and dS are rounded to bf16 as factors of the last three products (dS of
- * queries that see at most 256 keys, for dq, as the sum of two bf16 numbers).
+ * queries that see at most 256 keys, and of those that share one of the
+ * launch's 128-row tiles with such a query, for dq, as the sum of two bf16
+ * numbers).
  * dk, and dq of items of at most 64 keys, take D_i as sum_j P_ij dout_i . v_j,
  * the same number without out's rounding. Rows that nothing reaches get 0, and
  * so does dq of a query that sees one key (its probability is 1). dq, dk and dv

@@ -49,7 +49,7 @@ using namespace attn;
 constexpr int kWaves = 4;
 constexpr int kHeld = 32 * kWaves;       // rows (dq) or keys (dkv) held by a workgroup
 constexpr int kWalk = 64;                // keys of a tile that the dq kernel walks
-constexpr int kFineKeys = 256;           // rows seeing so many take dS in two factors
+constexpr int kFineKeys = 256;           // rows seeing at most so many take dS in two factors
 
 struct BwdArgs {
     AttnArgs a;
@@ -138,11 +138,13 @@ __global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dq_kernel(BwdAr
     part = (part + kWalk - 1) / kWalk * kWalk;
     const int begin = (int)min((int64_t)blockIdx.y * part, (int64_t)nk);
     int end = (int)min((int64_t)begin + part, (int64_t)nk);
-    int limit = end;
+    int limit = end, fewest = nk;            // fewest: keys that the tile's first row sees
     if (a.causal) {
         limit = min(end, live ? (int)token + nk - nq + 1 : end);
-        uint32_t last, m;
+        uint32_t first, last, m;
+        f.group.split(row0, first, m);
         f.group.split(min(row0 + kHeld, rows) - 1, last, m);
+        fewest = (int)first + nk - nq + 1;
         end = min(end, (int)last + nk - nq + 1);
     }
     const int all_see = __builtin_amdgcn_readfirstlane(limit);
@@ -325,7 +327,9 @@ __global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dq_kernel(BwdAr
         const float other = other_half(sum, own);
         minus_d = -(own + other);
     }
-    if (end <= kFineKeys) walk_all(std::true_type{});
+    // (by the item and the rows, not by this part's keys: how the launch is cut
+    // does not change a rounding)
+    if (fewest <= kFineKeys) walk_all(std::true_type{});
     else walk_all(std::false_type{});
 
     // A row that sees one key has P = 1 and dS = 0; P (dP - D) leaves a few

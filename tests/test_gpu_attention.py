@@ -315,3 +315,37 @@ def test_repeatable_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(first, (out, lse, *grads)))
         once()                                   # eager work between the replays
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_two_factors_reach_every_row_of_few_keys(hd):
+    """Rows that see 130 to 256 keys, in a launch whose tile of rows ends on
+    257 and in one whose tile ends on 256: dq takes dS as two factors in both,
+    so the same rows get the same bits."""
+    nq, nk, heads = 256, 257, 2
+    q, k, v, dout = (t.cuda() for t in make(nq, nk, heads, heads, hd, seed=12))
+    out, lse = forward(q, k, v, [0, nq], [0, nk], 0.1, True)
+    whole = backward(dout, q, k, v, out, lse, [0, nq], [0, nk], 0.1, True)["dq"]
+    rows = slice(128, 255)
+    part = backward(dout[rows], q[rows], k[:256], v[:256], out[rows], lse[rows], [0, 127],
+                    [0, 256], 0.1, True)["dq"]
+    assert torch.equal(whole[rows], part)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_roundings_do_not_depend_on_the_parts(hd):
+    """512 keys walked whole and in two parts; the second half's probabilities
+    are 0, so that the parts' sums add nothing: the same rows get the same
+    bits, however many parts the launch has."""
+    few, many, nk = 64, 32768, 512
+    q, k, v, dout = (t.cuda() for t in make(many, nk, 1, 1, hd, seed=13))
+    q[:, 0, 0], k[:256, 0, 0], k[256:, 0, 0] = 64, 0, -64
+    off = [0, few], [0, nk]
+    # the parts' workspace shows that one launch is cut and the other is not
+    stats = 256 + 2 * 512
+    assert p3d.p3d_attention_backward_workspace_size(q[:few], k, *off) >= stats + \
+        2 * few * (hd + 1) * 4
+    out, lse = forward(q, k, v, [0, many], [0, nk], 0.125, False)
+    whole = backward(dout, q, k, v, out, lse, [0, many], [0, nk], 0.125, False)["dq"]
+    part = backward(dout[:few], q[:few], k, v, out[:few], lse[:few], *off, 0.125, False)["dq"]
+    assert torch.equal(whole[:few], part)
