@@ -503,7 +503,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attention_single_kernel(FwdArg
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
         const float2 v = ml[w][row];
-        l += m == -INFINITY ? 0.f : v.y * __builtin_amdgcn_exp2f((v.x - m) * c);
+        // (no maximum: the sums are 0, or NaN where the scores were)
+        l += m == -INFINITY ? v.y : v.y * __builtin_amdgcn_exp2f((v.x - m) * c);
     }
     // [wave][register][lane]; the tiles are no longer read
     float* joint = reinterpret_cast<float*>(&tiles[0][0][0][0]);

@@ -349,3 +349,18 @@ def test_roundings_do_not_depend_on_the_parts(hd):
     whole = backward(dout, q, k, v, out, lse, [0, many], [0, nk], 0.125, False)["dq"]
     part = backward(dout[:few], q[:few], k, v, out[:few], lse[:few], *off, 0.125, False)["dq"]
     assert torch.equal(whole[:few], part)
+
+
+@pytest.mark.parametrize("keys", [40, 500, 5000])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_rows_of_nan_say_so(rows, keys):
+    """A query of NaN gives NaN in out and in lse (-inf is what a query that
+    sees no key gets), for single tokens and for many, and its neighbours what
+    they gave without it."""
+    q, k, v, _ = (t.cuda() for t in make(rows * 2, keys, 2, 1, 128, seed=14))
+    off = [0, rows, 2 * rows], [0, keys // 2, keys]
+    want, lse_want = forward(q, k, v, *off, 0.1, False)
+    q[0] = float("nan")
+    out, lse = forward(q, k, v, *off, 0.1, False)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.equal(out[rows:], want[rows:]) and torch.equal(lse[rows:], lse_want[rows:])
