@@ -222,7 +222,7 @@ p3d_status p3d_rotary_frequencies(double base, int32_t pairs, p3d_rotary_scaling
  *                otherwise, nor k or v (checked as the gradients' tensors are)
  *   head_dim     a multiple of 8, 8..128; heads a multiple of kv_heads,
  *                heads <= 1024
- *   scale        finite, > 0
+ *   scale        finite, > 0, at most 2^127 (the gradient: at least 2^-100)
  *   lse          float [nq, heads] (natural logarithm) or NULL
  *   Alignment: 16 bytes (lse: 4). nq * heads and nk * kv_heads < 2^30.
  *   workspace    p3d_attention_workspace_size(desc) bytes (few queries over

@@ -231,6 +231,9 @@ p3d_status check_attention(const char* fn, const p3d_attn_desc* d, AttnArgs* a) 
     if (!(isfinite(d->scale) && d->scale > 0.f))
         return set_error(P3D_ERR_INVALID_ARG, "%s: scale must be finite and > 0, got %g", fn,
                          (double)d->scale);
+    if (d->scale > 0x1p127f)                 // scale log2(e) has to be finite
+        return set_error(P3D_ERR_UNSUPPORTED, "%s: scale must be at most 2^127, got %g", fn,
+                         (double)d->scale);
     if (d->causal != 0 && d->causal != 1)
         return set_error(P3D_ERR_INVALID_ARG, "%s: causal must be 0 or 1, got %d", fn, d->causal);
     *a = AttnArgs{};
@@ -248,6 +251,15 @@ p3d_status check_attention(const char* fn, const p3d_attn_desc* d, AttnArgs* a) 
     a->head_dim = d->head_dim;
     a->causal = d->causal;
     a->scale = d->scale;
+    return P3D_OK;
+}
+
+// The gradient divides lse by the scale, which has to stay finite.
+p3d_status check_attention_backward(const char* fn, const p3d_attn_desc* d, AttnArgs* a) {
+    P3D_TRY(check_attention(fn, d, a));
+    if (d->scale < 0x1p-100f)
+        return set_error(P3D_ERR_UNSUPPORTED, "%s: scale must be at least 2^-100, got %g", fn,
+                         (double)d->scale);
     return P3D_OK;
 }
 
@@ -486,7 +498,8 @@ size_t p3d_attention_workspace_size(const p3d_attn_desc* desc) {
 
 size_t p3d_attention_backward_workspace_size(const p3d_attn_desc* desc) {
     AttnArgs a;
-    if (check_attention("p3d_attention_backward_workspace_size", desc, &a) != P3D_OK) return 0;
+    if (check_attention_backward("p3d_attention_backward_workspace_size", desc, &a) != P3D_OK)
+        return 0;
     set_ok();
     return (attention_plan(a).backward_bytes + 255) / 256 * 256;
 }
@@ -542,7 +555,7 @@ p3d_status p3d_attention_backward(const p3d_attn_desc* desc, const void* dout,
                                   void* workspace, size_t workspace_bytes, void* stream) {
     const char* fn = "p3d_attention_backward";
     AttnArgs a;
-    P3D_TRY(check_attention(fn, desc, &a));
+    P3D_TRY(check_attention_backward(fn, desc, &a));
     const bool queries = a.q_items.start[a.batch] > 0, keys = a.k_items.start[a.batch] > 0;
     const int64_t wq = (int64_t)a.heads * a.head_dim, wk = (int64_t)a.kv_heads * a.head_dim;
     P3D_TRY(check_tensor(fn, "dout", dout, queries));

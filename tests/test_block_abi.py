@@ -405,3 +405,24 @@ def test_attention_results_do_not_overlap(p3d):
     refused(p3d, fwd(stride=1600, q=base, out=base + 2 * 8), INVALID, "out must not overlap q", fn)
     refused(p3d, fwd(stride=1600, q=base, out=base + 2 * 1600), INVALID, "out must not overlap q",
             fn)
+
+
+def test_attention_scales_at_the_ends_of_binary32(p3d):
+    """scale log2(e) and, in the gradient, lse / scale have to be finite: past
+    that the answers were NaN for scores of 0, and gradients of 0."""
+    lib = p3d.lib
+    f32 = ctypes.c_float
+    assert math.isinf(f32(2.0 ** 127 * 1.5 * math.log2(math.e)).value)
+    assert math.isinf(f32(math.log(20) / 2.0 ** -127).value)
+    d = attn_desc(p3d, scale=2.0 ** 127 * 1.5)
+    args = [FAKE, 1 << 20] * 4, [FAKE, 1 << 20] * 5, [FAKE, 1 << 20] * 3
+    refused(p3d, lib.p3d_attention(d, *args[0], None, FAKE, 1 << 40, None), UNSUPPORTED, "2^127",
+            "p3d_attention")
+    assert lib.p3d_attention_workspace_size(d) == 0
+    d = attn_desc(p3d, scale=2.0 ** -101)
+    assert lib.p3d_attention_workspace_size(d) > 0
+    assert lib.p3d_attention_backward_workspace_size(d) == 0
+    refused(p3d, lib.p3d_attention_backward(d, *args[1], FAKE, *args[2], FAKE, 1 << 40, None),
+            UNSUPPORTED, "2^-100", "p3d_attention_backward")
+    for scale in (2.0 ** 127, 2.0 ** -100):
+        assert lib.p3d_attention_backward_workspace_size(attn_desc(p3d, scale=scale)) > 0
