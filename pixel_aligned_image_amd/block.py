@@ -243,6 +243,9 @@ def _rotary(x, positions, freqs, layout, magnitude, gamma, eps):
     pos_stride = positions.stride()
     if axes > 1 and pos_stride[1] != 1:
         raise ValueError("positions must have contiguous rows, got strides %s" % (pos_stride,))
+    if n > 1 and pos_stride[0] >= 1 << 31:   # (ctypes would pass it on modulo 2^32)
+        raise ValueError("positions must have rows less than 2^31 entries apart, got %d"
+                         % pos_stride[0])
     if freqs.dim() != 1:
         raise ValueError("freqs must be [pairs], got %s" % (tuple(freqs.shape),))
     pairs = freqs.shape[0]

@@ -158,3 +158,14 @@ def test_no_tokens_and_repeatable():
         torch.cuda.synchronize()
         got.append((dx, dg))
     assert all(torch.equal(a, b) for g in got[1:] for a, b in zip(got[0], g))
+
+
+def test_positions_further_apart_than_the_descriptor_holds():
+    """pos_stride is an int32: rows 2^32 + 1 entries apart, which would pass
+    as 1, are refused by name."""
+    x = torch.randn(2, 1, 8, device="cuda")
+    far = torch.zeros((1 << 32) + 2, dtype=torch.int32, device="cuda").as_strided(
+        (2, 1), ((1 << 32) + 1, 1))
+    freqs = p3d.p3d_rotary_frequencies(10000.0, 4).cuda()
+    with pytest.raises(ValueError, match="positions"):
+        p3d.p3d_rotary(x, far, freqs, torch.empty_like(x))
