@@ -105,3 +105,24 @@ def test_planted_mistakes_are_outside_the_tolerances():
     _, h = ref.gated_norm(x, [0, 7])
     _, wrong = ref.gated_norm(x, [0, 7], eps=1e-2)
     assert ref.off_by(wrong, h, ref.rounded_once(h, torch.float32)) > 1
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_the_two_forms_of_the_attention_gradients_agree(causal):
+    """block_ref's, and the one of whole heads that the GPU tests of large
+    launches use; a lost key shows in the latter."""
+    import test_gpu_block_regimes as regimes
+    g = torch.Generator().manual_seed(10)
+    q, dout, k, v = rnd(g, 30, 2, 16), rnd(g, 30, 2, 16), rnd(g, 25, 1, 16), rnd(g, 25, 1, 16)
+    want, tol = ref.attention_backward(dout, q, k, v, [0, 30], [0, 25], 0.3, causal)
+    out, lse, reach = ref.attention(q, k, v, [0, 30], [0, 25], 0.3, causal)
+    got = regimes.head_values(q, k[:, 0], v[:, 0], dout, 0.3, causal)
+    for n, w, t in (("out", out, (2.0 ** -7 + 2.0 ** -13) * reach), ("dq", want["dq"], tol["dq"]),
+                    ("dk", want["dk"][:, 0], tol["dk"][:, 0]),
+                    ("dv", want["dv"][:, 0], tol["dv"][:, 0])):
+        assert torch.allclose(got[n][0], w, rtol=1e-12, atol=1e-13), n
+        assert torch.allclose(got[n][1], t, rtol=1e-12, atol=1e-13), n
+    assert torch.allclose(got["lse"][0], lse, rtol=1e-13, atol=0)
+    less = regimes.head_values(q, k[1:, 0], v[1:, 0], dout, 0.3, causal)
+    for n in ("out", "dq"):
+        assert ref.off_by(less[n][0], got[n][0], got[n][1]) > 1, n
