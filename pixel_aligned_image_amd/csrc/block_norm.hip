@@ -267,7 +267,8 @@ __global__ __launch_bounds__(kThreads, VPT* Vec<T>::N <= 24 ? 2 : 1) void gated_
     constexpr int N = Vec<T>::N;
     constexpr int R = kThreads / TPR;        // rows in flight
     __shared__ float red[4];
-    extern __shared__ float cols[];          // [2][dim], then [R][TPR * VPT * N]
+    // [2][dim], read 16 bytes at a time, then [R][TPR * VPT * N]
+    extern __shared__ alignas(16) float cols[];
     float* mul = cols;                       // weight (1 + scale)
     float* lift = cols + a.dim;              // res_scale gate post_weight
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;

@@ -51,3 +51,18 @@ def test_attention_tiles_start_on_whole_rows():
     assert seen >= 10
     text = open(os.path.join(ROOT, "pixel_aligned_image_amd", "csrc", "attn_tile.h")).read()
     assert int(re.search(r"kTileAlign = (\d+);", text).group(1)) == 256
+
+
+def test_shared_arrays_are_aligned_as_they_are_read():
+    """Scalars in LDS that are read or written as 16-byte vectors say so: what
+    lies before them may have any size."""
+    for path in SOURCES:
+        text = open(path).read()
+        for kind, name in re.findall(r"__shared__ ([^;\n]*\b(?:float|float2)) (\w+)\[", text):
+            # the array itself, or a pointer set to a place in it
+            names = [name] + re.findall(r"\bfloat\s*\*\s*(\w+) = %s\b" % name, text)
+            wide = [n for n in names if re.search(
+                r"reinterpret_cast<(?:const )?float4\*>\(&?%s\b|\bfactors<N>\(%s\b" % (n, n),
+                text)]
+            if wide:
+                assert "alignas(16)" in kind, (path, name, wide)
