@@ -268,7 +268,7 @@ __global__ __launch_bounds__(kThreads, VPT* Vec<T>::N <= 24 ? 2 : 1) void gated_
     constexpr int R = kThreads / TPR;        // rows in flight
     __shared__ float red[4];
     // [2][dim], read 16 bytes at a time, then [R][TPR * VPT * N]
-    extern __shared__ alignas(16) float cols[];
+    extern __shared__ __align__(16) float cols[];
     float* mul = cols;                       // weight (1 + scale)
     float* lift = cols + a.dim;              // res_scale gate post_weight
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;

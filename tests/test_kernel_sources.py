@@ -65,4 +65,4 @@ def test_shared_arrays_are_aligned_as_they_are_read():
                 r"reinterpret_cast<(?:const )?float4\*>\(&?%s\b|\bfactors<N>\(%s\b" % (n, n),
                 text)]
             if wide:
-                assert "alignas(16)" in kind, (path, name, wide)
+                assert re.search(r"\balignas\(16\)|__align__\(16\)", kind), (path, name, wide)
