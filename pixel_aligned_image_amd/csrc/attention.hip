@@ -17,11 +17,14 @@
 // joined by combine_kernel. Two cases have kernels of their own: items of few
 // rows (single tokens), and items of few keys (global tokens).
 //
-// Bound by the matrix cores for heads of 128 (12,000 tokens, 12 heads: 0.83-
-// 0.94 ms with the clock that their load leaves, 0.94-1.06 PFLOP/s; causal
-// 12,289 tokens: 0.47 ms, 1.0 PFLOP/s of seen pairs; torch's products of 8192^3
-// reach 1.47 here) and by the vector instructions of the exponentials for heads
-// of 64 (7000 queries, 2 x 1029 keys, 16 heads: 58 us, 0.51 PFLOP/s).
+// Heads of 128 take 0.84 ms for 12,000 tokens of 12 heads (1.06 PFLOP/s) and
+// 0.46 ms for 12,289 causal ones (1.0 PFLOP/s of seen pairs; torch's products of
+// 8192^3 reach 1.47 here). Bound by the products and the vector instructions of
+// the exponentials together: a SIMD's matrix unit is busy 54 % of that time and
+// its vector unit 49 (causal 50 and 46), so its two waves mostly take turns, at
+// the 1.6-1.8 GHz that the load leaves. Heads of 64 (7000 queries, 2 x 1029
+// keys, 16 heads: 47 us and a join of 8, 0.56 PFLOP/s) have half the products
+// per exponential: 25 and 46 %, and a last round that is not full.
 #include <algorithm>
 #include <type_traits>
 

@@ -18,7 +18,7 @@
 // time if every row did), items of a single tile of keys sum D up before dq uses
 // it (1.78 -> 1.0 on three keys), and dk takes the D that the dq kernel sums up
 // (1.42). dk and dv of a key that one or two rows see carry the rounding of
-// those rows' dS and P whole: 1.4 as a mean, up to 1.75 for a key alone.
+// those rows' dS and P whole: 1.4 as a mean, up to 1.64 over 300 drawn cases.
 //
 // Each product's second factor is the softmax tile as the first product left
 // it in registers (attn_tile.h). The scores are computed twice, once per
@@ -29,12 +29,13 @@
 // Where few tiles face a long axis the walked axis is cut into parts whose
 // binary32 sums go to the workspace and are joined by join_kernel.
 //
-// Bound by the matrix cores for heads of 128 (causal, 12,289 tokens, 12 heads
-// on 4: dq 0.67 ms, dkv 0.86 ms, 1.04 and 1.08 PFLOP/s of seen pairs) and by
-// the issue of vector next to matrix instructions for heads of 64 (7000
-// queries, 2 x 1029 keys, 16 heads: dq 78 us, dkv 84 and join 12; a SIMD's
-// vector and matrix units are busy 41 and 25 % of dq's time, 31 and 32 % of
-// dkv's).
+// Causal, 12,289 tokens, 12 heads of 128 on 4: dq 0.68 ms, dkv 0.86 ms, 1.03 and
+// 1.07 PFLOP/s of seen pairs. dq is bound by its matrix and vector instructions
+// together (a SIMD's units are busy 51 and 46 % of the time), dkv by waits of
+// its two waves a SIMD beside them (54 and 30 %). Heads of 64 (7000 queries, 2 x
+// 1029 keys, 16 heads: dq 75 us, dkv 80 and join 12) fill neither unit: 24 and
+// 39 % of dq's time, 33 and 32 % of dkv's. Their waves stand at a wait or a
+// barrier for 36 and 26 % of theirs, and the last round is not full.
 #include <algorithm>
 #include <type_traits>
 
@@ -110,6 +111,8 @@ __device__ __forceinline__ void sums_in_turn() {
     }
 }
 
+// (Heads of 64, three waves a SIMD: three registers are kept in memory outside
+// the loop.)
 template <int HD>
 __global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dq_kernel(BwdArgs f) {
     using T = Tile<HD>;
@@ -192,8 +195,8 @@ __global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dq_kernel(BwdAr
     if (live) {
         lse = a.lse_in[(int64_t)(q0 + (int)token) * a.heads + head];
         const uint4* o = reinterpret_cast<const uint4*>(
-            reinterpret_cast<const uint16_t*>(a.out_in) + (int64_t)(q0 + (int)token) * a.out_stride +
-            head * a.head_dim);
+            reinterpret_cast<const uint16_t*>(a.out_in) +
+            (int64_t)(q0 + (int)token) * a.out_stride + head * a.head_dim);
 #pragma unroll
         for (int k = 0; k < T::kSteps; ++k) {
             const int chunk = 2 * k + h;
@@ -503,9 +506,10 @@ __global__ __launch_bounds__(64 * kWaves, HD <= 64 ? 3 : 2) void dkv_kernel(BwdA
     });
     settle(kf);
 
-    // 32 rows of a tile, from row `sub` on. The issue order is the written one: a matrix instruction, the
-    // reads of the fragments a few matrix instructions on, and in the first
-    // half of the sums the exponentials that the second half needs.
+    // 32 rows of a tile, from row `sub` on. The issue order is the written one:
+    // a matrix instruction, the reads of the fragments a few matrix instructions
+    // on, and in the first half of the sums the exponentials that the second
+    // half needs.
     auto walk = [&](bool masked, int buf, int sub, int row) {
         constexpr int kAhead = 3;
         const uint4* rows = tiles[buf] + sub * T::kChunks;
@@ -683,7 +687,8 @@ hipError_t backward_as(BwdArgs& f, const AttnPlan& p, hipStream_t s) {
                          dim3(64 * kWaves), 0, s>>>(f);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (f.splits > 1) {
-            const Joint dk{f.part, a.scale, a.dk, a.dk_stride}, dv{f.part2, 1.0f, a.dv, a.dv_stride};
+            const Joint dk{f.part, a.scale, a.dk, a.dk_stride};
+            const Joint dv{f.part2, 1.0f, a.dv, a.dv_stride};
             join_kernel<<<dim3((unsigned)((k_rows + 7) / 8), 2), dim3(256), 0, s>>>(
                 dk, dv, f.splits, k_rows, a.kv_heads, a.head_dim, nullptr, nullptr);
             return hipGetLastError();

@@ -8,9 +8,10 @@
 // the read and the last write: the forward call moves 4 planes (x, y in; r, h
 // out), the backward call 6 (x, y, dh, dr in; dx, dy out), and nothing else
 // grows with the rows. Both are bound by memory: 100,000 rows of 1536 bf16
-// take 222 us forward (5.5 TB/s), 200,000 rows 448 us and backward 743 us (5.0
-// TB/s); 4096 rows of 1024 binary32, which stay in the caches, 14 and 24 us
-// with 5 us of sums; 5 rows 5 us, a launch. A row belongs to a group of
+// take 222 us forward (5.5 TB/s), 200,000 rows 448 us and backward 739 us (5.0
+// TB/s; its loop reads two registers back from memory); 4096 rows of 1024
+// binary32 14 and 26 us (22 when the caches hold them) with 5 us of sums; 5 rows
+// 5 us, a launch. A row belongs to a group of
 // 16, 32, 64 or 256 threads, the smallest that holds it in at most VPT
 // 16-byte vectors each, so that its sums stay inside a wave wherever they can
 // (DPP, no LDS) and no lane idles on narrow rows.

@@ -6,9 +6,10 @@
 // +m sin for the second; (C, S) = (1, 0) past the turned part. The gradient is
 // the same with S negated. Both directions read and write every element once
 // and are bound by memory: 100,000 tokens of 24 bf16 heads of 128 take 220 us
-// (5.6 TB/s); 4096 tokens of binary32 heads, which stay in the caches, 14 us,
-// and 27 us backward with the gains' gradient, which is held up by the loads
-// of the few rows that a chunk has (4 us more for its sums).
+// (5.6 TB/s), and backward with the gains' gradient 392 us (4.7 TB/s: its 253
+// registers leave two waves a SIMD to keep loads in flight) and 7 for the sums;
+// 4096 tokens of 32 binary32 heads of 64 17 and 28 us (14 and 26 when the caches
+// hold them) and 4 for the sums, held up by the loads of the few rows of a chunk.
 //
 // A group of P2 lanes (a power of two) holds one head, one 16-byte vector per
 // lane, so its rms sum stays inside a wave. The angles of a token do not
