@@ -67,6 +67,10 @@ KERNEL_SOURCES = {
     "proj_cond_kernel": ["proj_cond.hip", "p3d_internal.h"],
     "sample_kernel": ["sample.hip", "p3d_internal.h", "order.hip"],
     "stats_kernel": ["stats.hip", "p3d_internal.h", "order.hip"],
+    "gated_norm_kernels": ["block_norm.hip", "block_internal.h", "p3d_internal.h"],
+    "rotary_kernels": ["block_rotary.hip", "block_internal.h", "p3d_internal.h"],
+    "attention_kernels": ["attention.hip", "attention_bwd.hip", "attn_tile.h",
+                          "block_internal.h", "p3d_internal.h"],
 }
 
 
