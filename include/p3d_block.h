@@ -254,13 +254,15 @@ p3d_status p3d_attention(const p3d_attn_desc* desc, const void* q, int64_t q_str
  * P and dS are rounded to bf16 as factors of the last three products (dS of
  * queries that see at most 256 keys, and of those that share one of the
  * launch's 128-row tiles with such a query, for dq, as the sum of two bf16
- * numbers).
- * dk, and dq of items of at most 64 keys, take D_i as sum_j P_ij dout_i . v_j,
- * the same number without out's rounding. Rows that nothing reaches get 0, and
- * so does dq of a query that sees one key (its probability is 1). dq, dk and dv
- * are strided like q, k and v, are overwritten and must not overlap another
- * tensor of the call (P3D_ERR_INVALID_ARG where the two have equal strides,
- * one has a single row or both start at one place; not looked for otherwise). */
+ * numbers). dk, and dq of items of at most 64 keys, take D_i as sum_j P_ij
+ * dout_i . v_j, the same number without out's rounding. Rows that nothing
+ * reaches get 0, and so does dq of a query that sees one key (its probability is
+ * 1). Entries that are not finite reach, as in the forward call, every result of
+ * their item that takes them with weight 0.
+ * dq, dk and dv are strided like q, k and v, are overwritten and must not
+ * overlap another tensor of the call (P3D_ERR_INVALID_ARG where the two have
+ * equal strides, one has a single row or both start at one place; not looked for
+ * otherwise). */
 size_t p3d_attention_backward_workspace_size(const p3d_attn_desc* desc);
 p3d_status p3d_attention_backward(const p3d_attn_desc* desc, const void* dout,
                                   int64_t dout_stride, const void* q, int64_t q_stride,
