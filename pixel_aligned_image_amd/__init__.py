@@ -542,3 +542,10 @@ from .block import *                                                  # noqa: E4
 
 block.bind(sys.modules[__name__])
 __all__ += block.__all__
+
+# the model's operators around the block (include/p3d_model.h)
+from . import model                                                   # noqa: E402
+from .model import *                                                  # noqa: E402,F401,F403
+
+model.bind(sys.modules[__name__])
+__all__ += model.__all__

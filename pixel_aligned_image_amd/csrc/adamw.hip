@@ -1,0 +1,437 @@
+// adamw.hip -- p3d_adamw and p3d_grad_norm: the AdamW step over many tensors
+// and the gradient norm it is clipped by.
+//
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   w = w (1 - lr decay) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// One pass over the data: memory bound at 28 bytes an element (binary32
+// weights and states) down to 10 (bf16 weights, 8-bit states). The tensors'
+// table travels in the kernel arguments, kTensors a launch; a workgroup takes
+// one chunk of one tensor, found by a search over the chunks' first numbers,
+// so that a launch over many small tensors fills the chip as a large one does.
+//
+// 8-bit states: a thread holds 8 neighbouring elements and 32 neighbouring
+// threads a block of 256 that shares a scale, so a block's largest state is a
+// maximum over half a wave and the states are read and written once.
+#include <cmath>
+
+#include "model_internal.h"
+
+namespace p3d {
+
+namespace {
+
+constexpr int kThreads = 256, kPer = 8;             // elements of a thread, neighbours
+constexpr int kTensors = 40;                        // of a launch
+constexpr int kRounds = 2;
+constexpr int64_t kChunk = (int64_t)kThreads * kPer * kRounds;
+constexpr int64_t kNormChunk = 4 * kChunk;
+constexpr int64_t kMaxGrid = int64_t(1) << 23;      // (a grid has fewer than 2^32 threads)
+
+struct Entry {
+    void* param;
+    float* master;
+    const void* grad;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    int64_t size;
+    uint32_t first;             // chunk of the launch
+    uint32_t key;               // of the tensor's random bits
+    float keep;                 // 1 - lr decay, or decay where lr is the device's
+};
+
+struct Step {
+    float b1, b2, c1, c2;       // c = 1 - b
+    float rate;                 // lr / (1 - b1^t)
+    float norm;                 // 1 / sqrt(1 - b2^t)
+    float eps;
+    int32_t count;
+    double lr, log_b1, log_b2;  // (log2) where lr or t are the device's
+    int64_t t;
+    const float* grad_scale;
+    const float* device_lr;
+    const int32_t* device_step;
+};
+
+struct Table {
+    Entry e[kTensors];
+};
+
+// The last tensor whose chunks start at or before `chunk` (tensors without
+// elements have no chunks and start where the next one does).
+__device__ __forceinline__ int tensor_of(const Table& t, int count, uint32_t chunk) {
+    int lo = 0, hi = count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.e[mid].first <= chunk) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
+    x ^= x >> 15;
+    x *= 0xB504F335u;
+    x ^= x >> 13;
+    x *= 0xDDB3D743u;
+    return x ^ (x >> 16);
+}
+
+// ------------------------------------------------- vectors of 8 elements ---
+__device__ __forceinline__ void widen8(const Bf16* p, float (&f)[8]) {
+    Vec<Bf16>::widen(*reinterpret_cast<const uint4*>(p), f);
+}
+__device__ __forceinline__ void widen8(const float* p, float (&f)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+__device__ __forceinline__ void narrow8(Bf16* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) = Vec<Bf16>::narrow(f);
+}
+__device__ __forceinline__ void narrow8(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ float widen1(Bf16 v) { return __uint_as_float((uint32_t)v.bits << 16); }
+__device__ __forceinline__ float widen1(float v) { return v; }
+__device__ __forceinline__ Bf16 narrow1(float f, Bf16) {
+    return Bf16{(uint16_t)(pack_bf16x2(f, 0.f) & 0xffffu)};
+}
+__device__ __forceinline__ float narrow1(float f, float) { return f; }
+
+// The `live` (0..8) elements from p on; zeros behind them.
+template <typename T>
+__device__ __forceinline__ void read8(const void* base, int64_t i, int live, float (&f)[8]) {
+    const T* p = reinterpret_cast<const T*>(base) + i;
+    if (live == 8) {
+        widen8(p, f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = e < live ? widen1(p[e]) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void write8(void* base, int64_t i, int live, const float (&f)[8]) {
+    T* p = reinterpret_cast<T*>(base) + i;
+    if (live == 8) {
+        narrow8(p, f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < live) p[e] = narrow1(f[e], T{});
+    }
+}
+
+__device__ __forceinline__ uint2 codes8(const void* base, int64_t i, int live) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(base) + i;
+    if (live == 8) return *reinterpret_cast<const uint2*>(p);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < live) w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void write_codes8(void* base, int64_t i, int live, uint2 c) {
+    uint8_t* p = reinterpret_cast<uint8_t*>(base) + i;
+    if (live == 8) {
+        *reinterpret_cast<uint2*>(p) = c;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < live) p[e] = (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
+}
+
+// e4m3 numbers as floats: the hardware's conversion, two at a time.
+__device__ __forceinline__ void decode8(uint2 c, float by, float (&f)[8]) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 v[4] = {__builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false),
+                        __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true),
+                        __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false),
+                        __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true)};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = v[e >> 1][e & 1] * by;
+}
+
+// The e4m3 number of |q| <= 448 that 16 random bits choose of the two around
+// it. From 2^-6 on a number keeps 3 of binary32's 23 mantissa bits: the random
+// bits go into the upper 16 of the 20 dropped ones (a carry moves on to the
+// next exponent as it should) and the exponent's bias changes by 120 (120 << 3
+// = 960). Below, numbers are multiples of 2^-9.
+__device__ __forceinline__ uint32_t encode(float q, uint32_t bits) {
+    const float a = fminf(fabsf(q), 448.f);
+    const uint32_t normal = ((__float_as_uint(a) + (bits << 4)) >> 20) - 960u;
+    const uint32_t small = (uint32_t)(a * 512.f + (float)bits * 0x1p-16f);
+    return (a < 0x1p-6f ? small : normal) | (__float_as_uint(q) >> 31 << 7);
+}
+
+// Maximum over 32 neighbouring lanes, in each of them.
+__device__ __forceinline__ float half_max(float v) {
+    float a;
+    v = fmaxf(v, dpp<0xB1>(v));
+    v = fmaxf(v, dpp<0x4E>(v));
+    v = fmaxf(v, dpp<0x141>(v));
+    v = fmaxf(v, dpp<0x140>(v));
+    const float b = other_row16(v, a);
+    return fmaxf(a, b);
+}
+
+// A block's scale and what its states are multiplied by. NaN and infinite
+// states leave a scale that is not finite.
+__device__ __forceinline__ void block_scale(float top, float& scale, float& by) {
+    if (top < 0x1p-100f) top = 0.f;
+    scale = top / 448.f;
+    by = top == 0.f ? 0.f : 448.f / top;
+}
+
+template <typename P, typename G, bool Master, int Bits>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(Table table, Step s) {
+    float by = 1.f;
+    if (s.grad_scale) {
+        by = *s.grad_scale;
+        if (!(fabsf(by) < INFINITY)) return;
+    }
+    const int at = tensor_of(table, s.count, blockIdx.x);
+    const Entry& t = table.e[at];
+    float keep = t.keep;
+    if (s.device_lr || s.device_step) {
+        // (1 - b^t with t log2 b: binary64 leaves 1 - 0.999 its 13 digits)
+        const double lr = s.device_lr ? (double)*s.device_lr : s.lr;
+        int64_t n = s.device_step ? (int64_t)*s.device_step : s.t;
+        n = n < 1 ? 1 : n;
+        keep = (float)(1. - lr * (double)t.keep);
+        s.rate = (float)(lr / (1. - exp2((double)n * s.log_b1)));
+        s.norm = (float)(1. / sqrt(1. - exp2((double)n * s.log_b2)));
+    }
+    const int64_t i0 = (int64_t)(blockIdx.x - t.first) * kChunk;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int64_t i = i0 + (int64_t)(r * kThreads + threadIdx.x) * kPer;
+        const int64_t left = t.size - i;
+        const int live = left >= kPer ? kPer : left > 0 ? (int)left : 0;
+        // (in 8 bits a wave stays whole: its lanes exchange the maximum)
+        if (Bits == 32 ? live == 0 : __ballot(live > 0) == 0) continue;
+        float g[8], m[8], v[8], w[8];
+        read8<G>(t.grad, i, live, g);
+        if constexpr (Master) read8<float>(t.master, i, live, w);
+        else read8<P>(t.param, i, live, w);
+        if constexpr (Bits == 32) {
+            read8<float>(t.m, i, live, m);
+            read8<float>(t.v, i, live, v);
+        } else {
+            const uint2 cm = codes8(t.m, i, live), cv = codes8(t.v, i, live);
+            const float sm = live ? t.m_scale[i >> 8] : 0.f, sv = live ? t.v_scale[i >> 8] : 0.f;
+            decode8(cm, sm, m);
+            decode8(cv, sv, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= v[e];
+        }
+        float root[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = g[e] * by;
+            m[e] = s.b1 * m[e] + s.c1 * x;
+            v[e] = s.b2 * v[e] + s.c2 * x * x;
+            root[e] = sqrtf(v[e]);
+            w[e] = w[e] * keep - s.rate * m[e] / (root[e] * s.norm + s.eps);
+        }
+        if constexpr (Master) write8<float>(t.master, i, live, w);
+        write8<P>(t.param, i, live, w);
+        if constexpr (Bits == 32) {
+            write8<float>(t.m, i, live, m);
+            write8<float>(t.v, i, live, v);
+        } else {
+            // a state that is not finite makes its block's scale so: x - x is
+            // 0 or NaN, and fmaxf would lose the NaN
+            float tm = 0.f, tv = 0.f, bad = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                tm = fmaxf(tm, fabsf(m[e]));
+                tv = fmaxf(tv, root[e]);
+                bad += (m[e] - m[e]) + (root[e] - root[e]);
+            }
+            tm = half_max(bad == 0.f ? tm : INFINITY);
+            tv = half_max(bad == 0.f ? tv : INFINITY);
+            float sm, sv, bm, bv;
+            block_scale(tm, sm, bm);
+            block_scale(tv, sv, bv);
+            uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
+            const uint32_t high = (uint32_t)((uint64_t)i >> 32) * 0xDDB3D743u ^ t.key;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t bits = mix(((uint32_t)i + e) * 0x9E3779B1u ^ high);
+                const uint32_t a = encode(m[e] * bm, bits & 0xffffu);
+                uint32_t b = encode(root[e] * bv, bits >> 16);
+                if (b == 0 && root[e] * bv > 0.f) b = 1;
+                cm[e >> 2] |= a << (8 * (e & 3));
+                cv[e >> 2] |= b << (8 * (e & 3));
+            }
+            write_codes8(t.m, i, live, make_uint2(cm[0], cm[1]));
+            write_codes8(t.v, i, live, make_uint2(cv[0], cv[1]));
+            if ((threadIdx.x & 31) == 0 && live) {
+                t.m_scale[i >> 8] = sm;
+                t.v_scale[i >> 8] = sv;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------- norm ---
+
+template <typename G>
+__global__ __launch_bounds__(kThreads) void norm_parts_kernel(Table table, int count,
+                                                              double* __restrict__ parts) {
+    __shared__ double wave[kThreads / 64];
+    const Entry& t = table.e[tensor_of(table, count, blockIdx.x)];
+    const int64_t i0 = (int64_t)(blockIdx.x - t.first) * kNormChunk + threadIdx.x * kPer;
+    double sum = 0.;
+#pragma unroll 4
+    for (int r = 0; r < kNormChunk / (kThreads * kPer); ++r) {
+        const int64_t i = i0 + (int64_t)r * kThreads * kPer, left = t.size - i;
+        if (left <= 0) break;
+        float g[8];
+        read8<G>(t.grad, i, left >= kPer ? kPer : (int)left, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fma((double)g[e], (double)g[e], sum);
+    }
+    for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
+    if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sum = 0.;
+        for (int k = 0; k < kThreads / 64; ++k) sum += wave[k];
+        parts[blockIdx.x] = sum;
+    }
+}
+
+__global__ __launch_bounds__(1024) void norm_join_kernel(const double* __restrict__ parts,
+                                                         int64_t n, float max_norm,
+                                                         float* __restrict__ out) {
+    __shared__ double wave[16];
+    double sum = 0.;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < n; i += 1024) sum += parts[i];
+    for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
+    if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x) return;
+    sum = 0.;
+    for (int k = 0; k < 16; ++k) sum += wave[k];
+    const double norm = sqrt(sum);
+    out[0] = (float)norm;
+    out[1] = !(norm < INFINITY) ? NAN
+             : norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
+}
+
+// ----------------------------------------------------------------- launch ---
+// The tensors in launches of at most kTensors, numbered from `chunk` elements
+// on: `run(table, count, chunks)` for each. A tensor's own chunks fit a grid by
+// its size's limit.
+template <typename Run>
+hipError_t in_launches(const p3d_adamw_desc& d, int64_t chunk, Run run) {
+    Table t;
+    int count = 0;
+    int64_t chunks = 0;
+    const auto flush = [&]() {
+        if (chunks == 0) {
+            count = 0;
+            return hipSuccess;
+        }
+        const hipError_t e = run(t, count, chunks);
+        count = 0;
+        chunks = 0;
+        return e;
+    };
+    const uint32_t key = mix((uint32_t)d.seed) ^ (uint32_t)(d.seed >> 32);
+    for (int32_t j = 0; j < d.count; ++j) {
+        const p3d_adamw_tensor& x = d.tensors[j];
+        if (x.size == 0) continue;
+        const int64_t more = (x.size + chunk - 1) / chunk;
+        if (count == kTensors || chunks + more > kMaxGrid) {
+            const hipError_t e = flush();
+            if (e != hipSuccess) return e;
+        }
+        Entry& to = t.e[count++];
+        to.param = x.param;
+        to.master = x.master;
+        to.grad = x.grad;
+        to.m = x.m;
+        to.v = x.v;
+        to.m_scale = x.m_scale;
+        to.v_scale = x.v_scale;
+        to.size = x.size;
+        to.first = (uint32_t)chunks;
+        to.key = mix((uint32_t)j * 0x9E3779B1u ^ key);
+        to.keep = d.device_lr || d.device_step ? x.weight_decay
+                                               : (float)(1. - d.lr * (double)x.weight_decay);
+        chunks += more;
+    }
+    return flush();
+}
+
+template <typename P, typename G, bool Master>
+hipError_t adamw_bits(const p3d_adamw_desc& d, const Step& step, hipStream_t s) {
+    return in_launches(d, kChunk, [&](const Table& t, int count, int64_t chunks) {
+        Step here = step;
+        here.count = count;
+        if (d.state_bits == 8)
+            adamw_kernel<P, G, Master, 8><<<(unsigned)chunks, kThreads, 0, s>>>(t, here);
+        else
+            adamw_kernel<P, G, Master, 32><<<(unsigned)chunks, kThreads, 0, s>>>(t, here);
+        return hipGetLastError();
+    });
+}
+
+template <typename G>
+hipError_t adamw_grad(const p3d_adamw_desc& d, const Step& step, bool master, hipStream_t s) {
+    if (d.param_dtype == P3D_F32) return adamw_bits<float, G, false>(d, step, s);
+    return master ? adamw_bits<Bf16, G, true>(d, step, s) : adamw_bits<Bf16, G, false>(d, step, s);
+}
+
+}  // namespace
+
+int64_t grad_norm_parts(const p3d_adamw_desc& d) {
+    int64_t n = 0;
+    for (int32_t j = 0; j < d.count; ++j) n += (d.tensors[j].size + kNormChunk - 1) / kNormChunk;
+    return n;
+}
+
+hipError_t launch_grad_norm(const p3d_adamw_desc& d, float max_norm, float* out, double* parts,
+                            hipStream_t s) {
+    int64_t at = 0;
+    const hipError_t e = in_launches(d, kNormChunk, [&](const Table& t, int count, int64_t chunks) {
+        if (d.grad_dtype == P3D_BF16)
+            norm_parts_kernel<Bf16><<<(unsigned)chunks, kThreads, 0, s>>>(t, count, parts + at);
+        else
+            norm_parts_kernel<float><<<(unsigned)chunks, kThreads, 0, s>>>(t, count, parts + at);
+        at += chunks;
+        return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    norm_join_kernel<<<1, 1024, 0, s>>>(parts, at, max_norm, out);
+    return hipGetLastError();
+}
+
+hipError_t launch_adamw(const p3d_adamw_desc& d, hipStream_t s) {
+    bool master = false;
+    for (int32_t j = 0; j < d.count; ++j) master = master || d.tensors[j].master;
+    Step step{};
+    step.b1 = (float)d.beta1;
+    step.b2 = (float)d.beta2;
+    step.c1 = (float)(1. - d.beta1);
+    step.c2 = (float)(1. - d.beta2);
+    step.rate = (float)(d.lr / (1. - std::pow(d.beta1, (double)d.step)));
+    step.norm = (float)(1. / std::sqrt(1. - std::pow(d.beta2, (double)d.step)));
+    step.eps = (float)d.eps;
+    step.lr = d.lr;
+    step.log_b1 = std::log2(d.beta1);
+    step.log_b2 = std::log2(d.beta2);
+    step.t = d.step;
+    step.grad_scale = d.grad_scale;
+    step.device_lr = d.device_lr;
+    step.device_step = d.device_step;
+    return d.grad_dtype == P3D_BF16 ? adamw_grad<Bf16>(d, step, master, s)
+                                    : adamw_grad<float>(d, step, master, s);
+}
+
+}  // namespace p3d

@@ -1,0 +1,631 @@
+// group_norm.hip -- p3d_group_norm and its gradient over channels-last rows.
+//
+//   x^ = (x - mean) rstd,  u = x^ w + b,  out = act(u)
+//   du = dout act'(u),  dbias = sum du,  dweight = sum du x^
+//   dx = rstd (w du - A - x^ B),  A, B = avg(w du), avg(w du x^) of the group
+//
+// Both directions are memory bound: statistics over a whole map stand between
+// the first and the last use of a row, so x (and dout) is read twice, from the
+// caches where it fits. A call is cut into chunks of whole rows; a thread owns
+// 16-byte vectors of channels and walks the chunk's rows, so loads are whole
+// rows and per-channel factors stay in registers. Chunk results go to the
+// workspace and a second kernel joins them in binary64, in a fixed order.
+#include <algorithm>
+
+#include "model_internal.h"
+
+namespace p3d {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// How a workgroup's threads lie over vectors of channels and rows.
+struct Lay {
+    int nv, tx, ty;             // vectors of a row; threads along it, rows at a time
+    __host__ __device__ explicit Lay(int vectors)
+        : nv(vectors), tx(vectors < kThreads ? vectors : kThreads), ty(kThreads / tx) {}
+};
+
+// The last item or chunk range that starts at or before `at`.
+__device__ __forceinline__ int range_of(const ItemTable& t, int batch, int at) {
+    int lo = 0, hi = batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.start[mid] <= at) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// The item and rows of a chunk.
+struct Chunk {
+    int item;
+    int64_t row0;
+    int rows;
+    __device__ __forceinline__ Chunk(const ItemTable& items, const ItemTable& chunk, int batch,
+                                     int64_t each, int at) {
+        item = range_of(chunk, batch, at);
+        row0 = items.start[item] + (int64_t)(at - chunk.start[item]) * each;
+        const int64_t left = items.start[item + 1] - row0;
+        rows = (int)(left < each ? left : each);
+    }
+};
+
+// Rows that thread row `ty` of `step` takes of `rows`.
+__device__ __forceinline__ int rows_of(int rows, int ty, int step) {
+    return ty < rows ? (rows - ty + step - 1) / step : 0;
+}
+
+template <typename T>
+__device__ __forceinline__ const uint4* vectors(const void* base, int64_t row, int64_t stride) {
+    return reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(base) +
+                                          row * stride * (16 / Vec<T>::N));
+}
+
+// One vector of a per-channel parameter, `other` where it is absent.
+template <typename T>
+__device__ __forceinline__ void param(const void* base, int v, float other,
+                                      float (&f)[Vec<T>::N]) {
+    if (base) {
+        Vec<T>::widen(reinterpret_cast<const uint4*>(base)[v], f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < Vec<T>::N; ++e) f[e] = other;
+    }
+}
+
+// ------------------------------------------------------------- statistics ---
+// Count, mean and sum of squared deviations of a set of numbers, and the same
+// of two sets together: no sum of squares is ever taken about another point
+// than the set's own mean, so a mean far from 0 costs no digits.
+template <typename F>
+struct Moments {
+    F n, mean, m2;
+    __device__ __forceinline__ void join(F bn, F bmean, F bm2) {
+        if (bn == F(0)) return;
+        const F all = n + bn, w = bn / all, d = bmean - mean;
+        mean += d * w;
+        m2 += bm2 + d * d * n * w;
+        n = all;
+    }
+};
+
+constexpr int kBatch = 8;       // rows that a thread loads before it uses them
+
+// The chunk's moments of every group. Where a vector's channels are of one
+// group (Whole), a thread keeps one pair for it, else a pair per channel.
+// One batch of 8 rows is centred on its own mean in registers and then joined
+// to the thread's: 4 operations a value in all, below the 13 that a bf16
+// stream at the memory's rate leaves.
+template <typename T, bool Whole>
+__global__ __launch_bounds__(kThreads, 4) void group_stats_kernel(
+    GroupArgs a, ItemTable chunk, int64_t each, float2* __restrict__ partial) {
+    constexpr int N = Vec<T>::N, K = Whole ? 1 : N, PerUnit = Whole ? N : 1;
+    __shared__ float2 unit[(Whole ? 1 : N) * 4096 / N];
+    const Lay lay(a.channels / N);
+    const Chunk c(a.items, chunk, a.batch, each, blockIdx.x);
+    const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
+    const int mine = ty < lay.ty ? rows_of(c.rows, ty, lay.ty) : 0;
+    const int64_t step = a.x_stride * (16 / N) * lay.ty;       // bytes
+    for (int v = tx; v < lay.nv && ty < lay.ty; v += lay.tx) {
+        const char* p = reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v);
+        float mean[K], m2[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) mean[k] = m2[k] = 0.f;
+        int r = 0;
+        for (; r + kBatch <= mine; r += kBatch) {
+            uint4 q[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                q[i] = *reinterpret_cast<const uint4*>(p);
+                p += step;
+            }
+            float s[K], d2[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) s[k] = d2[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                float f[N];
+                Vec<T>::widen(q[i], f);
+#pragma unroll
+                for (int e = 0; e < N; ++e) s[Whole ? 0 : e] += f[e];
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) s[k] *= 1.f / (kBatch * PerUnit);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                float f[N];
+                Vec<T>::widen(q[i], f);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float d = f[e] - s[Whole ? 0 : e];
+                    d2[Whole ? 0 : e] += d * d;
+                }
+            }
+            // rows before, and this batch's share of all
+            const float w = kBatch * __builtin_amdgcn_rcpf((float)(r + kBatch));
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const float d = s[k] - mean[k];
+                mean[k] += d * w;
+                m2[k] += d2[k] + d * d * ((float)r * w * PerUnit);
+            }
+        }
+        for (; r < mine; ++r) {
+            float f[N];
+            Vec<T>::widen(*reinterpret_cast<const uint4*>(p), f);
+            p += step;
+            const float w = __builtin_amdgcn_rcpf((float)(r + 1));
+            float s[K], d2[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) s[k] = d2[k] = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[Whole ? 0 : e] += f[e];
+            if constexpr (Whole) {
+                s[0] *= 1.f / N;
+#pragma unroll
+                for (int e = 0; e < N; ++e) d2[0] += (f[e] - s[0]) * (f[e] - s[0]);
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const float d = s[k] - mean[k];
+                mean[k] += d * w;
+                m2[k] += d2[k] + d * d * ((float)r * w * PerUnit);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) unit[(ty * lay.nv + v) * K + k] = make_float2(mean[k], m2[k]);
+    }
+    __syncthreads();
+    // a group's units, K a vector, of every thread row: by `lanes` lanes
+    const int per = Whole ? a.channels / a.groups / N : a.channels / a.groups;
+    const int width = lay.nv * K;
+    int lanes = 64;
+    while (lanes > 1 && lanes * a.groups > kThreads) lanes >>= 1;
+    const int lane = threadIdx.x & (lanes - 1);
+    for (int g0 = 0; g0 < a.groups; g0 += kThreads / lanes) {
+        const int g = g0 + threadIdx.x / lanes;
+        Moments<float> m{0.f, 0.f, 0.f};
+        if (g < a.groups) {
+            for (int e = lane; e < per * lay.ty; e += lanes) {
+                const int y = e / per;
+                const int n = rows_of(c.rows, y, lay.ty);
+                const float2 u = unit[y * width + g * per + (e - y * per)];
+                m.join((float)(n * PerUnit), u.x, u.y);
+            }
+        }
+        for (int off = 1; off < lanes; off <<= 1) {
+            const float n = __shfl_xor(m.n, off), mean = __shfl_xor(m.mean, off),
+                        m2 = __shfl_xor(m.m2, off);
+            m.join(n, mean, m2);
+        }
+        if (g < a.groups && lane == 0)
+            partial[(int64_t)blockIdx.x * a.groups + g] = make_float2(m.mean, m.m2);
+    }
+}
+
+// One wave joins the chunks of a group of an item. stat: the mean in two
+// binary32 parts (so that subtracting it from x loses nothing) and rstd.
+__global__ __launch_bounds__(kThreads) void group_join_kernel(GroupArgs a, ItemTable chunk,
+                                                              int64_t each,
+                                                              const float2* __restrict__ partial,
+                                                              float4* __restrict__ stat) {
+    const int64_t at = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+    if (at >= (int64_t)a.batch * a.groups) return;
+    const int b = (int)(at / a.groups), g = (int)(at % a.groups), lane = threadIdx.x & 63;
+    const int first = chunk.start[b], last = chunk.start[b + 1];
+    const int64_t rows = a.items.start[b + 1] - a.items.start[b];
+    const int per = a.channels / a.groups;
+    Moments<double> m{0., 0., 0.};
+    for (int c = first + lane; c < last; c += 64) {
+        const float2 u = partial[(int64_t)c * a.groups + g];
+        const int64_t left = rows - (int64_t)(c - first) * each;
+        m.join((double)((left < each ? left : each) * per), u.x, u.y);
+    }
+    for (int off = 1; off < 64; off <<= 1) {
+        const double n = __shfl_xor(m.n, off), mean = __shfl_xor(m.mean, off),
+                     m2 = __shfl_xor(m.m2, off);
+        m.join(n, mean, m2);
+    }
+    if (lane) return;
+    const double var = m.n > 0. ? m.m2 / m.n : 0.;
+    const float rstd = (float)(1. / sqrt(var + (double)a.eps));
+    const float hi = (float)m.mean;
+    stat[at] = make_float4(hi, (float)(m.mean - (double)hi), rstd, 0.f);
+    if (a.mean) a.mean[at] = hi;
+    if (a.rstd) a.rstd[at] = rstd;
+}
+
+// ------------------------------------------------------------------ apply ---
+// out = act((x - hi) k + o) with k = rstd w and o = b - lo k. The chunks run
+// last to first: what the statistics read last is still in the caches.
+template <typename T, int Act, bool Whole>
+__global__ __launch_bounds__(kThreads, 4) void group_apply_kernel(
+    GroupArgs a, ItemTable chunk, int64_t each, const float4* __restrict__ stat) {
+    constexpr int N = Vec<T>::N, K = Whole ? 1 : N, U = 4;
+    const Lay lay(a.channels / N);
+    const Chunk c(a.items, chunk, a.batch, each, gridDim.x - 1 - blockIdx.x);
+    const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
+    if (ty >= lay.ty) return;
+    const int mine = rows_of(c.rows, ty, lay.ty);
+    const int64_t step = a.x_stride * (16 / N) * lay.ty, ostep = a.out_stride * (16 / N) * lay.ty;
+    const int per = a.channels / a.groups;
+    for (int v = tx; v < lay.nv; v += lay.tx) {
+        const char* p = reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v);
+        char* o = const_cast<char*>(
+            reinterpret_cast<const char*>(vectors<T>(a.out, c.row0 + ty, a.out_stride) + v));
+        float hi[K], by[N], off[N];
+        param<T>(a.weight, v, 1.f, by);
+        param<T>(a.bias, v, 0.f, off);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float4 s = stat[(int64_t)c.item * a.groups + (v * N + (Whole ? 0 : e)) / per];
+            hi[Whole ? 0 : e] = s.x;
+            by[e] *= s.z;
+            off[e] -= s.y * by[e];
+        }
+        const auto one = [&](uint4 q) {
+            float f[N];
+            Vec<T>::widen(q, f);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                f[e] = activate<Act>((f[e] - hi[Whole ? 0 : e]) * by[e] + off[e]);
+            return Vec<T>::narrow(f);
+        };
+        int r = 0;
+        for (; r + U <= mine; r += U) {
+            uint4 q[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) q[i] = *reinterpret_cast<const uint4*>(p + i * step);
+#pragma unroll
+            for (int i = 0; i < U; ++i) store_nt16(o + i * ostep, one(q[i]));
+            p += U * step;
+            o += U * ostep;
+        }
+        for (; r < mine; ++r, p += step, o += ostep)
+            store_nt16(o, one(*reinterpret_cast<const uint4*>(p)));
+    }
+}
+
+// --------------------------------------------------------------- gradient ---
+// What the gradient's kernels know of a vector of channels.
+template <typename T, bool Whole>
+struct Channels {
+    static constexpr int N = Vec<T>::N, K = Whole ? 1 : N;
+    float mean[K], rstd[K], w[N], b[N];
+
+    __device__ __forceinline__ void load(const GroupArgs& a, int item, int v) {
+        const int per = a.channels / a.groups;
+        param<T>(a.weight, v, 1.f, w);
+        param<T>(a.bias, v, 0.f, b);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t at = (int64_t)item * a.groups + (v * N + k) / per;
+            mean[k] = a.mean_in[at];
+            rstd[k] = a.rstd_in[at];
+        }
+    }
+    // x^ and du of element e
+    template <int Act>
+    __device__ __forceinline__ void at(int e, float x, float d, float& xn, float& du) const {
+        xn = (x - mean[Whole ? 0 : e]) * rstd[Whole ? 0 : e];
+        du = d * slope<Act>(xn * w[e] + b[e]);
+    }
+};
+
+// Sums of du and of du x^ of every channel over the chunk: [2][channels].
+template <typename T, int Act, bool Whole>
+__global__ __launch_bounds__(kThreads, 4) void group_sums_kernel(GroupArgs a, ItemTable chunk,
+                                                                 int64_t each,
+                                                                 float* __restrict__ partial) {
+    constexpr int N = Vec<T>::N, U = 4;
+    __shared__ float sums[2 * kThreads * N];
+    const Lay lay(a.channels / N);
+    const Chunk c(a.items, chunk, a.batch, each, blockIdx.x);
+    const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
+    const int mine = ty < lay.ty ? rows_of(c.rows, ty, lay.ty) : 0;
+    const int64_t step = a.x_stride * (16 / N) * lay.ty, dstep = a.dout_stride * (16 / N) * lay.ty;
+    float* to = partial + (int64_t)blockIdx.x * 2 * a.channels;
+    for (int v = tx; v < lay.nv && ty < lay.ty; v += lay.tx) {
+        const char* p = reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v);
+        const char* d = reinterpret_cast<const char*>(
+            vectors<T>(a.dout, c.row0 + ty, a.dout_stride) + v);
+        Channels<T, Whole> ch;
+        ch.load(a, c.item, v);
+        float s1[N], s2[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) s1[e] = s2[e] = 0.f;
+        const auto add = [&](uint4 qx, uint4 qd) {
+            float fx[N], fd[N];
+            Vec<T>::widen(qx, fx);
+            Vec<T>::widen(qd, fd);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                float xn, du;
+                ch.template at<Act>(e, fx[e], fd[e], xn, du);
+                s1[e] += du;
+                s2[e] += du * xn;
+            }
+        };
+        int r = 0;
+        for (; r + U <= mine; r += U) {
+            uint4 qx[U], qd[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                qx[i] = *reinterpret_cast<const uint4*>(p + i * step);
+                qd[i] = *reinterpret_cast<const uint4*>(d + i * dstep);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) add(qx[i], qd[i]);
+            p += U * step;
+            d += U * dstep;
+        }
+        for (; r < mine; ++r, p += step, d += dstep)
+            add(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(d));
+        if (lay.ty == 1) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                to[v * N + e] = s1[e];
+                to[a.channels + v * N + e] = s2[e];
+            }
+        } else {
+            // (then tx covers the row: one vector a thread)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                sums[ty * a.channels + v * N + e] = s1[e];
+                sums[kThreads * N + ty * a.channels + v * N + e] = s2[e];
+            }
+        }
+    }
+    if (lay.ty == 1) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.channels; i += kThreads) {
+        const int half = i >= a.channels, col = i - half * a.channels;
+        const float* from = sums + half * kThreads * N + col;
+        float s = 0.f;
+        for (int y = 0; y < lay.ty; ++y) s += from[y * a.channels];
+        to[i] = s;
+    }
+}
+
+// The items' sums [batch][2][channels] of the chunks': 32 columns and 32 lanes
+// over the chunks.
+constexpr int kTotalCols = 32, kTotalLanes = 32;
+
+__global__ __launch_bounds__(kTotalCols * kTotalLanes) void group_totals_kernel(
+    int columns, ItemTable chunk, const float* __restrict__ partial, float* __restrict__ total) {
+    __shared__ double part[kTotalLanes][kTotalCols + 1];
+    const int x = threadIdx.x % kTotalCols, y = threadIdx.x / kTotalCols;
+    const int col = blockIdx.x * kTotalCols + x, b = blockIdx.y;
+    double s = 0.;
+    if (col < columns) {
+        const float* p = partial + col;
+#pragma unroll 8
+        for (int c = chunk.start[b] + y; c < chunk.start[b + 1]; c += kTotalLanes)
+            s += p[(int64_t)c * columns];
+    }
+    part[y][x] = s;
+    __syncthreads();
+    if (y == 0 && col < columns) {
+        for (int i = 1; i < kTotalLanes; ++i) s += part[i][x];
+        total[(int64_t)b * columns + col] = (float)s;
+    }
+}
+
+// dx; and, by the workgroups behind the chunks', dweight and dbias from the
+// items' sums.
+template <typename T, int Act, bool Whole>
+__global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, ItemTable chunk,
+                                                               int64_t each, int chunks,
+                                                               const float* __restrict__ total) {
+    constexpr int N = Vec<T>::N, U = 4;
+    extern __shared__ float2 avg[];         // [groups]: A and B of the item, with -1 / count
+    if ((int)blockIdx.x >= chunks) {
+        const int col = ((int)blockIdx.x - chunks) * kThreads + threadIdx.x;
+        if (col >= a.channels) return;
+        double s1 = 0., s2 = 0.;
+        for (int b = 0; b < a.batch; ++b) {
+            const float* t = total + (int64_t)b * 2 * a.channels + col;
+            s1 += t[0];
+            s2 += t[a.channels];
+        }
+        if (a.dbias) a.dbias[col] = (float)s1;
+        if (a.dweight) a.dweight[col] = (float)s2;
+        return;
+    }
+    const Lay lay(a.channels / N);
+    const Chunk c(a.items, chunk, a.batch, each, chunks - 1 - (int)blockIdx.x);
+    const int per = a.channels / a.groups;
+    {
+        const float* t = total + (int64_t)c.item * 2 * a.channels;
+        const int64_t count = (int64_t)(a.items.start[c.item + 1] - a.items.start[c.item]) * per;
+        const float by = (float)(-1. / (double)count);
+        int lanes = 64;
+        while (lanes > 1 && lanes * a.groups > kThreads) lanes >>= 1;
+        const int lane = threadIdx.x & (lanes - 1);
+        for (int g0 = 0; g0 < a.groups; g0 += kThreads / lanes) {
+            const int g = g0 + threadIdx.x / lanes;
+            float s1 = 0.f, s2 = 0.f;
+            if (g < a.groups) {
+                for (int e = lane; e < per; e += lanes) {
+                    const int col = g * per + e;
+                    float w = 1.f;
+                    if (a.weight) {
+                        if constexpr (N == 4) w = reinterpret_cast<const float*>(a.weight)[col];
+                        else w = __uint_as_float(
+                                 (uint32_t)reinterpret_cast<const uint16_t*>(a.weight)[col] << 16);
+                    }
+                    s1 += w * t[col];
+                    s2 += w * t[a.channels + col];
+                }
+            }
+            for (int off = 1; off < lanes; off <<= 1) {
+                s1 += __shfl_xor(s1, off);
+                s2 += __shfl_xor(s2, off);
+            }
+            if (g < a.groups && lane == 0) avg[g] = make_float2(s1 * by, s2 * by);
+        }
+    }
+    __syncthreads();
+    const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
+    if (ty >= lay.ty) return;
+    const int mine = rows_of(c.rows, ty, lay.ty);
+    const int64_t step = a.x_stride * (16 / N) * lay.ty, dstep = a.dout_stride * (16 / N) * lay.ty,
+                  ostep = a.out_stride * (16 / N) * lay.ty;
+    for (int v = tx; v < lay.nv; v += lay.tx) {
+        const char* p = reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v);
+        const char* d = reinterpret_cast<const char*>(
+            vectors<T>(a.dout, c.row0 + ty, a.dout_stride) + v);
+        char* o = const_cast<char*>(
+            reinterpret_cast<const char*>(vectors<T>(a.dx, c.row0 + ty, a.out_stride) + v));
+        Channels<T, Whole> ch;
+        ch.load(a, c.item, v);
+        constexpr int K = Channels<T, Whole>::K;
+        float2 m[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) m[k] = avg[(v * N + k) / per];
+        const auto one = [&](uint4 qx, uint4 qd) {
+            float fx[N], fd[N];
+            Vec<T>::widen(qx, fx);
+            Vec<T>::widen(qd, fd);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                float xn, du;
+                ch.template at<Act>(e, fx[e], fd[e], xn, du);
+                const int k = Whole ? 0 : e;
+                fx[e] = ch.rstd[k] * (du * ch.w[e] + (m[k].x + xn * m[k].y));
+            }
+            return Vec<T>::narrow(fx);
+        };
+        int r = 0;
+        for (; r + U <= mine; r += U) {
+            uint4 qx[U], qd[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                qx[i] = *reinterpret_cast<const uint4*>(p + i * step);
+                qd[i] = *reinterpret_cast<const uint4*>(d + i * dstep);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) store_nt16(o + i * ostep, one(qx[i], qd[i]));
+            p += U * step;
+            d += U * dstep;
+            o += U * ostep;
+        }
+        for (; r < mine; ++r, p += step, d += dstep, o += ostep)
+            store_nt16(o, one(*reinterpret_cast<const uint4*>(p),
+                              *reinterpret_cast<const uint4*>(d)));
+    }
+}
+
+// ----------------------------------------------------------------- launch ---
+template <typename T, bool Whole>
+hipError_t forward_of(const GroupArgs& a, const GroupPlan& p, float2* partial, float4* stat,
+                      hipStream_t s) {
+    const int chunks = p.chunk.start[a.batch];
+    if (chunks) {
+        group_stats_kernel<T, Whole><<<chunks, kThreads, 0, s>>>(a, p.chunk, p.rows, partial);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const int64_t waves = (int64_t)a.batch * a.groups;
+    group_join_kernel<<<(unsigned)((waves + 3) / 4), kThreads, 0, s>>>(a, p.chunk, p.rows, partial,
+                                                                       stat);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !chunks) return e;
+    const auto apply = [&](auto act) {
+        group_apply_kernel<T, decltype(act)::value, Whole>
+            <<<chunks, kThreads, 0, s>>>(a, p.chunk, p.rows, stat);
+    };
+    if (a.act == P3D_ACT_SILU) apply(std::integral_constant<int, P3D_ACT_SILU>());
+    else if (a.act == P3D_ACT_GELU) apply(std::integral_constant<int, P3D_ACT_GELU>());
+    else apply(std::integral_constant<int, P3D_ACT_NONE>());
+    return hipGetLastError();
+}
+
+template <typename T, int Act, bool Whole>
+hipError_t backward_act(const GroupArgs& a, const GroupPlan& p, float* partial, float* total,
+                        hipStream_t s) {
+    const int chunks = p.chunk.start[a.batch];
+    if (chunks) {
+        group_sums_kernel<T, Act, Whole><<<chunks, kThreads, 0, s>>>(a, p.chunk, p.rows, partial);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const dim3 grid((unsigned)((2 * a.channels + kTotalCols - 1) / kTotalCols), (unsigned)a.batch);
+    group_totals_kernel<<<grid, kTotalCols * kTotalLanes, 0, s>>>(2 * a.channels, p.chunk, partial,
+                                                                  total);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int more = a.dweight || a.dbias ? (a.channels + kThreads - 1) / kThreads : 0;
+    if (chunks + more == 0) return hipSuccess;
+    group_dx_kernel<T, Act, Whole><<<chunks + more, kThreads, a.groups * sizeof(float2), s>>>(
+        a, p.chunk, p.rows, chunks, total);
+    return hipGetLastError();
+}
+
+template <typename T, bool Whole>
+hipError_t backward_of(const GroupArgs& a, const GroupPlan& p, float* partial, float* total,
+                       hipStream_t s) {
+    if (a.act == P3D_ACT_SILU)
+        return backward_act<T, P3D_ACT_SILU, Whole>(a, p, partial, total, s);
+    if (a.act == P3D_ACT_GELU)
+        return backward_act<T, P3D_ACT_GELU, Whole>(a, p, partial, total, s);
+    return backward_act<T, P3D_ACT_NONE, Whole>(a, p, partial, total, s);
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+// Chunks for at most 4 workgroups a CU, all of them running at once, of at
+// least 4 rows a thread.
+GroupPlan group_norm_plan(const GroupArgs& a, p3d_dtype dt) {
+    GroupPlan p;
+    const Lay lay(a.channels / (dt == P3D_BF16 ? 8 : 4));
+    const int64_t n = a.items.start[a.batch], most = 4 * kComputeUnits;
+    p.rows = std::max<int64_t>((n + most - 1) / most, 4 * lay.ty);
+    p.rows = (p.rows + lay.ty - 1) / lay.ty * lay.ty;
+    int32_t at = 0;
+    for (int b = 0; b < a.batch; ++b) {
+        p.chunk.start[b] = at;
+        at += (int32_t)((a.items.start[b + 1] - a.items.start[b] + p.rows - 1) / p.rows);
+    }
+    for (int b = a.batch; b <= P3D_MAX_BATCH; ++b) p.chunk.start[b] = at;
+    const size_t chunks = at, batch = a.batch;
+    const size_t forward = round256(chunks * a.groups * sizeof(float2)) +
+                           batch * a.groups * sizeof(float4);
+    const size_t backward = round256(chunks * 2 * a.channels * sizeof(float)) +
+                            batch * 2 * a.channels * sizeof(float);
+    p.bytes = round256(std::max(forward, backward));
+    return p;
+}
+
+hipError_t launch_group_norm(const GroupArgs& a, const GroupPlan& p, p3d_dtype dt, void* ws,
+                             hipStream_t s) {
+    float2* partial = static_cast<float2*>(ws);
+    float4* stat = reinterpret_cast<float4*>(
+        static_cast<char*>(ws) +
+        round256((size_t)p.chunk.start[a.batch] * a.groups * sizeof(float2)));
+    const int per = a.channels / a.groups;
+    if (dt == P3D_BF16)
+        return per % 8 ? forward_of<Bf16, false>(a, p, partial, stat, s)
+                       : forward_of<Bf16, true>(a, p, partial, stat, s);
+    return per % 4 ? forward_of<float, false>(a, p, partial, stat, s)
+                   : forward_of<float, true>(a, p, partial, stat, s);
+}
+
+hipError_t launch_group_norm_backward(const GroupArgs& a, const GroupPlan& p, p3d_dtype dt,
+                                      void* ws, hipStream_t s) {
+    float* partial = static_cast<float*>(ws);
+    float* total = reinterpret_cast<float*>(
+        static_cast<char*>(ws) +
+        round256((size_t)p.chunk.start[a.batch] * 2 * a.channels * sizeof(float)));
+    const int per = a.channels / a.groups;
+    if (dt == P3D_BF16)
+        return per % 8 ? backward_of<Bf16, false>(a, p, partial, total, s)
+                       : backward_of<Bf16, true>(a, p, partial, total, s);
+    return per % 4 ? backward_of<float, false>(a, p, partial, total, s)
+                   : backward_of<float, true>(a, p, partial, total, s);
+}
+
+}  // namespace p3d

@@ -1,0 +1,331 @@
+"""Binding of include/p3d_model.h: the model's operators around the block.
+
+Same rules as block.py: every function has the name of its C entry point,
+checks its tensors and passes device pointers and torch's current HIP stream;
+results go into tensors the caller gives. Channels-last maps are passed as
+rows: a [B, H, W, C] map's ``.view(-1, C)`` with the items' row numbers.
+Tensors are on torch's current device.
+"""
+import ctypes
+
+import torch
+
+from . import block
+from ._streams import lends as _lends
+
+__all__ = ["p3d_group_norm", "p3d_group_norm_backward", "p3d_group_norm_workspace_size",
+           "p3d_quantize_rows", "p3d_linear_i8", "p3d_adamw", "p3d_grad_norm",
+           "p3d_grad_norm_workspace_size", "make_adamw_tensors", "ACT"]
+
+ACT = {"none": 0, "silu": 1, "gelu": 2}                                 # p3d_act
+
+_vp, _i32, _i64, _f32, _f64 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
+                               ctypes.c_double)
+_size = ctypes.c_size_t
+
+
+class p3d_group_desc(ctypes.Structure):
+    _fields_ = [("n", _i64), ("offsets", _vp), ("batch", _i32), ("channels", _i32),
+                ("groups", _i32), ("dtype", ctypes.c_int), ("act", ctypes.c_int), ("eps", _f32),
+                ("weight", _vp), ("bias", _vp)]
+
+
+class p3d_linear_i8_desc(ctypes.Structure):
+    _fields_ = [("n", _i64), ("in_dim", _i32), ("out_dim", _i32), ("dtype", ctypes.c_int),
+                ("act", ctypes.c_int), ("weight", _vp), ("weight_scale", _vp), ("bias", _vp)]
+
+
+class p3d_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", _vp), ("master", _vp), ("grad", _vp), ("m", _vp), ("v", _vp),
+                ("m_scale", _vp), ("v_scale", _vp), ("size", _i64), ("weight_decay", _f32)]
+
+
+class p3d_adamw_desc(ctypes.Structure):
+    _fields_ = [("count", _i32), ("tensors", _vp), ("param_dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("state_bits", _i32), ("lr", _f64), ("beta1", _f64),
+                ("beta2", _f64), ("eps", _f64), ("step", _i64), ("seed", ctypes.c_uint64),
+                ("grad_scale", _vp), ("device_lr", _vp), ("device_step", _vp)]
+
+
+lib = None          # set by bind()
+_core = None
+
+
+def bind(core):
+    """Declare the entry points on the loaded library (called on import)."""
+    global lib, _core
+    _core, lib = core, core.lib
+    group, linear, adamw = (ctypes.POINTER(t) for t in (p3d_group_desc, p3d_linear_i8_desc,
+                                                        p3d_adamw_desc))
+    for name, res, args in [
+            ("p3d_group_norm_workspace_size", _size, [group]),
+            ("p3d_group_norm", ctypes.c_int,
+             [group, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _size, _vp]),
+            ("p3d_group_norm_backward", ctypes.c_int,
+             [group] + [_vp, _i64] * 2 + [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _size, _vp]),
+            ("p3d_quantize_rows", ctypes.c_int,
+             [_vp, ctypes.c_int, _i64, _i32, _i64, _vp, _i64, _vp, _vp]),
+            ("p3d_linear_i8", ctypes.c_int,
+             [linear, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp]),
+            ("p3d_adamw", ctypes.c_int, [adamw, _vp]),
+            ("p3d_grad_norm_workspace_size", _size, [adamw]),
+            ("p3d_grad_norm", ctypes.c_int, [adamw, _f32, _vp, _vp, _size, _vp])]:
+        f = getattr(lib, name)
+        f.restype, f.argtypes = res, args
+
+
+# ----------------------------------------------------------------- helpers ---
+def _here(t, name):
+    """Refuses a tensor of another device than the one the call runs on."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s must be on torch's current device (%d), got %s"
+                         % (name, torch.cuda.current_device(), t.device))
+
+
+def _rows(t, name, dtype, shape=None):
+    """(pointer, row stride) of a [n, width] device tensor whose rows may be
+    strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be on the GPU, got %s" % (name, t.device))
+    _here(t, name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError("%s must be %s, got %s" % (
+            name, "[n, width]" if shape is None else list(shape), tuple(t.shape)))
+    n, width = t.shape
+    s = t.stride()
+    if width > 1 and s[1] != 1:
+        raise ValueError("%s must have contiguous rows, got strides %s" % (name, s))
+    return t.data_ptr(), (s[0] if n > 1 else width)
+
+
+def _ptr(t, name, dtype, shape):
+    p = block._ptr(t, name, dtype, shape)
+    if t is not None:
+        _here(t, name)
+    return p
+
+
+def _choice(table, name, value):
+    if value not in table:
+        raise ValueError("%s must be one of %s, got %r" % (name, ", ".join(table), value))
+    return table[value]
+
+
+# -------------------------------------------------------------- group norm ---
+def _group(x, groups, offsets, weight, bias, act, eps):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be [n, channels], got %s" % (tuple(getattr(x, "shape", ())),))
+    n, c = x.shape
+    off = block.make_offsets((0, n) if offsets is None else offsets)
+    d = p3d_group_desc(n, ctypes.addressof(off), len(off) - 1, c, int(groups),
+                       block._dtype(x, "x"), _choice(ACT, "act", act), eps,
+                       _ptr(weight, "weight", x.dtype, (c,)), _ptr(bias, "bias", x.dtype, (c,)))
+    return d, off
+
+
+def p3d_group_norm_workspace_size(x, groups, offsets=None):
+    """Bytes of device workspace p3d_group_norm and p3d_group_norm_backward
+    need for rows like x's."""
+    d, off = _group(x, groups, offsets, None, None, "none", 1e-5)
+    return block._sized(lib.p3d_group_norm_workspace_size(d))
+
+
+@_lends
+def p3d_group_norm(x, out, groups, offsets=None, weight=None, bias=None, act="none", eps=1e-5,
+                   mean=None, rstd=None, workspace=None, stream=None):
+    """Enqueue p3d_group_norm: out = act((x - mean) rstd weight + bias) with an
+    item's mean and rstd over its rows and each of `groups` ranges of channels.
+    x, out: [n, channels] float32 or bfloat16 (rows may be strided; out may be
+    x); weight, bias: [channels]; act: "none", "silu" or "gelu"; mean, rstd:
+    float32 [batch, groups], written unless None (the gradient needs them);
+    offsets: the items' rows (None: one item)."""
+    d, off = _group(x, groups, offsets, weight, bias, act, eps)
+    xp, xs = _rows(x, "x", x.dtype)
+    op, os = _rows(out, "out", x.dtype, x.shape)
+    stats = (d.batch, d.groups)
+    keep, ws, nbytes = block._work(workspace, lambda: lib.p3d_group_norm_workspace_size(d),
+                                   x.device, stream)
+    _core._check(lib.p3d_group_norm(d, xp, xs, op, os, _ptr(mean, "mean", torch.float32, stats),
+                                    _ptr(rstd, "rstd", torch.float32, stats), ws, nbytes,
+                                    block._stream(stream)))
+
+
+@_lends
+def p3d_group_norm_backward(dout, x, mean, rstd, dx, groups, offsets=None, weight=None, bias=None,
+                            act="none", dweight=None, dbias=None, workspace=None, stream=None):
+    """Enqueue p3d_group_norm_backward: dx (which may be dout or x) from dout,
+    the forward call's x and the mean and rstd it wrote; float32 dweight and
+    dbias [channels], each None where it is not wanted."""
+    d, off = _group(x, groups, offsets, weight, bias, act, 1e-5)
+    xp, xs = _rows(x, "x", x.dtype)
+    dp, ds = _rows(dout, "dout", x.dtype, x.shape)
+    op, os = _rows(dx, "dx", x.dtype, x.shape)
+    f, stats, cols = torch.float32, (d.batch, d.groups), (d.channels,)
+    keep, ws, nbytes = block._work(workspace, lambda: lib.p3d_group_norm_workspace_size(d),
+                                   x.device, stream)
+    _core._check(lib.p3d_group_norm_backward(
+        d, dp, ds, xp, xs, _ptr(mean, "mean", f, stats), _ptr(rstd, "rstd", f, stats), op, os,
+        _ptr(dweight, "dweight", f, cols), _ptr(dbias, "dbias", f, cols), ws, nbytes,
+        block._stream(stream)))
+
+
+# ------------------------------------------------------------------ linear ---
+@_lends
+def p3d_quantize_rows(x, q, scale, stream=None):
+    """Enqueue p3d_quantize_rows: q (int8, like x) and scale (float32 [n]) of
+    the rows of x [n, width], float32 or bfloat16 (rows may be strided):
+    tokens, or a weight [out, in]."""
+    xp, xs = _rows(x, "x", x.dtype)
+    qp, qs = _rows(q, "q", torch.int8, x.shape)
+    n, width = x.shape
+    _core._check(lib.p3d_quantize_rows(xp, block._dtype(x, "x"), n, width, xs, qp, qs,
+                                       _ptr(scale, "scale", torch.float32, (n,)),
+                                       block._stream(stream)))
+
+
+@_lends
+def p3d_linear_i8(q, scale, weight, weight_scale, out, bias=None, act="none", residual=None,
+                  stream=None):
+    """Enqueue p3d_linear_i8: out = act(q weight^T scale weight_scale + bias) +
+    residual. q: int8 [n, in] (rows may be strided) and scale: float32 [n] of
+    p3d_quantize_rows; weight: int8 [out, in]; weight_scale: float32 [out];
+    out, residual: [n, out] and bias: [out], float32 or bfloat16 (residual may
+    be out)."""
+    qp, qs = _rows(q, "q", torch.int8)
+    n, k = q.shape
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [out, in], got %s"
+                         % (tuple(getattr(weight, "shape", ())),))
+    m = weight.shape[0]
+    op, os = _rows(out, "out", out.dtype, (n, m))
+    rp, rs = (None, 0) if residual is None else _rows(residual, "residual", out.dtype, (n, m))
+    d = p3d_linear_i8_desc(n, k, m, block._dtype(out, "out"), _choice(ACT, "act", act),
+                           _ptr(weight, "weight", torch.int8, (m, k)),
+                           _ptr(weight_scale, "weight_scale", torch.float32, (m,)),
+                           _ptr(bias, "bias", out.dtype, (m,)))
+    _core._check(lib.p3d_linear_i8(d, qp, qs, _ptr(scale, "scale", torch.float32, (n,)), rp, rs,
+                                   op, os, block._stream(stream)))
+
+
+# ------------------------------------------------------------------- adamw ---
+class AdamWTensors(tuple):
+    """The tensors of p3d_adamw and their table (make_adamw_tensors)."""
+
+
+def _flat(t, name, dtype, size):
+    """Pointer of a contiguous device tensor of `size` elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be on the GPU, got %s" % (name, t.device))
+    _here(t, name)
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.numel() != size or not t.is_contiguous():
+        raise ValueError("%s must have %d contiguous elements, got %s, strides %s"
+                         % (name, size, tuple(t.shape), t.stride()))
+    return t.data_ptr() if size else None
+
+
+def make_adamw_tensors(params, grads, m, v, masters=None, m_scales=None, v_scales=None,
+                       weight_decay=0.0):
+    """The table of p3d_adamw and p3d_grad_norm, for callers to keep over the
+    steps: lists of contiguous tensors, one entry a parameter (of any shape).
+    params: float32 or bfloat16; grads: likewise; m, v: float32, or 8-bit
+    (torch.float8_e4m3fn or uint8) with float32 m_scales and v_scales of
+    (size + 255) // 256; masters: float32 copies of bfloat16 params, or None;
+    weight_decay: a number or one for each. The table keeps the tensors: a
+    gradient in another tensor needs another table."""
+    params, grads, m, v = list(params), list(grads), list(m), list(v)
+    n = len(params)
+    lists = [("grads", grads), ("m", m), ("v", v)]
+    masters, m_scales, v_scales = (None if x is None else list(x)
+                                   for x in (masters, m_scales, v_scales))
+    lists += [(k, x) for k, x in (("masters", masters), ("m_scales", m_scales),
+                                  ("v_scales", v_scales)) if x is not None]
+    decay = ([float(w) for w in weight_decay] if hasattr(weight_decay, "__len__")
+             else [float(weight_decay)] * n)
+    for name, x in lists + [("weight_decay", decay)]:
+        if len(x) != n:
+            raise ValueError("%s must have one entry for each of %d params, got %d"
+                             % (name, n, len(x)))
+    if (m_scales is None) != (v_scales is None):
+        raise ValueError("m_scales and v_scales go together")
+    pt, gt = (x[0].dtype if n else torch.float32 for x in (params, grads))
+    for x, name in ((pt, "params"), (gt, "grads")):
+        if x not in _core._DT:
+            raise TypeError("%s must be float32 or bfloat16, got %s" % (name, x))
+    bits = 32 if m_scales is None else 8
+    st = torch.float32 if bits == 32 else (torch.float8_e4m3fn, torch.uint8)
+    f = torch.float32
+    rows = (p3d_adamw_tensor * max(1, n))()
+    for j in range(n):
+        size, to = params[j].numel(), rows[j]
+        blocks = (size + 255) // 256
+        to.param = _flat(params[j], "params[%d]" % j, pt, size)
+        to.grad = _flat(grads[j], "grads[%d]" % j, gt, size)
+        to.m = _flat(m[j], "m[%d]" % j, st, size)
+        to.v = _flat(v[j], "v[%d]" % j, st, size)
+        if masters is not None:
+            to.master = _flat(masters[j], "masters[%d]" % j, f, size)
+        if bits == 8:
+            to.m_scale = _flat(m_scales[j], "m_scales[%d]" % j, f, blocks)
+            to.v_scale = _flat(v_scales[j], "v_scales[%d]" % j, f, blocks)
+        to.size, to.weight_decay = size, decay[j]
+    table = AdamWTensors(params + grads + m + v + (masters or []) + (m_scales or [])
+                         + (v_scales or []))
+    table.rows, table.count, table.bits = rows, n, bits
+    table.param_dtype, table.grad_dtype = _core._DT[pt], _core._DT[gt]
+    table.device = params[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    return table
+
+
+def _adamw(tensors):
+    if not isinstance(tensors, AdamWTensors):
+        raise TypeError("tensors must be a table of make_adamw_tensors")
+    if tensors.device.index != torch.cuda.current_device():
+        raise ValueError("tensors must be on torch's current device (%d), got %s"
+                         % (torch.cuda.current_device(), tensors.device))
+    return p3d_adamw_desc(tensors.count, ctypes.addressof(tensors.rows), tensors.param_dtype,
+                          tensors.grad_dtype, tensors.bits)
+
+
+@_lends
+def p3d_adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0, grad_scale=None,
+              device_lr=None, device_step=None, stream=None):
+    """Enqueue p3d_adamw: step `step` (from 1 on) on a table of
+    make_adamw_tensors. grad_scale: float32 device tensor of one element (the
+    second of p3d_grad_norm's result) or None; seed: of the random bits that
+    8-bit states are rounded by, another for every step; device_lr, device_step:
+    float32 / int32 device tensors of one element that are read instead of lr
+    and step when the work runs, or None."""
+    d = _adamw(tensors)
+    d.lr, d.beta1, d.beta2, d.eps, d.step = lr, beta1, beta2, eps, step
+    d.seed = seed & 0xffffffffffffffff
+    f = torch.float32
+    for name, t, dt in (("grad_scale", grad_scale, f), ("device_lr", device_lr, f),
+                        ("device_step", device_step, torch.int32)):
+        if t is not None:
+            setattr(d, name, _flat(t, name, dt, 1))
+    _core._check(lib.p3d_adamw(d, block._stream(stream)))
+
+
+def p3d_grad_norm_workspace_size(tensors):
+    """Bytes of device workspace p3d_grad_norm needs."""
+    return block._sized(lib.p3d_grad_norm_workspace_size(_adamw(tensors)))
+
+
+@_lends
+def p3d_grad_norm(tensors, out, max_norm=float("inf"), workspace=None, stream=None):
+    """Enqueue p3d_grad_norm: out (float32 [2]) = the norm over the table's
+    gradients, and the factor that brings it to max_norm where it is above (NaN
+    where it is not finite)."""
+    d = _adamw(tensors)
+    keep, ws, nbytes = block._work(workspace, lambda: lib.p3d_grad_norm_workspace_size(d),
+                                   tensors.device, stream)
+    _core._check(lib.p3d_grad_norm(d, max_norm, _ptr(out, "out", torch.float32, (2,)), ws, nbytes,
+                                   block._stream(stream)))
