@@ -1,0 +1,244 @@
+"""p3d_group_norm and its gradient on the GPU against 64 bits."""
+import pytest
+import torch
+
+import model_ref as ref
+import pixel_aligned_image_amd as p3d
+from block_ref import uneven
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def made(n, c, dtype, seed, mean=0.5, by=1.5):
+    g = torch.Generator().manual_seed(seed)
+
+    def randn(*shape, scale=1.0, base=0.0):
+        return (torch.randn(*shape, generator=g) * scale + base).to(dtype).cuda()
+
+    x = randn(n, c, scale=by) + randn(c, scale=mean)
+    return dict(x=x, w=randn(c, scale=0.3, base=1.0), b=randn(c, scale=0.5), dout=randn(n, c))
+
+
+def strided(t, more):
+    """The same rows in a wider buffer of NaN."""
+    wide = torch.full((t.shape[0], t.shape[1] + more), float("nan"), dtype=t.dtype, device="cuda")
+    wide[:, more // 2:more // 2 + t.shape[1]] = t
+    return wide[:, more // 2:more // 2 + t.shape[1]], wide
+
+
+def near(got, want, dtype, slack, what):
+    """Within half a step of the type of the value, and `slack` of binary32's
+    roundings before that (which the last rounding may carry over a step)."""
+    got, want = got.double().cpu(), want
+    assert got.shape == want.shape
+    if got.numel() == 0:
+        return
+    bound = ref.HALF[dtype] * want.abs() + slack * (1 + 2 * ref.HALF[dtype]) + 1e-37
+    off = (got - want).abs()
+    assert bool((off <= bound).all()), (what, float((off / bound).max()),
+                                        int((off / bound).argmax()))
+
+
+def check(n, c, groups, dtype, kind, off=None, s=None, seed=0, affine=True, eps=1e-5, stride=0,
+          in_place=False):
+    off = [0, n] if off is None else off
+    s = made(n, c, dtype, seed) if s is None else s
+    w, b = (s["w"], s["b"]) if affine else (None, None)
+    x64, w64, b64 = ref.f64(s["x"]), ref.f64(w), ref.f64(b)
+    items = len(off) - 1
+    mean, rstd = (torch.full((items, groups), float("nan"), device="cuda") for _ in range(2))
+    x = s["x"].clone()
+    out = x if in_place else torch.full_like(x, float("nan"))
+    if stride:
+        x, _ = strided(x, stride)
+        out, wide = strided(out, 2 * stride)
+    p3d.p3d_group_norm(x, out, groups, off, w, b, kind, eps, mean, rstd)
+    torch.cuda.synchronize()
+    want, u = ref.group_norm(x64, off, groups, w64, b64, kind, eps)
+    m64, r64 = ref.group_stats(x64, off, groups, eps)
+    # the statistics: a chunk's are sums of batches' own means, each good to a
+    # few roundings of the largest value, 64 of them one after the other
+    top = float(x64.abs().max()) if n else 0.0
+    assert torch.all((mean.cpu().double() - m64).abs() <= 2 * ref.U * m64.abs() + 64 * ref.U * top)
+    assert torch.all((rstd.cpu().double() - r64).abs() <= 64 * ref.U * r64 * (1 + r64 * top * 1e-2))
+    # u: the mean's error times rstd and weight, and a few roundings of its terms;
+    # the activation: |act'| <= 1.13, and a hardware exponential and reciprocal
+    gain = ref.spread(r64, off, c) * (1 if w64 is None else w64.abs())
+    size = u.abs() + (0 if b64 is None else b64.abs())
+    slack = 1.2 * (64 * ref.U * top * gain + 80 * ref.U * size) + 4 * ref.U * want.abs() * (
+        2 + 2 * u.abs())
+    near(out, want, dtype, slack, "out")
+    if stride:
+        assert wide[:, :stride].isnan().all() and wide[:, stride + c:].isnan().all()
+
+    grads = ref.group_norm_backward(ref.f64(s["dout"]), x64, off, groups, w64, b64, kind, eps)
+    dweight, dbias = (torch.full((c,), float("nan"), device="cuda") for _ in range(2))
+    x, dout = s["x"].clone(), s["dout"].clone()
+    dx = dout if in_place else torch.full_like(x, float("nan"))
+    if stride:
+        x, _ = strided(x, stride)
+        dout, _ = strided(dout, 3 * stride)
+        dx, wide = strided(dx, 2 * stride)
+    p3d.p3d_group_norm_backward(dout, x, mean, rstd, dx, groups, off, w, b, kind, dweight, dbias)
+    torch.cuda.synchronize()
+    # du carries the slope's error (hardware exponential and reciprocal of u,
+    # and u's own), sums over rows a thread's serial roundings
+    d64 = ref.f64(s["dout"]).abs() * 1.2
+    du = d64 * (64 * ref.U * (2 + size) + 64 * ref.U * top * gain)
+    xn = (x64 - ref.spread(m64, off, c)).abs() * ref.spread(r64, off, c)
+    w1 = 1 if w64 is None else w64.abs()
+    terms = d64 * w1
+
+    def average(v):                          # over an item's group, back on its elements
+        out = torch.zeros(items, groups, dtype=torch.float64)
+        for i in range(items):
+            r = v[off[i]:off[i + 1]]
+            if r.shape[0]:
+                out[i] = r.reshape(-1, groups, c // groups).mean((0, 2))
+        return ref.spread(out, off, c)
+
+    each = du * w1 + 128 * ref.U * terms
+    slack = ref.spread(r64, off, c) * (each + average(each) + (xn + 1) * average(each * (xn + 1)))
+    near(dx, grads["dx"], dtype, slack, "dx")
+    sums = (du + 128 * ref.U * d64)
+    near(dbias, grads["dbias"], torch.float32, sums.sum(0), "dbias")
+    near(dweight, grads["dweight"], torch.float32, (sums * (xn + 1)).sum(0), "dweight")
+    if stride:
+        assert wide[:, :stride].isnan().all() and wide[:, stride + c:].isnan().all()
+
+
+@pytest.mark.parametrize("kind", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,c,groups", [
+    (1, 8, 1), (2, 8, 8), (3, 24, 3), (7, 40, 5), (5, 104, 13), (33, 64, 32), (100, 320, 32),
+    (257, 96, 1), (1000, 512, 32), (64, 2056, 8), (130, 4096, 32), (9, 4096, 4096),
+    (4097, 72, 9)])
+def test_sizes(n, c, groups, dtype, kind):
+    check(n, c, groups, TYPES[dtype], kind, seed=n + c)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,items", [(1, 3), (40, 7), (3000, 5), (20000, 17), (700, 256)])
+def test_ragged_items(n, items, dtype):
+    check(n, 64, 16, TYPES[dtype], "silu", uneven(n, items), seed=items)
+
+
+def test_one_channel_a_group_and_no_affine():
+    check(77, 12, 12, torch.float32, "gelu", affine=False)
+    check(77, 24, 24, torch.bfloat16, "none", affine=False)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_strided_rows_keep_what_lies_between(dtype):
+    check(301, 72, 9, TYPES[dtype], "silu", uneven(301, 4), stride=16)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_in_place(dtype):
+    check(1500, 128, 8, TYPES[dtype], "silu", uneven(1500, 3), in_place=True)
+
+
+def test_a_large_mean_keeps_the_digits():
+    """Channels a thousand deviations from 0: the deviations come out as the
+    input holds them."""
+    s = made(5000, 64, torch.float32, 5)
+    s["x"] = (torch.randn(5000, 64, generator=torch.Generator().manual_seed(6)) + 1000).cuda()
+    check(5000, 64, 8, torch.float32, "none", s=s)
+
+
+def test_constant_rows():
+    """A variance of 0: out is act(bias), rstd is 1 / sqrt(eps)."""
+    s = made(500, 32, torch.float32, 7)
+    s["x"] = torch.full((500, 32), 3.25, device="cuda")
+    out, mean, rstd = torch.empty_like(s["x"]), torch.empty(1, 4, device="cuda"), torch.empty(
+        1, 4, device="cuda")
+    p3d.p3d_group_norm(s["x"], out, 4, weight=s["w"], bias=s["b"], mean=mean, rstd=rstd)
+    assert torch.equal(out, s["b"].expand(500, 32)) and (mean == 3.25).all()
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_values_that_are_not_finite_stay_in_their_group(dtype):
+    n, c, groups, off = 300, 64, 8, [0, 100, 250, 300]
+    s = made(n, c, TYPES[dtype], 8)
+    clean = torch.empty_like(s["x"])
+    p3d.p3d_group_norm(s["x"], clean, groups, off, s["w"], s["b"], "silu")
+    s["x"][120, 10] = float("nan")
+    s["x"][220, 63] = float("inf")
+    out = torch.empty_like(clean)
+    p3d.p3d_group_norm(s["x"], out, groups, off, s["w"], s["b"], "silu")
+    bad = torch.zeros(n, c, dtype=torch.bool, device="cuda")
+    bad[100:250, 8:16] = True
+    bad[100:250, 56:64] = True
+    assert out[bad].isnan().all() and torch.equal(out[~bad], clean[~bad])
+
+
+def test_no_rows():
+    x = torch.empty(0, 32, device="cuda")
+    mean, rstd = torch.empty(2, 4, device="cuda"), torch.empty(2, 4, device="cuda")
+    p3d.p3d_group_norm(x, x.clone(), 4, [0, 0, 0], mean=mean, rstd=rstd)
+    assert (mean == 0).all() and torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5))
+    dw, db = torch.full((32,), 7.0, device="cuda"), torch.full((32,), 7.0, device="cuda")
+    p3d.p3d_group_norm_backward(x, x, mean, rstd, x.clone(), 4, [0, 0, 0], dweight=dw, dbias=db)
+    assert not dw.any() and not db.any()
+
+
+def test_only_the_gradients_that_are_wanted():
+    s = made(400, 64, torch.bfloat16, 9)
+    mean, rstd = torch.empty(1, 8, device="cuda"), torch.empty(1, 8, device="cuda")
+    p3d.p3d_group_norm(s["x"], torch.empty_like(s["x"]), 8, mean=mean, rstd=rstd)
+    got = []
+    for dw, db in ((1, 1), (1, 0), (0, 1), (0, 0)):
+        dx = torch.empty_like(s["x"])
+        dw, db = (torch.empty(64, device="cuda") if k else None for k in (dw, db))
+        p3d.p3d_group_norm_backward(s["dout"], s["x"], mean, rstd, dx, 8, dweight=dw, dbias=db)
+        got.append((dx, dw, db))
+    assert all(torch.equal(g[0], got[0][0]) for g in got)
+    assert torch.equal(got[1][1], got[0][1]) and torch.equal(got[2][2], got[0][2])
+
+
+def test_the_same_call_gives_the_same_bytes():
+    s = made(30000, 256, torch.bfloat16, 10)
+    off = uneven(30000, 5)
+    runs = []
+    for _ in range(3):
+        mean, rstd = torch.empty(5, 32, device="cuda"), torch.empty(5, 32, device="cuda")
+        out, dx = torch.empty_like(s["x"]), torch.empty_like(s["x"])
+        dw, db = torch.empty(256, device="cuda"), torch.empty(256, device="cuda")
+        p3d.p3d_group_norm(s["x"], out, 32, off, s["w"], s["b"], "silu", 1e-5, mean, rstd)
+        p3d.p3d_group_norm_backward(s["dout"], s["x"], mean, rstd, dx, 32, off, s["w"], s["b"],
+                                    "silu", dw, db)
+        runs.append((out, mean, rstd, dx, dw, db))
+    for r in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(r, runs[0]))
+
+
+def test_gradient_against_differences():
+    """Central differences of the GPU's own forward results in binary32, summed
+    in 64 bits: a difference's error is the results' over the step."""
+    n, c, groups = 40, 16, 4
+    s = made(n, c, torch.float32, 11)
+    mean, rstd = torch.empty(1, groups, device="cuda"), torch.empty(1, groups, device="cuda")
+
+    def loss(x):
+        out = torch.empty_like(x)
+        p3d.p3d_group_norm(x, out, groups, weight=s["w"], bias=s["b"], act="silu", mean=mean,
+                           rstd=rstd)
+        return float((out.double() * s["dout"].double()).sum())
+
+    loss(s["x"])
+    dx = torch.empty_like(s["x"])
+    p3d.p3d_group_norm_backward(s["dout"], s["x"], mean, rstd, dx, groups, weight=s["w"],
+                                bias=s["b"], act="silu")
+    h = 2.0 ** -6
+    for i in range(0, n * c, 37):
+        ends = []
+        for d in (h, -h):
+            x = s["x"].clone()
+            x.view(-1)[i] += d
+            ends.append(loss(x))
+        # (640 results of size 3 good to 2^-20, over 2 h; and h^2 / 6 of a third
+        # derivative of a few units)
+        assert abs((ends[0] - ends[1]) / (2 * h) - float(dx.view(-1)[i])) < 640 ** 0.5 * 3 * (
+            2.0 ** -20) / h + 10 * h * h, i
