@@ -6,9 +6,12 @@
 // Tiles of out features x tokens, the weights as the row operand of
 // v_mfma_i32_32x32x32_i8 (a lane holds 16 neighbouring integers of one row,
 // half l / 32 of 32) and the tokens as the column operand, so that a lane's
-// results are neighbouring features of one token. K advances in chunks of 128
-// integers: rows of 128 bytes in LDS, 16-byte slots swizzled so that 16 lanes
-// reading one slot of 16 neighbouring rows meet every bank once.
+// results are neighbouring features of one token. K advances in stages of 64
+// integers, four of them in LDS: while one is multiplied the next has arrived
+// and two more are on their way, which covers the memory's latency with one
+// workgroup on a CU.
+#include <type_traits>
+
 #include "attn_tile.h"
 #include "model_internal.h"
 
@@ -23,8 +26,8 @@ using attn::tile_barrier;
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kThreads = 256;
-constexpr int kStep = 128;                      // integers of K in a stage
+constexpr int kStep = 64, kSlots = kStep / 16;  // integers and 16-byte slots of a row in a stage
+constexpr int kStages = 4;                      // in LDS
 
 __device__ __forceinline__ i32x16 mfma(i32x4 a, i32x4 b, i32x16 c) {
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
@@ -79,71 +82,41 @@ struct Finish {
 };
 
 // ------------------------------------------------------------------ tiles ---
-// Four waves, 2 x 2 of them, each BI x BJ blocks of 32 features x 32 tokens.
-template <int BI, int BJ>
+// WM x WN waves, each BI x BJ blocks of 32 features x 32 tokens.
+template <int BI_, int BJ_, int WM_, int WN_>
 struct Shape {
-    static constexpr int M = 64 * BI, N = 64 * BJ;              // features, tokens
+    static constexpr int BI = BI_, BJ = BJ_, WM = WM_, kWaves = WM_ * WN_, kThreads = 64 * kWaves;
+    static constexpr int M = WM_ * BI * 32, N = WN_ * BJ * 32;  // features, tokens
     static constexpr int kStage = (M + N) * kStep;              // bytes
     static constexpr int kPitch = BI * 32 + 4;                  // floats of a staged token
-    static constexpr int kStaged = 4 * 32 * kPitch * 4;
-    static constexpr int kLds = 2 * kStage > kStaged ? 2 * kStage : kStaged;
+    static constexpr int kStaged = kWaves * 32 * kPitch * 4;
+    static constexpr int kLds = kStages * kStage > kStaged ? kStages * kStage : kStaged;
+    static constexpr int LM = M / 16 / kWaves, LN = N / 16 / kWaves;    // loads of a wave, a stage
 };
 
-__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
-
-// Rows [0, Rows) of a tile from `base` on (rows past `last` repeat it; what they
-// give is not stored), into LDS at `to`: a uniform base and a 32-bit offset a
-// lane (rows are at most 2^22 bytes apart). Of a last chunk that K ends in only
-// the `slots` that exist are loaded; `Zero` puts zeros into the others. (One
-// operand's zeros are enough: integers have no NaN.) The lane number is opaque:
-// offsets made ahead of the loop would take registers that the products need.
-template <int Rows, bool Zero>
-__device__ __forceinline__ void load_tile(const int8_t* base, int stride, int last, int slots,
-                                          char* lds, int wave, int lane) {
-    const uint32_t to = lds_offset(lds);
-    asm volatile("" : "+v"(lane));
-    const int slot = (lane & 7) ^ swizzle(wave * 8 + (lane >> 3));  // (of every row below)
-    const auto offset = [&](int i) {
-        return (uint32_t)(min((i * 4 + wave) * 8 + (lane >> 3), last) * stride + slot * 16);
-    };
-    if (slots >= 8) {
-#pragma unroll
-        for (int i = 0; i < Rows / 32; ++i)
-            dma16_from(base, offset(i), to + (i * 4 + wave) * 8 * kStep);
-        return;
-    }
-#pragma unroll 1
-    for (int i = 0; i < Rows / 32; ++i) {
-        const int r0 = (i * 4 + wave) * 8;
-        if (slot < slots) dma16_from(base, offset(i), to + r0 * kStep);
-        else if (Zero)
-            reinterpret_cast<uint4*>(lds)[r0 * 8 + lane] = make_uint4(0, 0, 0, 0);
-    }
-}
+// Slot c of row r of a stage sits at c ^ swizzle(r): 16 lanes that read one
+// slot of 16 neighbouring rows (64 bytes each) meet every bank once.
+__device__ __forceinline__ int swizzle(int row) { return (row >> 2) & (kSlots - 1); }
 
 typedef const __attribute__((address_space(3))) char lds_char;
 
-__device__ __forceinline__ uint32_t frag_base(const char* tile, int row0, int lane) {
-    const int r = lane & 31;
-    uint32_t at = lds_offset(tile) + (row0 + r) * kStep + (((lane >> 5) ^ swizzle(r)) << 4);
-    asm volatile("" : "+v"(at));
-    return at;
+// 16 bytes of LDS from `at`, a register, and a constant distance on.
+__device__ __forceinline__ i32x4 read_frag(uint32_t at, int on) {
+    return *(const __attribute__((address_space(3))) i32x4*)((lds_char*)(uintptr_t)at + on);
 }
 
-template <int B>
-__device__ __forceinline__ void read_frags(uint32_t base, int step, i32x4 (&f)[B]) {
-    lds_char* p = (lds_char*)(uintptr_t)(base ^ (32 * step));
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-        f[i] = *(const __attribute__((address_space(3))) i32x4*)(p + i * 32 * kStep);
-}
+// The order of a stage's instructions is the source's: the fragments and loads
+// of what comes next stand between the products, one at a time.
+__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
 
-template <typename T, int Act, int BI, int BJ>
-__global__ __launch_bounds__(kThreads, (BI * BJ > 8 ? 1 : 2)) void linear_kernel(
-    LinearArgs a, int tiles_m, int tiles) {
-    using S = Shape<BI, BJ>;
+__device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
+
+template <typename T, int Act, typename S>
+__global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, int tiles_m,
+                                                               int tiles) {
+    constexpr int BI = S::BI, BJ = S::BJ, LM = S::LM, LN = S::LN, kLoads = LM + LN;
     extern __shared__ __align__(256) char lds[];    // (fragments reach a slot by an exclusive or)
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     // Workgroups go round the 8 dies: each die takes a run of tiles, features
     // fastest, so that a token tile is read into one die's L2 once.
     const int per = (tiles + 7) / 8;
@@ -151,17 +124,40 @@ __global__ __launch_bounds__(kThreads, (BI * BJ > 8 ? 1 : 2)) void linear_kernel
     if (tile >= tiles || (int)(blockIdx.x >> 3) >= per) return;
     const int m0 = tile % tiles_m * S::M;
     const int64_t n0 = (int64_t)(tile / tiles_m) * S::N;
-    const int last_m = a.out_dim - 1 - m0;
-    const int last_n = a.n - n0 < S::N ? (int)(a.n - n0) - 1 : S::N - 1;
-    const int8_t *wm0 = a.weight + (int64_t)m0 * a.in_dim, *qn0 = a.q + n0 * a.q_stride;
     const int stages = (a.in_dim + kStep - 1) / kStep;
 
-    const auto load = [&](int st) {
-        char* to = lds + (st & 1) * S::kStage;
-        const int slots = (a.in_dim - st * kStep) / 16;
-        load_tile<S::M, true>(wm0 + st * kStep, a.in_dim, last_m, slots, to, wave, lane);
-        load_tile<S::N, false>(qn0 + st * kStep, (int)a.q_stride, last_n, slots, to + S::M * kStep,
-                               wave, lane);
+    // Loads: 16 rows an instruction, a uniform base and a 32-bit offset a lane
+    // (rows are at most 2^22 bytes apart). Rows past the last repeat it; what
+    // they give is not stored. Slots past K, in the last stage, repeat the
+    // row's first there; the weights' fragments of those are cleared.
+    const int8_t *wm0 = a.weight + (int64_t)m0 * a.in_dim, *qn0 = a.q + n0 * a.q_stride;
+    const int last_m = a.out_dim - 1 - m0;
+    const int last_n = a.n - n0 < S::N ? (int)(a.n - n0) - 1 : S::N - 1;
+    const int row = wave * 16 + (lane >> 2), slot = (lane & 3) ^ swizzle(row);
+    const int last_slots = (a.in_dim - (stages - 1) * kStep) / 16;
+    const int back = slot < last_slots ? 0 : slot * 16;
+    int off_m[LM], off_n[LN];
+#pragma unroll
+    for (int i = 0; i < LM; ++i)
+        off_m[i] = min(i * 16 * S::kWaves + row, last_m) * a.in_dim + slot * 16;
+#pragma unroll
+    for (int j = 0; j < LN; ++j)
+        off_n[j] = min(j * 16 * S::kWaves + row, last_n) * (int)a.q_stride + slot * 16;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds)) + wave * 16 * kStep;
+    // load `l` (0 .. kLoads) of this wave's share of stage st
+    const auto load = [&](int st, int l) {
+        const uint32_t to =
+            lds0 + (st & (kStages - 1)) * S::kStage + l * 16 * S::kWaves * kStep;
+        if (l < LM) dma16_from(wm0 + st * kStep, off_m[l < LM ? l : 0], to);
+        else dma16_from(qn0 + st * kStep, off_n[l < LM ? 0 : l - LM], to);
+    };
+    const auto before_load = [&](int st) {
+        if (st == stages - 1) {
+#pragma unroll
+            for (int i = 0; i < LM; ++i) off_m[i] -= back;
+#pragma unroll
+            for (int j = 0; j < LN; ++j) off_n[j] -= back;
+        }
     };
 
     i32x16 acc[BI][BJ];
@@ -172,43 +168,96 @@ __global__ __launch_bounds__(kThreads, (BI * BJ > 8 ? 1 : 2)) void linear_kernel
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
-    const int wm = (wave & 1) * BI * 32, wn = (wave >> 1) * BJ * 32;
-    const uint32_t fa = frag_base(lds, wm, lane), fb = frag_base(lds + S::M * kStep, wn, lane);
+    const int wm = wave % S::WM * BI * 32, wn = wave / S::WM * BJ * 32;
+    const int r32 = lane & 31;
+    uint32_t at = ((lane >> 5) ^ swizzle(r32)) << 4;
+    at += lds_offset(lds) + r32 * kStep;
+    const uint32_t fa = at + wm * kStep, fb = at + (S::M + wn) * kStep;
     i32x4 fm[2][BI], fn[2][BJ];
+    // where step s of stage st has this lane's fragments; fragment f of it
+    struct Place { uint32_t m, n; };
+    const auto place = [&](int st, int s) {
+        const uint32_t stage = (st & (kStages - 1)) * S::kStage;
+        Place p{(fa ^ (32 * s)) + stage, (fb ^ (32 * s)) + stage};
+        asm volatile("" : "+v"(p.m), "+v"(p.n));
+        return p;
+    };
+    const auto read = [&](const Place& p, int s, int f) {
+        if (f < BI) fm[s][f < BI ? f : 0] = read_frag(p.m, f * 32 * kStep);
+        else fn[s][f < BI ? 0 : f - BI] = read_frag(p.n, (f - BI) * 32 * kStep);
+    };
+    const auto clear = [&](int s) {                 // what lies past K
+        if (2 * s + (lane >> 5) >= last_slots)
+#pragma unroll
+            for (int i = 0; i < BI; ++i) fm[s][i] = i32x4{0, 0, 0, 0};
+    };
 
-    load(0);
-    tile_barrier();
-    read_frags<BI>(fa, 0, fm[0]);
-    read_frags<BJ>(fb, 0, fn[0]);
-    if (stages > 1) load(1);
-    for (int st = 0; st < stages; ++st) {
-        const uint32_t at = (st & 1) * S::kStage, other = S::kStage - at;
+    // A stage: two steps of 32. `flying`: later stages' loads that stay on
+    // their way when the next one has to be there.
+    constexpr int kProducts = BI * BJ, kFrags = BI + BJ;
+    const auto stage = [&](int st, auto flying, auto loads, auto next) {
+        constexpr bool kLoad = decltype(loads)::value, kNext = decltype(next)::value;
+        if constexpr (!kNext) clear(0);
+        if constexpr (kLoad) before_load(st + kStages);
+        const Place here = place(st, 1), then = place(st + 1, 0);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int cur = s & 1, nxt = cur ^ 1;
-            if (s < 3) {
-                read_frags<BI>(fa + at, s + 1, fm[nxt]);
-                read_frags<BJ>(fb + at, s + 1, fn[nxt]);
-            } else if (st + 1 < stages) {
-                // The next stage has come, and every wave has its last
-                // fragments of this one: its place is free.
-                tile_barrier();
-                read_frags<BI>(fa + other, 0, fm[nxt]);
-                read_frags<BJ>(fb + other, 0, fn[nxt]);
-                if (st + 2 < stages) load(st + 2);
-            }
+        for (int p = 0, f = 0; p < kProducts; ++p) {
+            acc[p / BJ][p % BJ] = mfma(fm[0][p / BJ], fn[0][p % BJ], acc[p / BJ][p % BJ]);
 #pragma unroll
-            for (int i = 0; i < BI; ++i)
-#pragma unroll
-                for (int j = 0; j < BJ; ++j)
-                    acc[i][j] = mfma(fm[cur][i], fn[cur][j], acc[i][j]);
+            for (; f < kFrags && f * kProducts < (p + 1) * 2 * kFrags; ++f) read(here, 1, f);
+            pin();
         }
-    }
+        // Every wave has its fragments of this stage, so its place is free, and
+        // the next stage has come.
+        if constexpr (kNext) {
+            attn::wave_wait<decltype(flying)::value * kLoads>();
+            meet();
+        } else {
+            clear(1);
+        }
+        pin();
+#pragma unroll
+        for (int p = 0, f = 0, l = 0; p < kProducts; ++p) {
+            acc[p / BJ][p % BJ] = mfma(fm[1][p / BJ], fn[1][p % BJ], acc[p / BJ][p % BJ]);
+            if constexpr (kNext) {
+#pragma unroll
+                for (; f < kFrags && f * kProducts < (p + 1) * 2 * kFrags; ++f) read(then, 0, f);
+            }
+            if constexpr (kLoad) {
+#pragma unroll
+                for (; l < kLoads && l * kProducts < (2 * p + 2 - kProducts) * kLoads; ++l)
+                    load(st + kStages, l);
+            }
+            pin();
+        }
+    };
+    using std::integral_constant;
+    using Yes = std::true_type;
+    using No = std::false_type;
+
+#pragma unroll
+    for (int st = 0; st < kStages; ++st)
+        if (st < stages) {
+            before_load(st);
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) load(st, l);
+        }
+    if (stages >= 4) attn::wave_wait<3 * kLoads>();
+    else attn::wave_wait<0>();
+    meet();
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) read(place(0, 0), 0, f);
+    int st = 0;
+    for (; st + kStages < stages; ++st) stage(st, integral_constant<int, 2>(), Yes(), Yes());
+    if (stages - st >= 4) stage(st++, integral_constant<int, 2>(), No(), Yes());
+    if (stages - st >= 3) stage(st++, integral_constant<int, 1>(), No(), Yes());
+    if (stages - st >= 2) stage(st++, integral_constant<int, 0>(), No(), Yes());
+    stage(st, integral_constant<int, 0>(), No(), No());
     tile_barrier();                     // the tiles' place is the epilogue's
 
     // A wave turns 32 tokens at a time in LDS, so that a token's features
     // leave in 16-byte pieces of whole rows.
-    float* stage = reinterpret_cast<float*>(lds) + wave * 32 * S::kPitch;
+    float* turned = reinterpret_cast<float*>(lds) + wave * 32 * S::kPitch;
     constexpr int kAcross = BI * 4, kDown = 64 / kAcross;       // lanes of a token, tokens at once
     const int d = m0 + wm + (lane % kAcross) * 8;
     Finish<T, Act> finish;
@@ -220,7 +269,7 @@ __global__ __launch_bounds__(kThreads, (BI * BJ > 8 ? 1 : 2)) void linear_kernel
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const i32x16& v = acc[i][j];
-                *reinterpret_cast<float4*>(stage + (lane & 31) * S::kPitch + i * 32 + q * 8 +
+                *reinterpret_cast<float4*>(turned + (lane & 31) * S::kPitch + i * 32 + q * 8 +
                                            (lane >> 5) * 4) =
                     make_float4((float)v[4 * q], (float)v[4 * q + 1], (float)v[4 * q + 2],
                                 (float)v[4 * q + 3]);
@@ -229,7 +278,7 @@ __global__ __launch_bounds__(kThreads, (BI * BJ > 8 ? 1 : 2)) void linear_kernel
 #pragma unroll 2
         for (int r = lane / kAcross; r < 32; r += kDown) {
             const int64_t token = n0 + wn + j * 32 + r;
-            const float* from = stage + r * S::kPitch + (lane % kAcross) * 8;
+            const float* from = turned + r * S::kPitch + (lane % kAcross) * 8;
             const float4 x = *reinterpret_cast<const float4*>(from),
                          y = *reinterpret_cast<const float4*>(from + 4);
             float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -305,14 +354,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinearArgs a
 }
 
 // ----------------------------------------------------------------- launch ---
-template <typename T, int Act, int BI, int BJ>
+template <typename T, int Act, typename S>
 hipError_t tiles_of(const LinearArgs& a, hipStream_t s) {
-    using S = Shape<BI, BJ>;
     const int64_t tiles_m = (a.out_dim + S::M - 1) / S::M, tiles_n = (a.n + S::N - 1) / S::N;
     const int64_t tiles = tiles_m * tiles_n;
     const unsigned grid = (unsigned)((tiles + 7) / 8 * 8);
-    linear_kernel<T, Act, BI, BJ>
-        <<<grid, kThreads, S::kLds, s>>>(a, (int)tiles_m, (int)tiles);
+    linear_kernel<T, Act, S><<<grid, S::kThreads, S::kLds, s>>>(a, (int)tiles_m, (int)tiles);
     return hipGetLastError();
 }
 
@@ -326,9 +373,9 @@ hipError_t linear_of(const LinearArgs& a, hipStream_t s) {
         const auto tiles = [&](int m) {
             return ((a.out_dim + m - 1) / m) * ((a.n + m - 1) / m);
         };
-        if (tiles(256) >= kComputeUnits) return tiles_of<T, Act, 4, 4>(a, s);
-        if (tiles(128) >= kComputeUnits / 2) return tiles_of<T, Act, 2, 2>(a, s);
-        return tiles_of<T, Act, 1, 1>(a, s);
+        if (tiles(256) >= kComputeUnits) return tiles_of<T, Act, Shape<4, 2, 2, 4>>(a, s);
+        if (tiles(128) >= kComputeUnits / 2) return tiles_of<T, Act, Shape<2, 2, 2, 2>>(a, s);
+        return tiles_of<T, Act, Shape<1, 1, 2, 2>>(a, s);
     }
     return hipGetLastError();
 }
