@@ -59,10 +59,11 @@ struct Finish {
             f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
         }
     }
-    __device__ __forceinline__ void write(const LinearArgs& a, int64_t token, int d, float s,
+    // (f: the sums times the token's scale)
+    __device__ __forceinline__ void write(const LinearArgs& a, int64_t token, int d,
                                           float (&f)[8]) const {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = activate<Act>(f[e] * s * t[e] + b[e]);
+        for (int e = 0; e < 8; ++e) f[e] = activate<Act>(f[e] * t[e] + b[e]);
         if (a.residual) {
             float r[8];
             read(a.residual, token * a.residual_stride + d, r);
@@ -231,6 +232,19 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
             pin();
         }
     };
+    // What the epilogue needs: the scales of the lane's tokens, and eight
+    // features' of the lane's in the turned tile.
+    constexpr int kAcross = BI * 4, kDown = 64 / kAcross;       // lanes of a token, tokens at once
+    const int d = m0 + wm + (lane % kAcross) * 8;
+    Finish<T, Act> finish;
+    if (d < a.out_dim) finish.load(a, d);
+    float scale[BJ];
+#pragma unroll
+    for (int j = 0; j < BJ; ++j) {
+        const int64_t token = n0 + wn + j * 32 + r32;
+        scale[j] = a.scale[token < a.n ? token : a.n - 1];
+    }
+
     using std::integral_constant;
     using Yes = std::true_type;
     using No = std::false_type;
@@ -258,10 +272,6 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
     // A wave turns 32 tokens at a time in LDS, so that a token's features
     // leave in 16-byte pieces of whole rows.
     float* turned = reinterpret_cast<float*>(lds) + wave * 32 * S::kPitch;
-    constexpr int kAcross = BI * 4, kDown = 64 / kAcross;       // lanes of a token, tokens at once
-    const int d = m0 + wm + (lane % kAcross) * 8;
-    Finish<T, Act> finish;
-    if (d < a.out_dim) finish.load(a, d);
 #pragma unroll
     for (int j = 0; j < BJ; ++j) {
 #pragma unroll
@@ -269,10 +279,10 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const i32x16& v = acc[i][j];
-                *reinterpret_cast<float4*>(turned + (lane & 31) * S::kPitch + i * 32 + q * 8 +
+                *reinterpret_cast<float4*>(turned + r32 * S::kPitch + i * 32 + q * 8 +
                                            (lane >> 5) * 4) =
-                    make_float4((float)v[4 * q], (float)v[4 * q + 1], (float)v[4 * q + 2],
-                                (float)v[4 * q + 3]);
+                    make_float4((float)v[4 * q] * scale[j], (float)v[4 * q + 1] * scale[j],
+                                (float)v[4 * q + 2] * scale[j], (float)v[4 * q + 3] * scale[j]);
             }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 2
@@ -282,7 +292,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
             const float4 x = *reinterpret_cast<const float4*>(from),
                          y = *reinterpret_cast<const float4*>(from + 4);
             float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            if (token < a.n && d < a.out_dim) finish.write(a, token, d, a.scale[token], f);
+            if (token < a.n && d < a.out_dim) finish.write(a, token, d, f);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
@@ -345,11 +355,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinearArgs a
             int s = 0;
 #pragma unroll
             for (int k = 0; k < kFewWaves; ++k) s += part[k][token][d + e];
-            f[e] = (float)s;
+            f[e] = (float)s * a.scale[token];
         }
         Finish<T, Act> finish;
         finish.load(a, d0 + d);
-        finish.write(a, token, d0 + d, a.scale[token], f);
+        finish.write(a, token, d0 + d, f);
     }
 }
 
