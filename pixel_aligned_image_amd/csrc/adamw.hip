@@ -13,7 +13,9 @@
 // 8-bit states: a thread holds 8 neighbouring elements and 32 neighbouring
 // threads a block of 256 that shares a scale, so a block's largest state is a
 // maximum over half a wave and the states are read and written once.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "model_internal.h"
 
@@ -23,9 +25,8 @@ namespace {
 
 constexpr int kThreads = 256, kPer = 8;             // elements of a thread, neighbours
 constexpr int kTensors = 40;                        // of a launch
-constexpr int kRounds = 2;
-constexpr int64_t kChunk = (int64_t)kThreads * kPer * kRounds;
-constexpr int64_t kNormChunk = 4 * kChunk;
+constexpr int64_t kChunk = (int64_t)kThreads * kPer;
+constexpr int kNormLoads = 8;                       // 16 bytes each, of a thread and a chunk
 constexpr int64_t kMaxGrid = int64_t(1) << 23;      // (a grid has fewer than 2^32 threads)
 
 struct Entry {
@@ -35,7 +36,6 @@ struct Entry {
     void *m, *v;
     float *m_scale, *v_scale;
     int64_t size;
-    uint32_t first;             // chunk of the launch
     uint32_t key;               // of the tensor's random bits
     float keep;                 // 1 - lr decay, or decay where lr is the device's
 };
@@ -55,17 +55,16 @@ struct Step {
 
 struct Table {
     Entry e[kTensors];
+    uint32_t first[kTensors];   // chunk of the launch
 };
 
-// The last tensor whose chunks start at or before `chunk` (tensors without
-// elements have no chunks and start where the next one does).
+// The last tensor whose chunks start at or before `chunk`: a lane looks at one
+// (a search would wait for a load per step).
 __device__ __forceinline__ int tensor_of(const Table& t, int count, uint32_t chunk) {
-    int lo = 0, hi = count;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (t.e[mid].first <= chunk) lo = mid; else hi = mid;
-    }
-    return lo;
+    static_assert(kTensors <= 64, "a lane a tensor");
+    const int lane = threadIdx.x & 63;
+    const uint64_t starts = __ballot(lane < count && t.first[lane < count ? lane : 0] <= chunk);
+    return __builtin_amdgcn_readfirstlane(63 - __clzll((long long)starts));
 }
 
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -85,12 +84,14 @@ __device__ __forceinline__ void widen8(const float* p, float (&f)[8]) {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
+// (past the caches: 231 us for 252 where 44 million elements of 28 bytes stream by)
 __device__ __forceinline__ void narrow8(Bf16* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(p) = Vec<Bf16>::narrow(f);
+    store_nt16(p, Vec<Bf16>::narrow(f));
 }
 __device__ __forceinline__ void narrow8(float* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
+    store_nt16(p, Vec<float>::narrow(a));
+    store_nt16(p + 4, Vec<float>::narrow(b));
 }
 __device__ __forceinline__ float widen1(Bf16 v) { return __uint_as_float((uint32_t)v.bits << 16); }
 __device__ __forceinline__ float widen1(float v) { return v; }
@@ -153,32 +154,33 @@ __device__ __forceinline__ void decode8(uint2 c, float by, float (&f)[8]) {
     for (int e = 0; e < 8; ++e) f[e] = v[e >> 1][e & 1] * by;
 }
 
-// The e4m3 number of |q| <= 448 that 16 random bits choose of the two around
-// it. From 2^-6 on a number keeps 3 of binary32's 23 mantissa bits: the random
-// bits go into the upper 16 of the 20 dropped ones (a carry moves on to the
-// next exponent as it should) and the exponent's bias changes by 120 (120 << 3
-// = 960). Below, numbers are multiples of 2^-9.
-__device__ __forceinline__ uint32_t encode(float q, uint32_t bits) {
-    const float a = fminf(fabsf(q), 448.f);
-    const uint32_t normal = ((__float_as_uint(a) + (bits << 4)) >> 20) - 960u;
-    const uint32_t small = (uint32_t)(a * 512.f + (float)bits * 0x1p-16f);
-    return (a < 0x1p-6f ? small : normal) | (__float_as_uint(q) >> 31 << 7);
+// The e4m3 number that the 16 random bits in `high`'s upper half choose of the
+// two around q, limited to 448, into byte `At` of `word`: the hardware's
+// conversion adds random bits 31 .. 12 to the 20 mantissa bits that it drops (a
+// carry moves on to the next exponent as it should), below 2^-6 to the bits
+// below 2^-9.
+template <int At>
+__device__ __forceinline__ uint32_t encode(float q, uint32_t high, uint32_t word) {
+    return (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(__builtin_amdgcn_fmed3f(q, -448.f, 448.f),
+                                                     high, (int)word, At);
 }
 
-// Maximum over 32 neighbouring lanes, in each of them.
-__device__ __forceinline__ float half_max(float v) {
-    float a;
-    v = fmaxf(v, dpp<0xB1>(v));
-    v = fmaxf(v, dpp<0x4E>(v));
-    v = fmaxf(v, dpp<0x141>(v));
-    v = fmaxf(v, dpp<0x140>(v));
-    const float b = other_row16(v, a);
-    return fmaxf(a, b);
+// The largest of 32 neighbouring lanes' numbers, in each of them. Magnitudes
+// compare as their bits do: NaN is above infinity, and that above the rest.
+__device__ __forceinline__ uint32_t half_max(uint32_t v) {
+    const auto step = [&](float other) { v = max(v, __float_as_uint(other)); };
+    step(dpp<0xB1>(__uint_as_float(v)));
+    step(dpp<0x4E>(__uint_as_float(v)));
+    step(dpp<0x141>(__uint_as_float(v)));
+    step(dpp<0x140>(__uint_as_float(v)));
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max(r[0], r[1]);
 }
 
-// A block's scale and what its states are multiplied by. NaN and infinite
-// states leave a scale that is not finite.
-__device__ __forceinline__ void block_scale(float top, float& scale, float& by) {
+// A block's scale, from its largest state, and what its states are multiplied
+// by. A state that is not finite leaves a scale that is not.
+__device__ __forceinline__ void block_scale(uint32_t largest, float& scale, float& by) {
+    float top = __uint_as_float(largest);
     if (top < 0x1p-100f) top = 0.f;
     scale = top / 448.f;
     by = top == 0.f ? 0.f : 448.f / top;
@@ -203,97 +205,137 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table table, Step s) {
         s.rate = (float)(lr / (1. - exp2((double)n * s.log_b1)));
         s.norm = (float)(1. / sqrt(1. - exp2((double)n * s.log_b2)));
     }
-    const int64_t i0 = (int64_t)(blockIdx.x - t.first) * kChunk;
+    const int64_t i = (int64_t)(blockIdx.x - table.first[at]) * kChunk + threadIdx.x * kPer;
+    const int64_t left = t.size - i;
+    const int live = left >= kPer ? kPer : left > 0 ? (int)left : 0;
+    // (in 8 bits a wave stays whole: its lanes exchange the maximum)
+    if (Bits == 32 ? live == 0 : __ballot(live > 0) == 0) return;
+    float g[8], m[8], v[8], w[8];
+    read8<G>(t.grad, i, live, g);
+    if constexpr (Master) read8<float>(t.master, i, live, w);
+    else read8<P>(t.param, i, live, w);
+    if constexpr (Bits == 32) {
+        read8<float>(t.m, i, live, m);
+        read8<float>(t.v, i, live, v);
+    } else {
+        const uint2 cm = codes8(t.m, i, live), cv = codes8(t.v, i, live);
+        const float sm = live ? t.m_scale[i >> 8] : 0.f, sv = live ? t.v_scale[i >> 8] : 0.f;
+        decode8(cm, sm, m);
+        decode8(cv, sv, v);
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        const int64_t i = i0 + (int64_t)(r * kThreads + threadIdx.x) * kPer;
-        const int64_t left = t.size - i;
-        const int live = left >= kPer ? kPer : left > 0 ? (int)left : 0;
-        // (in 8 bits a wave stays whole: its lanes exchange the maximum)
-        if (Bits == 32 ? live == 0 : __ballot(live > 0) == 0) continue;
-        float g[8], m[8], v[8], w[8];
-        read8<G>(t.grad, i, live, g);
-        if constexpr (Master) read8<float>(t.master, i, live, w);
-        else read8<P>(t.param, i, live, w);
+        for (int e = 0; e < 8; ++e) v[e] *= v[e];
+    }
+    float root[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float x = g[e] * by;
+        m[e] = s.b1 * m[e] + s.c1 * x;
+        v[e] = s.b2 * v[e] + s.c2 * x * x;
         if constexpr (Bits == 32) {
-            read8<float>(t.m, i, live, m);
-            read8<float>(t.v, i, live, v);
-        } else {
-            const uint2 cm = codes8(t.m, i, live), cv = codes8(t.v, i, live);
-            const float sm = live ? t.m_scale[i >> 8] : 0.f, sv = live ? t.v_scale[i >> 8] : 0.f;
-            decode8(cm, sm, m);
-            decode8(cv, sv, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= v[e];
-        }
-        float root[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float x = g[e] * by;
-            m[e] = s.b1 * m[e] + s.c1 * x;
-            v[e] = s.b2 * v[e] + s.c2 * x * x;
             root[e] = sqrtf(v[e]);
             w[e] = w[e] * keep - s.rate * m[e] / (root[e] * s.norm + s.eps);
-        }
-        if constexpr (Master) write8<float>(t.master, i, live, w);
-        write8<P>(t.param, i, live, w);
-        if constexpr (Bits == 32) {
-            write8<float>(t.m, i, live, m);
-            write8<float>(t.v, i, live, v);
         } else {
-            // a state that is not finite makes its block's scale so: x - x is
-            // 0 or NaN, and fmaxf would lose the NaN
-            float tm = 0.f, tv = 0.f, bad = 0.f;
+            // (hardware root and reciprocal, each good to its last place: the
+            // exact ones are 20 operations more of the 60 a state may cost)
+            root[e] = __builtin_amdgcn_sqrtf(v[e]);
+            w[e] = w[e] * keep -
+                   s.rate * m[e] * __builtin_amdgcn_rcpf(root[e] * s.norm + s.eps);
+        }
+    }
+    if constexpr (Master) write8<float>(t.master, i, live, w);
+    write8<P>(t.param, i, live, w);
+    if constexpr (Bits == 32) {
+        write8<float>(t.m, i, live, m);
+        write8<float>(t.v, i, live, v);
+    } else {
+        uint32_t tm = 0, tv = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                tm = fmaxf(tm, fabsf(m[e]));
-                tv = fmaxf(tv, root[e]);
-                bad += (m[e] - m[e]) + (root[e] - root[e]);
-            }
-            tm = half_max(bad == 0.f ? tm : INFINITY);
-            tv = half_max(bad == 0.f ? tv : INFINITY);
-            float sm, sv, bm, bv;
-            block_scale(tm, sm, bm);
-            block_scale(tv, sv, bv);
-            uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
-            const uint32_t high = (uint32_t)((uint64_t)i >> 32) * 0xDDB3D743u ^ t.key;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t bits = mix(((uint32_t)i + e) * 0x9E3779B1u ^ high);
-                const uint32_t a = encode(m[e] * bm, bits & 0xffffu);
-                uint32_t b = encode(root[e] * bv, bits >> 16);
-                if (b == 0 && root[e] * bv > 0.f) b = 1;
-                cm[e >> 2] |= a << (8 * (e & 3));
-                cv[e >> 2] |= b << (8 * (e & 3));
-            }
-            write_codes8(t.m, i, live, make_uint2(cm[0], cm[1]));
-            write_codes8(t.v, i, live, make_uint2(cv[0], cv[1]));
-            if ((threadIdx.x & 31) == 0 && live) {
-                t.m_scale[i >> 8] = sm;
-                t.v_scale[i >> 8] = sv;
-            }
+        for (int e = 0; e < 8; ++e) {
+            tm = max(tm, __float_as_uint(m[e]) & 0x7fffffffu);
+            tv = max(tv, __float_as_uint(root[e]) & 0x7fffffffu);
+        }
+        float sm, sv, bm, bv;
+        block_scale(half_max(tm), sm, bm);
+        block_scale(half_max(tv), sv, bv);
+        uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
+        const uint32_t base = (uint32_t)i * 0x9E3779B1u;
+        const uint32_t high = (uint32_t)((uint64_t)i >> 32) * 0xDDB3D743u ^ t.key;
+        const auto one = [&](auto at) {
+            constexpr int e = decltype(at)::value;
+            const uint32_t bits = mix((base + e * 0x9E3779B1u) ^ high);
+            // a root that is not 0 is at least the smallest number
+            float q = root[e] * bv;
+            q = q > 0.f ? fmaxf(q, 0x1p-9f) : q;
+            cm[e >> 2] = encode<(e & 3)>(m[e] * bm, bits << 16, cm[e >> 2]);
+            cv[e >> 2] = encode<(e & 3)>(q, bits & 0xffff0000u, cv[e >> 2]);
+        };
+        one(std::integral_constant<int, 0>());
+        one(std::integral_constant<int, 1>());
+        one(std::integral_constant<int, 2>());
+        one(std::integral_constant<int, 3>());
+        one(std::integral_constant<int, 4>());
+        one(std::integral_constant<int, 5>());
+        one(std::integral_constant<int, 6>());
+        one(std::integral_constant<int, 7>());
+        write_codes8(t.m, i, live, make_uint2(cm[0], cm[1]));
+        write_codes8(t.v, i, live, make_uint2(cv[0], cv[1]));
+        if ((threadIdx.x & 31) == 0 && live) {
+            t.m_scale[i >> 8] = sm;
+            t.v_scale[i >> 8] = sv;
         }
     }
 }
 
 // ------------------------------------------------------------------- norm ---
 
+// At most kNormGrid workgroups a launch take its chunks in turn, a chunk's loads
+// all on their way before the first is used. Squares and sums are binary64, so
+// that no gradient's square leaves the numbers.
+constexpr int64_t kNormGrid = 6 * kComputeUnits;
+constexpr int64_t norm_chunk(p3d_dtype dt) {
+    return (int64_t)kThreads * kNormLoads * (dt == P3D_BF16 ? 8 : 4);
+}
+
 template <typename G>
 __global__ __launch_bounds__(kThreads) void norm_parts_kernel(Table table, int count,
+                                                              uint32_t chunks,
                                                               double* __restrict__ parts) {
+    constexpr int N = Vec<G>::N;
+    constexpr int64_t kAll = (int64_t)kThreads * kNormLoads * N;
     __shared__ double wave[kThreads / 64];
-    const Entry& t = table.e[tensor_of(table, count, blockIdx.x)];
-    const int64_t i0 = (int64_t)(blockIdx.x - t.first) * kNormChunk + threadIdx.x * kPer;
-    double sum = 0.;
-#pragma unroll 4
-    for (int r = 0; r < kNormChunk / (kThreads * kPer); ++r) {
-        const int64_t i = i0 + (int64_t)r * kThreads * kPer, left = t.size - i;
-        if (left <= 0) break;
-        float g[8];
-        read8<G>(t.grad, i, left >= kPer ? kPer : (int)left, g);
+    double sums[4] = {0., 0., 0., 0.};
+    const auto add = [&](uint4 q) {
+        float g[N];
+        Vec<G>::widen(q, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fma((double)g[e], (double)g[e], sum);
+        for (int e = 0; e < N; ++e) sums[e & 3] = fma((double)g[e], (double)g[e], sums[e & 3]);
+    };
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int at = tensor_of(table, count, c);
+        const Entry& t = table.e[at];
+        const int64_t i0 = (int64_t)(c - table.first[at]) * kAll;
+        const G* g = reinterpret_cast<const G*>(t.grad);
+        if (t.size - i0 >= kAll) {
+            const uint4* p = reinterpret_cast<const uint4*>(g + i0) + threadIdx.x;
+            uint4 q[kNormLoads];
+#pragma unroll
+            for (int r = 0; r < kNormLoads; ++r) q[r] = p[r * kThreads];
+#pragma unroll
+            for (int r = 0; r < kNormLoads; ++r) add(q[r]);
+            continue;
+        }
+        for (int64_t i = i0 + threadIdx.x * N; i < t.size; i += (int64_t)kThreads * N) {
+            if (t.size - i >= N) {
+                add(*reinterpret_cast<const uint4*>(g + i));
+            } else {
+                for (int64_t k = i; k < t.size; ++k) {
+                    const double x = (double)widen1(g[k]);
+                    sums[0] = fma(x, x, sums[0]);
+                }
+            }
+        }
     }
+    double sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
     for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
     if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = sum;
     __syncthreads();
@@ -351,6 +393,7 @@ hipError_t in_launches(const p3d_adamw_desc& d, int64_t chunk, Run run) {
             const hipError_t e = flush();
             if (e != hipSuccess) return e;
         }
+        t.first[count] = (uint32_t)chunks;
         Entry& to = t.e[count++];
         to.param = x.param;
         to.master = x.master;
@@ -360,7 +403,6 @@ hipError_t in_launches(const p3d_adamw_desc& d, int64_t chunk, Run run) {
         to.m_scale = x.m_scale;
         to.v_scale = x.v_scale;
         to.size = x.size;
-        to.first = (uint32_t)chunks;
         to.key = mix((uint32_t)j * 0x9E3779B1u ^ key);
         to.keep = d.device_lr || d.device_step ? x.weight_decay
                                                : (float)(1. - d.lr * (double)x.weight_decay);
@@ -390,21 +432,29 @@ hipError_t adamw_grad(const p3d_adamw_desc& d, const Step& step, bool master, hi
 
 }  // namespace
 
+// (a launch's chunks, of which it has at most kNormGrid parts, in as many
+// launches as the table takes; more would be room for nothing)
 int64_t grad_norm_parts(const p3d_adamw_desc& d) {
     int64_t n = 0;
-    for (int32_t j = 0; j < d.count; ++j) n += (d.tensors[j].size + kNormChunk - 1) / kNormChunk;
+    (void)in_launches(d, norm_chunk(d.grad_dtype), [&](const Table&, int, int64_t chunks) {
+        n += std::min(chunks, kNormGrid);
+        return hipSuccess;
+    });
     return n;
 }
 
 hipError_t launch_grad_norm(const p3d_adamw_desc& d, float max_norm, float* out, double* parts,
                             hipStream_t s) {
     int64_t at = 0;
-    const hipError_t e = in_launches(d, kNormChunk, [&](const Table& t, int count, int64_t chunks) {
+    const hipError_t e = in_launches(d, norm_chunk(d.grad_dtype), [&](const Table& t, int count, int64_t chunks) {
+        const int64_t grid = std::min(chunks, kNormGrid);
         if (d.grad_dtype == P3D_BF16)
-            norm_parts_kernel<Bf16><<<(unsigned)chunks, kThreads, 0, s>>>(t, count, parts + at);
+            norm_parts_kernel<Bf16>
+                <<<(unsigned)grid, kThreads, 0, s>>>(t, count, (uint32_t)chunks, parts + at);
         else
-            norm_parts_kernel<float><<<(unsigned)chunks, kThreads, 0, s>>>(t, count, parts + at);
-        at += chunks;
+            norm_parts_kernel<float>
+                <<<(unsigned)grid, kThreads, 0, s>>>(t, count, (uint32_t)chunks, parts + at);
+        at += grid;
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;

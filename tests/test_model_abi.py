@@ -342,7 +342,7 @@ def test_grad_norm_checks(p3d):
     d = table(p3d)
     d.keep[0].size = 1 << 33
     size = p3d.lib.p3d_grad_norm_workspace_size(d)
-    assert size >= (1 << 33) // 65536 * 8 and size % 256 == 0
+    assert size >= 1536 * 8 and size % 256 == 0          # a part for each of 1536 workgroups
     assert p3d.lib.p3d_grad_norm_workspace_size(table(p3d, grad_dtype=4)) == 0
     assert "grad_dtype" in p3d.p3d_last_error()
 
