@@ -6,10 +6,12 @@
 //
 // Both directions are memory bound: statistics over a whole map stand between
 // the first and the last use of a row, so x (and dout) is read twice, from the
-// caches where it fits. A call is cut into chunks of whole rows; a thread owns
-// 16-byte vectors of channels and walks the chunk's rows, so loads are whole
-// rows and per-channel factors stay in registers. Chunk results go to the
-// workspace and a second kernel joins them in binary64, in a fixed order.
+// caches where it fits. A call is cut into chunks of rows and slices of whole
+// groups; a thread owns 16-byte vectors of channels and walks the chunk's rows,
+// so per-channel factors stay in registers. Slices are as narrow as whole cache
+// lines allow: the narrower, the more rows a chunk has, and the fewer chunks
+// there are to join. Chunk results go to the workspace and are joined in a
+// fixed order.
 #include <algorithm>
 
 #include "model_internal.h"
@@ -20,9 +22,10 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// How a workgroup's threads lie over vectors of channels and rows.
+// How a workgroup's threads lie over the vectors of its slice of channels, and
+// over rows.
 struct Lay {
-    int nv, tx, ty;             // vectors of a row; threads along it, rows at a time
+    int nv, tx, ty;             // vectors of the slice; threads along it, rows at a time
     __host__ __device__ explicit Lay(int vectors)
         : nv(vectors), tx(vectors < kThreads ? vectors : kThreads), ty(kThreads / tx) {}
 };
@@ -74,16 +77,22 @@ __device__ __forceinline__ void param(const void* base, int v, float other,
     }
 }
 
+// Lanes for each of `groups` in a workgroup.
+__device__ __forceinline__ int lanes_of(int groups) {
+    int lanes = 64;
+    while (lanes > 1 && lanes * groups > kThreads) lanes >>= 1;
+    return lanes;
+}
+
 // ------------------------------------------------------------- statistics ---
 // Count, mean and sum of squared deviations of a set of numbers, and the same
 // of two sets together: no sum of squares is ever taken about another point
 // than the set's own mean, so a mean far from 0 costs no digits.
-template <typename F>
 struct Moments {
-    F n, mean, m2;
-    __device__ __forceinline__ void join(F bn, F bmean, F bm2) {
-        if (bn == F(0)) return;
-        const F all = n + bn, w = bn / all, d = bmean - mean;
+    float n, mean, m2;
+    __device__ __forceinline__ void join(float bn, float bmean, float bm2) {
+        if (bn == 0.f) return;
+        const float all = n + bn, w = bn * __builtin_amdgcn_rcpf(all), d = bmean - mean;
         mean += d * w;
         m2 += bm2 + d * d * n * w;
         n = all;
@@ -102,13 +111,15 @@ __global__ __launch_bounds__(kThreads, 4) void group_stats_kernel(
     GroupArgs a, ItemTable chunk, int64_t each, float2* __restrict__ partial) {
     constexpr int N = Vec<T>::N, K = Whole ? 1 : N, PerUnit = Whole ? N : 1;
     __shared__ float2 unit[(Whole ? 1 : N) * 4096 / N];
-    const Lay lay(a.channels / N);
+    const Lay lay(a.channels / N / gridDim.y);
+    const int v0 = blockIdx.y * lay.nv, groups = a.groups / gridDim.y, group0 = blockIdx.y * groups;
     const Chunk c(a.items, chunk, a.batch, each, blockIdx.x);
     const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
     const int mine = ty < lay.ty ? rows_of(c.rows, ty, lay.ty) : 0;
     const int64_t step = a.x_stride * (16 / N) * lay.ty;       // bytes
     for (int v = tx; v < lay.nv && ty < lay.ty; v += lay.tx) {
-        const char* p = reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v);
+        const char* p =
+            reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v0 + v);
         float mean[K], m2[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) mean[k] = m2[k] = 0.f;
@@ -180,13 +191,11 @@ __global__ __launch_bounds__(kThreads, 4) void group_stats_kernel(
     // a group's units, K a vector, of every thread row: by `lanes` lanes
     const int per = Whole ? a.channels / a.groups / N : a.channels / a.groups;
     const int width = lay.nv * K;
-    int lanes = 64;
-    while (lanes > 1 && lanes * a.groups > kThreads) lanes >>= 1;
-    const int lane = threadIdx.x & (lanes - 1);
-    for (int g0 = 0; g0 < a.groups; g0 += kThreads / lanes) {
+    const int lanes = lanes_of(groups), lane = threadIdx.x & (lanes - 1);
+    for (int g0 = 0; g0 < groups; g0 += kThreads / lanes) {
         const int g = g0 + threadIdx.x / lanes;
-        Moments<float> m{0.f, 0.f, 0.f};
-        if (g < a.groups) {
+        Moments m{0.f, 0.f, 0.f};
+        if (g < groups) {
             for (int e = lane; e < per * lay.ty; e += lanes) {
                 const int y = e / per;
                 const int n = rows_of(c.rows, y, lay.ty);
@@ -199,13 +208,84 @@ __global__ __launch_bounds__(kThreads, 4) void group_stats_kernel(
                         m2 = __shfl_xor(m.m2, off);
             m.join(n, mean, m2);
         }
-        if (g < a.groups && lane == 0)
-            partial[(int64_t)blockIdx.x * a.groups + g] = make_float2(m.mean, m.m2);
+        if (g < groups && lane == 0)
+            partial[(int64_t)(group0 + g) * gridDim.x + blockIdx.x] = make_float2(m.mean, m.m2);
     }
 }
 
-// One wave joins the chunks of a group of an item. stat: the mean in two
-// binary32 parts (so that subtracting it from x loses nothing) and rstd.
+// Mean and variance of an item's group from the moments of its `n` chunks, in
+// binary64, by `lanes` neighbouring lanes (a power of two, 64 at most). The
+// chunks' counts are known, so the mean comes first and the deviations are about
+// it: no division a chunk. The chunks were written by other dies, so a load
+// takes a microsecond: kHeld of a lane are on their way at once.
+struct Joined {
+    double mean, var;
+};
+constexpr int kHeld = 16;
+
+__device__ __forceinline__ double over_lanes(double v, int lanes) {
+    for (int off = 1; off < lanes; off <<= 1) v += __shfl_xor(v, off);
+    return v;
+}
+
+__device__ __forceinline__ Joined join_chunks(const float2* __restrict__ p, int n, int lane,
+                                              int lanes, int64_t rows, int64_t each, int per) {
+    // (only the last chunk's count is another; its mean's excess is taken back)
+    // The quotient is made while the loads are on their way.
+    const double count = 1. / ((double)rows * per), full = (double)(each * per);
+    const float over = (float)((each * n - rows) * per);
+    float2 u[kHeld];
+    double sum[4] = {0., 0., 0., 0.};
+    float m2[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f};
+    const auto load = [&](int base) {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int c = base + k * lanes + lane;
+            u[k] = c < n ? p[c] : make_float2(0.f, 0.f);
+        }
+    };
+    const float last = n > 0 ? p[n - 1].x : 0.f;
+    for (int base = 0; base < n; base += kHeld * lanes) {
+        load(base);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            sum[k & 3] += (double)u[k].x;
+            m2[k & 3] += u[k].y;
+        }
+    }
+    Joined j{0., 0.};
+    if (n == 0) return j;
+    const double all = over_lanes((sum[0] + sum[1]) + (sum[2] + sum[3]), lanes);
+    j.mean = (full * all - (double)over * (double)last) * count;
+    // deviations of the chunks' means: the difference is taken in two parts, so
+    // binary32 holds it
+    const float hi = (float)j.mean, lo = (float)(j.mean - (double)hi);
+    for (int base = 0; base < n; base += kHeld * lanes) {
+        if (n > kHeld * lanes) load(base);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int c = base + k * lanes + lane;
+            const float d = c < n ? (u[k].x - hi) - lo : 0.f;
+            d2[k & 3] += d * d;
+        }
+    }
+    const double dl = (double)((last - hi) - lo);
+    const double within = over_lanes((double)((m2[0] + m2[1]) + (m2[2] + m2[3])), lanes);
+    const double between = over_lanes((double)((d2[0] + d2[1]) + (d2[2] + d2[3])), lanes);
+    j.var = (within + full * between - (double)over * (dl * dl)) * count;
+    if (j.var < 0.) j.var = 0.;
+    return j;
+}
+
+// The mean in two binary32 parts (so that subtracting it from x loses nothing)
+// and rstd.
+__device__ __forceinline__ float4 stat_of(const Joined& j, float eps) {
+    const float hi = (float)j.mean;
+    return make_float4(hi, (float)(j.mean - (double)hi),
+                       1.f / sqrtf((float)(j.var + (double)eps)), 0.f);
+}
+
+// A wave joins the chunks of a group of an item.
 __global__ __launch_bounds__(kThreads) void group_join_kernel(GroupArgs a, ItemTable chunk,
                                                               int64_t each,
                                                               const float2* __restrict__ partial,
@@ -213,60 +293,106 @@ __global__ __launch_bounds__(kThreads) void group_join_kernel(GroupArgs a, ItemT
     const int64_t at = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
     if (at >= (int64_t)a.batch * a.groups) return;
     const int b = (int)(at / a.groups), g = (int)(at % a.groups), lane = threadIdx.x & 63;
-    const int first = chunk.start[b], last = chunk.start[b + 1];
-    const int64_t rows = a.items.start[b + 1] - a.items.start[b];
-    const int per = a.channels / a.groups;
-    Moments<double> m{0., 0., 0.};
-    for (int c = first + lane; c < last; c += 64) {
-        const float2 u = partial[(int64_t)c * a.groups + g];
-        const int64_t left = rows - (int64_t)(c - first) * each;
-        m.join((double)((left < each ? left : each) * per), u.x, u.y);
-    }
-    for (int off = 1; off < 64; off <<= 1) {
-        const double n = __shfl_xor(m.n, off), mean = __shfl_xor(m.mean, off),
-                     m2 = __shfl_xor(m.m2, off);
-        m.join(n, mean, m2);
-    }
+    const int first = chunk.start[b];
+    const Joined j = join_chunks(partial + (int64_t)g * chunk.start[a.batch] + first,
+                                 chunk.start[b + 1] - first, lane, 64,
+                                 a.items.start[b + 1] - a.items.start[b], each,
+                                 a.channels / a.groups);
     if (lane) return;
-    const double var = m.n > 0. ? m.m2 / m.n : 0.;
-    const float rstd = (float)(1. / sqrt(var + (double)a.eps));
-    const float hi = (float)m.mean;
-    stat[at] = make_float4(hi, (float)(m.mean - (double)hi), rstd, 0.f);
-    if (a.mean) a.mean[at] = hi;
-    if (a.rstd) a.rstd[at] = rstd;
+    const float4 s = stat_of(j, a.eps);
+    stat[at] = s;
+    if (a.mean) a.mean[at] = s.x;
+    if (a.rstd) a.rstd[at] = s.z;
+}
+
+// The same by a workgroup for `groups` groups of item b from group0 on, into LDS;
+// `write` as well into mean and rstd.
+__device__ __forceinline__ void join_here(const GroupArgs& a, const ItemTable& chunk, int64_t each,
+                                          const float2* __restrict__ partial, int b, int group0,
+                                          int groups, bool write, float4* __restrict__ stat) {
+    const int lanes = lanes_of(groups), lane = threadIdx.x & (lanes - 1);
+    const int first = chunk.start[b], n = chunk.start[b + 1] - first;
+    for (int g0 = 0; g0 < groups; g0 += kThreads / lanes) {
+        const int g = g0 + threadIdx.x / lanes;
+        const bool on = g < groups;
+        const Joined j = join_chunks(
+            partial + (int64_t)(group0 + (on ? g : 0)) * chunk.start[a.batch] + first, n, lane, lanes, a.items.start[b + 1] - a.items.start[b], each,
+                                     a.channels / a.groups);
+        if (on && lane == 0) {
+            const float4 s = stat_of(j, a.eps);
+            stat[g] = s;
+            if (write && a.mean) a.mean[(int64_t)b * a.groups + group0 + g] = s.x;
+            if (write && a.rstd) a.rstd[(int64_t)b * a.groups + group0 + g] = s.z;
+        }
+    }
+    __syncthreads();
 }
 
 // ------------------------------------------------------------------ apply ---
+template <bool Past>
+__device__ __forceinline__ uint4 load16(const char* p) {
+    if constexpr (Past)
+        return __builtin_bit_cast(uint4,
+                                  __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p)));
+    else
+        return *reinterpret_cast<const uint4*>(p);
+}
+
 // out = act((x - hi) k + o) with k = rstd w and o = b - lo k. The chunks run
-// last to first: what the statistics read last is still in the caches.
-template <typename T, int Act, bool Whole>
+// last to first: what the statistics read last is still in the caches. `Past`:
+// a map larger than those is loaded past them here, so that what was just read
+// does not drive out what was read before and is wanted next (269 us for 310
+// where x has 537 MB; 168 for 163 with the gradient where it has 102 MB).
+// `Here`: the workgroup joins its item's chunks itself.
+template <typename T, int Act, bool Whole, bool Past, bool Here>
 __global__ __launch_bounds__(kThreads, 4) void group_apply_kernel(
-    GroupArgs a, ItemTable chunk, int64_t each, const float4* __restrict__ stat) {
+    GroupArgs a, ItemTable chunk, int64_t each, const float2* __restrict__ partial,
+    const float4* __restrict__ stats) {
     constexpr int N = Vec<T>::N, K = Whole ? 1 : N, U = 4;
-    const Lay lay(a.channels / N);
-    const Chunk c(a.items, chunk, a.batch, each, gridDim.x - 1 - blockIdx.x);
+    extern __shared__ float4 joined[];              // Here: [groups]
+    const Lay lay(a.channels / N / gridDim.y);
+    const int v0 = blockIdx.y * lay.nv, groups = a.groups / gridDim.y, group0 = blockIdx.y * groups;
+    const int at = gridDim.x - 1 - blockIdx.x;
+    const Chunk c(a.items, chunk, a.batch, each, at);
     const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
-    if (ty >= lay.ty) return;
-    const int mine = rows_of(c.rows, ty, lay.ty);
+    const int mine = ty < lay.ty ? rows_of(c.rows, ty, lay.ty) : 0;
     const int64_t step = a.x_stride * (16 / N) * lay.ty, ostep = a.out_stride * (16 / N) * lay.ty;
     const int per = a.channels / a.groups;
+    // The first rows are on their way before the statistics are there.
+    uint4 q[U];
+    const auto load = [&](const char* p, int rows) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (i < rows) q[i] = load16<Past>(p + i * step);
+    };
+    const char* x0 = reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v0);
+    char* o0 = const_cast<char*>(
+        reinterpret_cast<const char*>(vectors<T>(a.out, c.row0 + ty, a.out_stride) + v0));
+    load(x0 + tx * 16, mine);
+    const float4* stat = joined;
+    if constexpr (Here)
+        join_here(a, chunk, each, partial, c.item, group0, groups, at == chunk.start[c.item],
+                  joined);
+    else
+        stat = stats + (int64_t)c.item * a.groups + group0;
+    if (mine == 0) return;
     for (int v = tx; v < lay.nv; v += lay.tx) {
-        const char* p = reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v);
-        char* o = const_cast<char*>(
-            reinterpret_cast<const char*>(vectors<T>(a.out, c.row0 + ty, a.out_stride) + v));
+        const char* p = x0 + v * 16;
+        char* o = o0 + v * 16;
+        if (v != tx) load(p, mine);
         float hi[K], by[N], off[N];
-        param<T>(a.weight, v, 1.f, by);
-        param<T>(a.bias, v, 0.f, off);
+        param<T>(a.weight, v0 + v, 1.f, by);
+        param<T>(a.bias, v0 + v, 0.f, off);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const float4 s = stat[(int64_t)c.item * a.groups + (v * N + (Whole ? 0 : e)) / per];
+            const float4 s = stat[(v * N + (Whole ? 0 : e)) / per];
             hi[Whole ? 0 : e] = s.x;
             by[e] *= s.z;
             off[e] -= s.y * by[e];
         }
-        const auto one = [&](uint4 q) {
+        const auto one = [&](uint4 x) {
             float f[N];
-            Vec<T>::widen(q, f);
+            Vec<T>::widen(x, f);
 #pragma unroll
             for (int e = 0; e < N; ++e)
                 f[e] = activate<Act>((f[e] - hi[Whole ? 0 : e]) * by[e] + off[e]);
@@ -274,16 +400,15 @@ __global__ __launch_bounds__(kThreads, 4) void group_apply_kernel(
         };
         int r = 0;
         for (; r + U <= mine; r += U) {
-            uint4 q[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i) q[i] = *reinterpret_cast<const uint4*>(p + i * step);
 #pragma unroll
             for (int i = 0; i < U; ++i) store_nt16(o + i * ostep, one(q[i]));
             p += U * step;
             o += U * ostep;
+            load(p, mine - r - U);
         }
-        for (; r < mine; ++r, p += step, o += ostep)
-            store_nt16(o, one(*reinterpret_cast<const uint4*>(p)));
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (r + i < mine) store_nt16(o + i * ostep, one(q[i]));
     }
 }
 
@@ -320,18 +445,20 @@ __global__ __launch_bounds__(kThreads, 4) void group_sums_kernel(GroupArgs a, It
                                                                  float* __restrict__ partial) {
     constexpr int N = Vec<T>::N, U = 4;
     __shared__ float sums[2 * kThreads * N];
-    const Lay lay(a.channels / N);
+    const Lay lay(a.channels / N / gridDim.y);
+    const int v0 = blockIdx.y * lay.nv, width = lay.nv * N;
     const Chunk c(a.items, chunk, a.batch, each, blockIdx.x);
     const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
     const int mine = ty < lay.ty ? rows_of(c.rows, ty, lay.ty) : 0;
     const int64_t step = a.x_stride * (16 / N) * lay.ty, dstep = a.dout_stride * (16 / N) * lay.ty;
-    float* to = partial + (int64_t)blockIdx.x * 2 * a.channels;
+    float* to = partial + (int64_t)blockIdx.x * 2 * a.channels + v0 * N;
     for (int v = tx; v < lay.nv && ty < lay.ty; v += lay.tx) {
-        const char* p = reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v);
+        const char* p =
+            reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v0 + v);
         const char* d = reinterpret_cast<const char*>(
-            vectors<T>(a.dout, c.row0 + ty, a.dout_stride) + v);
+            vectors<T>(a.dout, c.row0 + ty, a.dout_stride) + v0 + v);
         Channels<T, Whole> ch;
-        ch.load(a, c.item, v);
+        ch.load(a, c.item, v0 + v);
         float s1[N], s2[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) s1[e] = s2[e] = 0.f;
@@ -372,19 +499,19 @@ __global__ __launch_bounds__(kThreads, 4) void group_sums_kernel(GroupArgs a, It
             // (then tx covers the row: one vector a thread)
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                sums[ty * a.channels + v * N + e] = s1[e];
-                sums[kThreads * N + ty * a.channels + v * N + e] = s2[e];
+                sums[ty * width + v * N + e] = s1[e];
+                sums[kThreads * N + ty * width + v * N + e] = s2[e];
             }
         }
     }
     if (lay.ty == 1) return;
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.channels; i += kThreads) {
-        const int half = i >= a.channels, col = i - half * a.channels;
+    for (int i = threadIdx.x; i < 2 * width; i += kThreads) {
+        const int half = i >= width, col = i - half * width;
         const float* from = sums + half * kThreads * N + col;
         float s = 0.f;
-        for (int y = 0; y < lay.ty; ++y) s += from[y * a.channels];
-        to[i] = s;
+        for (int y = 0; y < lay.ty; ++y) s += from[y * width];
+        to[half * a.channels + col] = s;
     }
 }
 
@@ -421,6 +548,7 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
     constexpr int N = Vec<T>::N, U = 4;
     extern __shared__ float2 avg[];         // [groups]: A and B of the item, with -1 / count
     if ((int)blockIdx.x >= chunks) {
+        if (blockIdx.y) return;
         const int col = ((int)blockIdx.x - chunks) * kThreads + threadIdx.x;
         if (col >= a.channels) return;
         double s1 = 0., s2 = 0.;
@@ -433,22 +561,21 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
         if (a.dweight) a.dweight[col] = (float)s2;
         return;
     }
-    const Lay lay(a.channels / N);
+    const Lay lay(a.channels / N / gridDim.y);
+    const int v0 = blockIdx.y * lay.nv, groups = a.groups / gridDim.y;
     const Chunk c(a.items, chunk, a.batch, each, chunks - 1 - (int)blockIdx.x);
     const int per = a.channels / a.groups;
     {
         const float* t = total + (int64_t)c.item * 2 * a.channels;
         const int64_t count = (int64_t)(a.items.start[c.item + 1] - a.items.start[c.item]) * per;
         const float by = (float)(-1. / (double)count);
-        int lanes = 64;
-        while (lanes > 1 && lanes * a.groups > kThreads) lanes >>= 1;
-        const int lane = threadIdx.x & (lanes - 1);
-        for (int g0 = 0; g0 < a.groups; g0 += kThreads / lanes) {
+        const int lanes = lanes_of(groups), lane = threadIdx.x & (lanes - 1);
+        for (int g0 = 0; g0 < groups; g0 += kThreads / lanes) {
             const int g = g0 + threadIdx.x / lanes;
             float s1 = 0.f, s2 = 0.f;
-            if (g < a.groups) {
+            if (g < groups) {
                 for (int e = lane; e < per; e += lanes) {
-                    const int col = g * per + e;
+                    const int col = v0 * N + g * per + e;
                     float w = 1.f;
                     if (a.weight) {
                         if constexpr (N == 4) w = reinterpret_cast<const float*>(a.weight)[col];
@@ -463,7 +590,7 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
                 s1 += __shfl_xor(s1, off);
                 s2 += __shfl_xor(s2, off);
             }
-            if (g < a.groups && lane == 0) avg[g] = make_float2(s1 * by, s2 * by);
+            if (g < groups && lane == 0) avg[g] = make_float2(s1 * by, s2 * by);
         }
     }
     __syncthreads();
@@ -473,13 +600,14 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
     const int64_t step = a.x_stride * (16 / N) * lay.ty, dstep = a.dout_stride * (16 / N) * lay.ty,
                   ostep = a.out_stride * (16 / N) * lay.ty;
     for (int v = tx; v < lay.nv; v += lay.tx) {
-        const char* p = reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v);
+        const char* p =
+            reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v0 + v);
         const char* d = reinterpret_cast<const char*>(
-            vectors<T>(a.dout, c.row0 + ty, a.dout_stride) + v);
+            vectors<T>(a.dout, c.row0 + ty, a.dout_stride) + v0 + v);
         char* o = const_cast<char*>(
-            reinterpret_cast<const char*>(vectors<T>(a.dx, c.row0 + ty, a.out_stride) + v));
+            reinterpret_cast<const char*>(vectors<T>(a.dx, c.row0 + ty, a.out_stride) + v0 + v));
         Channels<T, Whole> ch;
-        ch.load(a, c.item, v);
+        ch.load(a, c.item, v0 + v);
         constexpr int K = Channels<T, Whole>::K;
         float2 m[K];
 #pragma unroll
@@ -518,23 +646,53 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
 }
 
 // ----------------------------------------------------------------- launch ---
+// Whether the apply kernel's workgroups join their item's chunks themselves: what
+// they read for it, all together, against a launch of 4 us (a map of 4096 rows
+// in 256 chunks of 32 groups: 16 MB).
+bool join_in_apply(const GroupArgs& a, const GroupPlan& p) {
+    int64_t pairs = 0;
+    for (int b = 0; b < a.batch; ++b) {
+        const int64_t n = p.chunk.start[b + 1] - p.chunk.start[b];
+        if (n == 0) return false;                   // (nothing would write its mean and rstd)
+        pairs += n * n;
+    }
+    return pairs * a.groups * (int64_t)sizeof(float2) <= (int64_t(16) << 20);
+}
+
+// x of more bytes than this is loaded past the caches in its second pass.
+constexpr int64_t kPast = int64_t(200) << 20;
+
 template <typename T, bool Whole>
 hipError_t forward_of(const GroupArgs& a, const GroupPlan& p, float2* partial, float4* stat,
                       hipStream_t s) {
     const int chunks = p.chunk.start[a.batch];
     if (chunks) {
-        group_stats_kernel<T, Whole><<<chunks, kThreads, 0, s>>>(a, p.chunk, p.rows, partial);
+        group_stats_kernel<T, Whole><<<dim3(chunks, p.slices), kThreads, 0, s>>>(a, p.chunk, p.rows, partial);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const int64_t waves = (int64_t)a.batch * a.groups;
-    group_join_kernel<<<(unsigned)((waves + 3) / 4), kThreads, 0, s>>>(a, p.chunk, p.rows, partial,
-                                                                       stat);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !chunks) return e;
+    const bool here = join_in_apply(a, p);
+    if (!here) {
+        const int64_t waves = (int64_t)a.batch * a.groups;
+        group_join_kernel<<<(unsigned)((waves + 3) / 4), kThreads, 0, s>>>(a, p.chunk, p.rows,
+                                                                           partial, stat);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || !chunks) return e;
+    }
+    const bool past = (int64_t)a.items.start[a.batch] * a.channels * (16 / Vec<T>::N) > kPast;
     const auto apply = [&](auto act) {
-        group_apply_kernel<T, decltype(act)::value, Whole>
-            <<<chunks, kThreads, 0, s>>>(a, p.chunk, p.rows, stat);
+        constexpr int A = decltype(act)::value;
+        const size_t lds = here ? a.groups / p.slices * sizeof(float4) : 0;
+        const dim3 grid(chunks, p.slices);
+        if (here)
+            group_apply_kernel<T, A, Whole, false, true>
+                <<<grid, kThreads, lds, s>>>(a, p.chunk, p.rows, partial, stat);
+        else if (past)
+            group_apply_kernel<T, A, Whole, true, false>
+                <<<grid, kThreads, 0, s>>>(a, p.chunk, p.rows, partial, stat);
+        else
+            group_apply_kernel<T, A, Whole, false, false>
+                <<<grid, kThreads, 0, s>>>(a, p.chunk, p.rows, partial, stat);
     };
     if (a.act == P3D_ACT_SILU) apply(std::integral_constant<int, P3D_ACT_SILU>());
     else if (a.act == P3D_ACT_GELU) apply(std::integral_constant<int, P3D_ACT_GELU>());
@@ -547,7 +705,8 @@ hipError_t backward_act(const GroupArgs& a, const GroupPlan& p, float* partial, 
                         hipStream_t s) {
     const int chunks = p.chunk.start[a.batch];
     if (chunks) {
-        group_sums_kernel<T, Act, Whole><<<chunks, kThreads, 0, s>>>(a, p.chunk, p.rows, partial);
+        group_sums_kernel<T, Act, Whole>
+            <<<dim3(chunks, p.slices), kThreads, 0, s>>>(a, p.chunk, p.rows, partial);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -558,8 +717,9 @@ hipError_t backward_act(const GroupArgs& a, const GroupPlan& p, float* partial, 
     if (e != hipSuccess) return e;
     const int more = a.dweight || a.dbias ? (a.channels + kThreads - 1) / kThreads : 0;
     if (chunks + more == 0) return hipSuccess;
-    group_dx_kernel<T, Act, Whole><<<chunks + more, kThreads, a.groups * sizeof(float2), s>>>(
-        a, p.chunk, p.rows, chunks, total);
+    group_dx_kernel<T, Act, Whole>
+        <<<dim3(chunks + more, p.slices), kThreads, a.groups / p.slices * sizeof(float2), s>>>(
+            a, p.chunk, p.rows, chunks, total);
     return hipGetLastError();
 }
 
@@ -577,12 +737,22 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// Chunks for at most 4 workgroups a CU, all of them running at once, of at
-// least 4 rows a thread.
+// Chunks of at least 4 rows a thread, for at most 4 workgroups a CU, all of them
+// running at once. A map that does not fill those is cut into slices of whole
+// groups, the narrowest of whole cache lines (8 vectors), so that it has fewer
+// chunks to join: 11 + 5 us for 8 + 5 where 4096 rows have 512 channels. A larger
+// map is read in whole rows (265 us for 335 where 262,144 rows have 1024).
 GroupPlan group_norm_plan(const GroupArgs& a, p3d_dtype dt) {
     GroupPlan p;
-    const Lay lay(a.channels / (dt == P3D_BF16 ? 8 : 4));
-    const int64_t n = a.items.start[a.batch], most = 4 * kComputeUnits;
+    const int unit = dt == P3D_BF16 ? 8 : 4;
+    const int64_t most = 4 * kComputeUnits;
+    p.slices = 1;
+    if (a.items.start[a.batch] < most * 4 * Lay(a.channels / unit).ty)
+        for (int d = 2; d <= a.groups; ++d)
+            if (a.groups % d == 0 && a.channels / d % unit == 0 && a.channels / d / unit >= 8)
+                p.slices = d;
+    const Lay lay(a.channels / unit / p.slices);
+    const int64_t n = a.items.start[a.batch] * (int64_t)p.slices;
     p.rows = std::max<int64_t>((n + most - 1) / most, 4 * lay.ty);
     p.rows = (p.rows + lay.ty - 1) / lay.ty * lay.ty;
     int32_t at = 0;

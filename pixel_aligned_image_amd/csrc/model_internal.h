@@ -59,9 +59,11 @@ struct GroupArgs {
     ItemTable items;
 };
 
-// How a call's rows are cut: chunk.start[b] .. chunk.start[b + 1] are item b's
-// chunks, `rows` rows each but for an item's last.
+// How a call is cut: its channels into `slices`, its rows into chunks.
+// chunk.start[b] .. chunk.start[b + 1] are item b's, `rows` rows each but for an
+// item's last.
 struct GroupPlan {
+    int32_t slices;
     int64_t rows;
     ItemTable chunk;
     size_t bytes;                   // of the workspace

@@ -75,38 +75,48 @@ def bind(core):
 
 
 # ----------------------------------------------------------------- helpers ---
-def _here(t, name):
-    """Refuses a tensor of another device than the one the call runs on."""
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s must be on torch's current device (%d), got %s"
-                         % (name, torch.cuda.current_device(), t.device))
+# The smallest calls last a few microseconds, as long as the checks of ten
+# tensors: one condition passes what is right, _refuse words what is not.
+def _device():
+    """The device that a call runs on (of no tensor, before there is one)."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
 
-def _rows(t, name, dtype, shape=None):
-    """(pointer, row stride) of a [n, width] device tensor whose rows may be
-    strided."""
+def _refuse(t, name, dtype, dev, wanted):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be on the GPU, got %s" % (name, t.device))
-    _here(t, name)
-    if t.dtype is not dtype:
+    if t.get_device() != dev:
+        raise ValueError("%s must be on torch's current device (%d), got %s"
+                         % (name, dev, t.device))
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError("%s must be %s, got %s" % (
-            name, "[n, width]" if shape is None else list(shape), tuple(t.shape)))
-    n, width = t.shape
-    s = t.stride()
-    if width > 1 and s[1] != 1:
-        raise ValueError("%s must have contiguous rows, got strides %s" % (name, s))
-    return t.data_ptr(), (s[0] if n > 1 else width)
+    raise ValueError("%s must be %s, got %s, strides %s"
+                     % (name, wanted, tuple(t.shape), t.stride()))
 
 
-def _ptr(t, name, dtype, shape):
-    p = block._ptr(t, name, dtype, shape)
-    if t is not None:
-        _here(t, name)
-    return p
+def _rows(t, name, dtype, dev, shape=None):
+    """(pointer, row stride) of a [n, width] device tensor whose rows may be
+    strided."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.dim() == 2 and (shape is None or t.shape == shape)):
+        n, width = t.shape
+        step, one = t.stride()
+        if one == 1 or width <= 1:
+            return t.data_ptr(), (step if n > 1 else width)
+    _refuse(t, name, dtype, dev, "%s with contiguous rows" % (
+        "[n, width]" if shape is None else list(shape)))
+
+
+def _ptr(t, name, dtype, dev, shape):
+    """Pointer of an optional contiguous tensor."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, dev, "%s and contiguous" % (list(shape),))
 
 
 def _choice(table, name, value):
@@ -116,21 +126,22 @@ def _choice(table, name, value):
 
 
 # -------------------------------------------------------------- group norm ---
-def _group(x, groups, offsets, weight, bias, act, eps):
+def _group(x, groups, offsets, weight, bias, act, eps, dev):
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be [n, channels], got %s" % (tuple(getattr(x, "shape", ())),))
     n, c = x.shape
     off = block.make_offsets((0, n) if offsets is None else offsets)
+    dt = x.dtype
     d = p3d_group_desc(n, ctypes.addressof(off), len(off) - 1, c, int(groups),
                        block._dtype(x, "x"), _choice(ACT, "act", act), eps,
-                       _ptr(weight, "weight", x.dtype, (c,)), _ptr(bias, "bias", x.dtype, (c,)))
+                       _ptr(weight, "weight", dt, dev, (c,)), _ptr(bias, "bias", dt, dev, (c,)))
     return d, off
 
 
 def p3d_group_norm_workspace_size(x, groups, offsets=None):
     """Bytes of device workspace p3d_group_norm and p3d_group_norm_backward
     need for rows like x's."""
-    d, off = _group(x, groups, offsets, None, None, "none", 1e-5)
+    d, off = _group(x, groups, offsets, None, None, "none", 1e-5, None)
     return block._sized(lib.p3d_group_norm_workspace_size(d))
 
 
@@ -143,14 +154,15 @@ def p3d_group_norm(x, out, groups, offsets=None, weight=None, bias=None, act="no
     x); weight, bias: [channels]; act: "none", "silu" or "gelu"; mean, rstd:
     float32 [batch, groups], written unless None (the gradient needs them);
     offsets: the items' rows (None: one item)."""
-    d, off = _group(x, groups, offsets, weight, bias, act, eps)
-    xp, xs = _rows(x, "x", x.dtype)
-    op, os = _rows(out, "out", x.dtype, x.shape)
+    dev, f = _device(), torch.float32
+    d, off = _group(x, groups, offsets, weight, bias, act, eps, dev)
+    xp, xs = _rows(x, "x", x.dtype, dev)
+    op, os = _rows(out, "out", x.dtype, dev, x.shape)
     stats = (d.batch, d.groups)
     keep, ws, nbytes = block._work(workspace, lambda: lib.p3d_group_norm_workspace_size(d),
                                    x.device, stream)
-    _core._check(lib.p3d_group_norm(d, xp, xs, op, os, _ptr(mean, "mean", torch.float32, stats),
-                                    _ptr(rstd, "rstd", torch.float32, stats), ws, nbytes,
+    _core._check(lib.p3d_group_norm(d, xp, xs, op, os, _ptr(mean, "mean", f, dev, stats),
+                                    _ptr(rstd, "rstd", f, dev, stats), ws, nbytes,
                                     block._stream(stream)))
 
 
@@ -160,17 +172,18 @@ def p3d_group_norm_backward(dout, x, mean, rstd, dx, groups, offsets=None, weigh
     """Enqueue p3d_group_norm_backward: dx (which may be dout or x) from dout,
     the forward call's x and the mean and rstd it wrote; float32 dweight and
     dbias [channels], each None where it is not wanted."""
-    d, off = _group(x, groups, offsets, weight, bias, act, 1e-5)
-    xp, xs = _rows(x, "x", x.dtype)
-    dp, ds = _rows(dout, "dout", x.dtype, x.shape)
-    op, os = _rows(dx, "dx", x.dtype, x.shape)
-    f, stats, cols = torch.float32, (d.batch, d.groups), (d.channels,)
+    dev, dt, f = _device(), x.dtype, torch.float32
+    d, off = _group(x, groups, offsets, weight, bias, act, 1e-5, dev)
+    xp, xs = _rows(x, "x", dt, dev)
+    dp, ds = _rows(dout, "dout", dt, dev, x.shape)
+    op, os = _rows(dx, "dx", dt, dev, x.shape)
+    stats, cols = (d.batch, d.groups), (d.channels,)
     keep, ws, nbytes = block._work(workspace, lambda: lib.p3d_group_norm_workspace_size(d),
                                    x.device, stream)
     _core._check(lib.p3d_group_norm_backward(
-        d, dp, ds, xp, xs, _ptr(mean, "mean", f, stats), _ptr(rstd, "rstd", f, stats), op, os,
-        _ptr(dweight, "dweight", f, cols), _ptr(dbias, "dbias", f, cols), ws, nbytes,
-        block._stream(stream)))
+        d, dp, ds, xp, xs, _ptr(mean, "mean", f, dev, stats), _ptr(rstd, "rstd", f, dev, stats),
+        op, os, _ptr(dweight, "dweight", f, dev, cols), _ptr(dbias, "dbias", f, dev, cols), ws,
+        nbytes, block._stream(stream)))
 
 
 # ------------------------------------------------------------------ linear ---
@@ -179,11 +192,12 @@ def p3d_quantize_rows(x, q, scale, stream=None):
     """Enqueue p3d_quantize_rows: q (int8, like x) and scale (float32 [n]) of
     the rows of x [n, width], float32 or bfloat16 (rows may be strided):
     tokens, or a weight [out, in]."""
-    xp, xs = _rows(x, "x", x.dtype)
-    qp, qs = _rows(q, "q", torch.int8, x.shape)
+    dev = _device()
+    xp, xs = _rows(x, "x", x.dtype, dev)
+    qp, qs = _rows(q, "q", torch.int8, dev, x.shape)
     n, width = x.shape
     _core._check(lib.p3d_quantize_rows(xp, block._dtype(x, "x"), n, width, xs, qp, qs,
-                                       _ptr(scale, "scale", torch.float32, (n,)),
+                                       _ptr(scale, "scale", torch.float32, dev, (n,)),
                                        block._stream(stream)))
 
 
@@ -195,20 +209,21 @@ def p3d_linear_i8(q, scale, weight, weight_scale, out, bias=None, act="none", re
     p3d_quantize_rows; weight: int8 [out, in]; weight_scale: float32 [out];
     out, residual: [n, out] and bias: [out], float32 or bfloat16 (residual may
     be out)."""
-    qp, qs = _rows(q, "q", torch.int8)
+    dev, dt, f = _device(), out.dtype, torch.float32
+    qp, qs = _rows(q, "q", torch.int8, dev)
     n, k = q.shape
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [out, in], got %s"
                          % (tuple(getattr(weight, "shape", ())),))
     m = weight.shape[0]
-    op, os = _rows(out, "out", out.dtype, (n, m))
-    rp, rs = (None, 0) if residual is None else _rows(residual, "residual", out.dtype, (n, m))
+    op, os = _rows(out, "out", dt, dev, (n, m))
+    rp, rs = (None, 0) if residual is None else _rows(residual, "residual", dt, dev, (n, m))
     d = p3d_linear_i8_desc(n, k, m, block._dtype(out, "out"), _choice(ACT, "act", act),
-                           _ptr(weight, "weight", torch.int8, (m, k)),
-                           _ptr(weight_scale, "weight_scale", torch.float32, (m,)),
-                           _ptr(bias, "bias", out.dtype, (m,)))
-    _core._check(lib.p3d_linear_i8(d, qp, qs, _ptr(scale, "scale", torch.float32, (n,)), rp, rs,
-                                   op, os, block._stream(stream)))
+                           _ptr(weight, "weight", torch.int8, dev, (m, k)),
+                           _ptr(weight_scale, "weight_scale", f, dev, (m,)),
+                           _ptr(bias, "bias", dt, dev, (m,)))
+    _core._check(lib.p3d_linear_i8(d, qp, qs, _ptr(scale, "scale", f, dev, (n,)), rp, rs, op, os,
+                                   block._stream(stream)))
 
 
 # ------------------------------------------------------------------- adamw ---
@@ -216,19 +231,14 @@ class AdamWTensors(tuple):
     """The tensors of p3d_adamw and their table (make_adamw_tensors)."""
 
 
-def _flat(t, name, dtype, size):
-    """Pointer of a contiguous device tensor of `size` elements."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be on the GPU, got %s" % (name, t.device))
-    _here(t, name)
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.numel() != size or not t.is_contiguous():
-        raise ValueError("%s must have %d contiguous elements, got %s, strides %s"
-                         % (name, size, tuple(t.shape), t.stride()))
-    return t.data_ptr() if size else None
+def _flat(t, name, dtype, dev, size):
+    """Pointer of a contiguous device tensor of `size` elements, of a type or
+    one of several."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.numel() == size
+            and (t.dtype is dtype or isinstance(dtype, tuple) and t.dtype in dtype)
+            and t.is_contiguous()):
+        return t.data_ptr() if size else None
+    _refuse(t, name, dtype, dev, "%d contiguous elements" % size)
 
 
 def make_adamw_tensors(params, grads, m, v, masters=None, m_scales=None, v_scales=None,
@@ -262,36 +272,37 @@ def make_adamw_tensors(params, grads, m, v, masters=None, m_scales=None, v_scale
     bits = 32 if m_scales is None else 8
     st = torch.float32 if bits == 32 else (torch.float8_e4m3fn, torch.uint8)
     f = torch.float32
-    rows = (p3d_adamw_tensor * max(1, n))()
+    rows, dev = (p3d_adamw_tensor * max(1, n))(), _device()
     for j in range(n):
         size, to = params[j].numel(), rows[j]
         blocks = (size + 255) // 256
-        to.param = _flat(params[j], "params[%d]" % j, pt, size)
-        to.grad = _flat(grads[j], "grads[%d]" % j, gt, size)
-        to.m = _flat(m[j], "m[%d]" % j, st, size)
-        to.v = _flat(v[j], "v[%d]" % j, st, size)
+        to.param = _flat(params[j], "params[%d]" % j, pt, dev, size)
+        to.grad = _flat(grads[j], "grads[%d]" % j, gt, dev, size)
+        to.m = _flat(m[j], "m[%d]" % j, st, dev, size)
+        to.v = _flat(v[j], "v[%d]" % j, st, dev, size)
         if masters is not None:
-            to.master = _flat(masters[j], "masters[%d]" % j, f, size)
+            to.master = _flat(masters[j], "masters[%d]" % j, f, dev, size)
         if bits == 8:
-            to.m_scale = _flat(m_scales[j], "m_scales[%d]" % j, f, blocks)
-            to.v_scale = _flat(v_scales[j], "v_scales[%d]" % j, f, blocks)
+            to.m_scale = _flat(m_scales[j], "m_scales[%d]" % j, f, dev, blocks)
+            to.v_scale = _flat(v_scales[j], "v_scales[%d]" % j, f, dev, blocks)
         to.size, to.weight_decay = size, decay[j]
     table = AdamWTensors(params + grads + m + v + (masters or []) + (m_scales or [])
                          + (v_scales or []))
     table.rows, table.count, table.bits = rows, n, bits
     table.param_dtype, table.grad_dtype = _core._DT[pt], _core._DT[gt]
-    table.device = params[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    table.index = dev
     return table
 
 
 def _adamw(tensors):
     if not isinstance(tensors, AdamWTensors):
         raise TypeError("tensors must be a table of make_adamw_tensors")
-    if tensors.device.index != torch.cuda.current_device():
-        raise ValueError("tensors must be on torch's current device (%d), got %s"
-                         % (torch.cuda.current_device(), tensors.device))
-    return p3d_adamw_desc(tensors.count, ctypes.addressof(tensors.rows), tensors.param_dtype,
-                          tensors.grad_dtype, tensors.bits)
+    dev = _device()
+    if tensors.index != dev:
+        raise ValueError("tensors must be on torch's current device (%d), got %d"
+                         % (dev, tensors.index))
+    return dev, p3d_adamw_desc(tensors.count, ctypes.addressof(tensors.rows),
+                               tensors.param_dtype, tensors.grad_dtype, tensors.bits)
 
 
 @_lends
@@ -303,20 +314,20 @@ def p3d_adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0, gra
     8-bit states are rounded by, another for every step; device_lr, device_step:
     float32 / int32 device tensors of one element that are read instead of lr
     and step when the work runs, or None."""
-    d = _adamw(tensors)
+    dev, d = _adamw(tensors)
     d.lr, d.beta1, d.beta2, d.eps, d.step = lr, beta1, beta2, eps, step
     d.seed = seed & 0xffffffffffffffff
     f = torch.float32
     for name, t, dt in (("grad_scale", grad_scale, f), ("device_lr", device_lr, f),
                         ("device_step", device_step, torch.int32)):
         if t is not None:
-            setattr(d, name, _flat(t, name, dt, 1))
+            setattr(d, name, _flat(t, name, dt, dev, 1))
     _core._check(lib.p3d_adamw(d, block._stream(stream)))
 
 
 def p3d_grad_norm_workspace_size(tensors):
     """Bytes of device workspace p3d_grad_norm needs."""
-    return block._sized(lib.p3d_grad_norm_workspace_size(_adamw(tensors)))
+    return block._sized(lib.p3d_grad_norm_workspace_size(_adamw(tensors)[1]))
 
 
 @_lends
@@ -324,8 +335,8 @@ def p3d_grad_norm(tensors, out, max_norm=float("inf"), workspace=None, stream=No
     """Enqueue p3d_grad_norm: out (float32 [2]) = the norm over the table's
     gradients, and the factor that brings it to max_norm where it is above (NaN
     where it is not finite)."""
-    d = _adamw(tensors)
+    dev, d = _adamw(tensors)
     keep, ws, nbytes = block._work(workspace, lambda: lib.p3d_grad_norm_workspace_size(d),
-                                   tensors.device, stream)
-    _core._check(lib.p3d_grad_norm(d, max_norm, _ptr(out, "out", torch.float32, (2,)), ws, nbytes,
-                                   block._stream(stream)))
+                                   torch.device("cuda", dev), stream)
+    _core._check(lib.p3d_grad_norm(d, max_norm, _ptr(out, "out", torch.float32, dev, (2,)), ws,
+                                   nbytes, block._stream(stream)))
