@@ -3,10 +3,12 @@
 //   s = max |x| / 127,  q = x / s to the nearest integer, ties to even
 //
 // A row is read once: it stays in registers between its maximum and its
-// quotients. Memory bound (3 bytes a bf16 element), so the quotient must stay
-// cheap and exact: x (1 / s) to the nearest integer is off by one at most
-// near the middle between two integers, and the remainder x - q s, which one
-// fused operation gives without rounding, says so.
+// quotients. Memory bound (3 bytes a bf16 element) only if an element costs
+// fewer than 20 operations, so the quotient has to be cheap and exact. x (1 / s)
+// is off by two roundings of 127 at most: where it is further than that from the
+// middle between two integers, the nearest to it is the nearest to x / s. A wave
+// with an element nearer to a middle (8 % of rows of 2048) takes the remainder
+// x - q s, which one fused operation gives without rounding.
 #include <algorithm>
 
 #include "model_internal.h"
@@ -110,10 +112,41 @@ __global__ __launch_bounds__(Waves > 4 ? 64 * Waves : kThreads) void quantize_ke
         const bool tiny = s < 0x1p-100f;
         const float inv = 1.f / s;
         int8_t* q = a.q + row * a.q_stride;
+        const auto store = [&](int u, uint32_t lo, uint32_t hi) {
+            const int v = u * kRow + t;
+            if (v < nv) *reinterpret_cast<uint2*>(q + v * 8) = make_uint2(lo, hi);
+        };
+        if (some && !tiny) {
+            // (kMagic has 1 as its last place: adding it rounds to an integer,
+            // ties to even, whose low byte is the sum's)
+            constexpr float kMagic = 12582912.f;
+            uint32_t w[V][2];
+            float far = 0.f;
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                float f[8];
+                raw[u].widen(f);
+                uint32_t n[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float x = f[e] * inv, m = x + kMagic;
+                    far = fmaxf(far, fabsf(x - (m - kMagic)));
+                    n[e] = __float_as_uint(m);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    w[u][h] = __builtin_amdgcn_perm(
+                        __builtin_amdgcn_perm(n[4 * h + 3], n[4 * h + 2], 0x0c0c0400),
+                        __builtin_amdgcn_perm(n[4 * h + 1], n[4 * h], 0x0c0c0400), 0x05040100);
+            }
+            if (__ballot(far > 0.5f - 0x1p-14f) == 0) {
+#pragma unroll
+                for (int u = 0; u < V; ++u) store(u, w[u][0], w[u][1]);
+                continue;
+            }
+        }
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            const int v = u * kRow + t;
-            if (v >= nv) continue;
             float f[8];
             raw[u].widen(f);
             uint32_t w[2] = {0, 0};
@@ -126,7 +159,7 @@ __global__ __launch_bounds__(Waves > 4 ? 64 * Waves : kThreads) void quantize_ke
                              : nearest(f[e], s, inv);
                 w[e >> 2] |= (uint32_t)(n & 0xff) << (8 * (e & 3));
             }
-            *reinterpret_cast<uint2*>(q + v * 8) = make_uint2(w[0], w[1]);
+            store(u, w[0], w[1]);
         }
     }
 }
