@@ -10,6 +10,7 @@
 // integers, four of them in LDS: while one is multiplied the next has arrived
 // and two more are on their way, which covers the memory's latency with one
 // workgroup on a CU.
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_tile.h"
@@ -88,11 +89,17 @@ template <int BI_, int BJ_, int WM_, int WN_>
 struct Shape {
     static constexpr int BI = BI_, BJ = BJ_, WM = WM_, kWaves = WM_ * WN_, kThreads = 64 * kWaves;
     static constexpr int M = WM_ * BI * 32, N = WN_ * BJ * 32;  // features, tokens
-    static constexpr int kStage = (M + N) * kStep;              // bytes
-    static constexpr int kPitch = BI * 32 + 4;                  // floats of a staged token
-    static constexpr int kStaged = kWaves * 32 * kPitch * 4;
-    static constexpr int kLds = kStages * kStage > kStaged ? kStages * kStage : kStaged;
-    static constexpr int LM = M / 16 / kWaves, LN = N / 16 / kWaves;    // loads of a wave, a stage
+    // Loads of a wave and a stage, 16 rows each, the same number for every wave:
+    // rows past the tile's repeat its last one and are not read.
+    static constexpr int kRound = 16 * kWaves;
+    static constexpr int LM = (M + kRound - 1) / kRound, LN = (N + kRound - 1) / kRound;
+    static constexpr int kRowsM = LM * kRound, kStage = (kRowsM + LN * kRound) * kStep;  // bytes
+    // The epilogue turns kTurn blocks of features at a time, behind the first two
+    // stages' place.
+    static constexpr int kTurn = BI % 2 ? 1 : 2, kPitch = kTurn * 32 + 4;   // floats of a token
+    static constexpr int kTurned = 2 * kStage + kWaves * 32 * kPitch * 4;
+    static constexpr int kLds = kStages * kStage > kTurned ? kStages * kStage : kTurned;
+    static constexpr int kPerCu = 160 * 1024 / kLds;            // workgroups
 };
 
 // Slot c of row r of a stage sits at c ^ swizzle(r): 16 lanes that read one
@@ -112,6 +119,9 @@ __device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
 
 __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
 
+// A workgroup takes tiles in turn. The next tile's first two stages are on their
+// way while this one's results are turned and stored, which hides the memory's
+// latency at a tile's start and its own stores.
 template <typename T, int Act, typename S>
 __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, int tiles_m,
                                                                int tiles) {
@@ -120,35 +130,40 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     // Workgroups go round the 8 dies: each die takes a run of tiles, features
     // fastest, so that a token tile is read into one die's L2 once.
-    const int per = (tiles + 7) / 8;
-    const int tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (tile >= tiles || (int)(blockIdx.x >> 3) >= per) return;
-    const int m0 = tile % tiles_m * S::M;
-    const int64_t n0 = (int64_t)(tile / tiles_m) * S::N;
+    const int per = (tiles + 7) / 8, turn = gridDim.x >> 3;
+    const int first = (blockIdx.x & 7) * per, end = min(first + per, tiles);
+    int tile = first + (blockIdx.x >> 3);
+    if (tile >= end) return;
     const int stages = (a.in_dim + kStep - 1) / kStep;
 
     // Loads: 16 rows an instruction, a uniform base and a 32-bit offset a lane
     // (rows are at most 2^22 bytes apart). Rows past the last repeat it; what
     // they give is not stored. Slots past K, in the last stage, repeat the
     // row's first there; the weights' fragments of those are cleared.
-    const int8_t *wm0 = a.weight + (int64_t)m0 * a.in_dim, *qn0 = a.q + n0 * a.q_stride;
-    const int last_m = a.out_dim - 1 - m0;
-    const int last_n = a.n - n0 < S::N ? (int)(a.n - n0) - 1 : S::N - 1;
     const int row = wave * 16 + (lane >> 2), slot = (lane & 3) ^ swizzle(row);
     const int last_slots = (a.in_dim - (stages - 1) * kStep) / 16;
     const int back = slot < last_slots ? 0 : slot * 16;
-    int off_m[LM], off_n[LN];
+    int m0, off_m[LM], off_n[LN];
+    int64_t n0;
+    const int8_t *wm0, *qn0;
+    const auto begin = [&](int t) {
+        m0 = t % tiles_m * S::M;
+        n0 = (int64_t)(t / tiles_m) * S::N;
+        wm0 = a.weight + (int64_t)m0 * a.in_dim;
+        qn0 = a.q + n0 * a.q_stride;
+        const int last_m = min(a.out_dim - m0, S::M) - 1;
+        const int last_n = a.n - n0 < S::N ? (int)(a.n - n0) - 1 : S::N - 1;
 #pragma unroll
-    for (int i = 0; i < LM; ++i)
-        off_m[i] = min(i * 16 * S::kWaves + row, last_m) * a.in_dim + slot * 16;
+        for (int i = 0; i < LM; ++i)
+            off_m[i] = min(i * S::kRound + row, last_m) * a.in_dim + slot * 16;
 #pragma unroll
-    for (int j = 0; j < LN; ++j)
-        off_n[j] = min(j * 16 * S::kWaves + row, last_n) * (int)a.q_stride + slot * 16;
+        for (int j = 0; j < LN; ++j)
+            off_n[j] = min(j * S::kRound + row, last_n) * (int)a.q_stride + slot * 16;
+    };
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds)) + wave * 16 * kStep;
     // load `l` (0 .. kLoads) of this wave's share of stage st
     const auto load = [&](int st, int l) {
-        const uint32_t to =
-            lds0 + (st & (kStages - 1)) * S::kStage + l * 16 * S::kWaves * kStep;
+        const uint32_t to = lds0 + (st & (kStages - 1)) * S::kStage + l * S::kRound * kStep;
         if (l < LM) dma16_from(wm0 + st * kStep, off_m[l < LM ? l : 0], to);
         else dma16_from(qn0 + st * kStep, off_n[l < LM ? 0 : l - LM], to);
     };
@@ -160,20 +175,19 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
             for (int j = 0; j < LN; ++j) off_n[j] -= back;
         }
     };
+    const auto load_stage = [&](int st) {
+        if (st >= stages) return;
+        before_load(st);
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) load(st, l);
+    };
 
     i32x16 acc[BI][BJ];
-#pragma unroll
-    for (int i = 0; i < BI; ++i)
-#pragma unroll
-        for (int j = 0; j < BJ; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-
     const int wm = wave % S::WM * BI * 32, wn = wave / S::WM * BJ * 32;
     const int r32 = lane & 31;
     uint32_t at = ((lane >> 5) ^ swizzle(r32)) << 4;
     at += lds_offset(lds) + r32 * kStep;
-    const uint32_t fa = at + wm * kStep, fb = at + (S::M + wn) * kStep;
+    const uint32_t fa = at + wm * kStep, fb = at + (S::kRowsM + wn) * kStep;
     i32x4 fm[2][BI], fn[2][BJ];
     // where step s of stage st has this lane's fragments; fragment f of it
     struct Place { uint32_t m, n; };
@@ -232,69 +246,94 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
             pin();
         }
     };
-    // What the epilogue needs: the scales of the lane's tokens, and eight
-    // features' of the lane's in the turned tile.
-    constexpr int kAcross = BI * 4, kDown = 64 / kAcross;       // lanes of a token, tokens at once
-    const int d = m0 + wm + (lane % kAcross) * 8;
-    Finish<T, Act> finish;
-    if (d < a.out_dim) finish.load(a, d);
-    float scale[BJ];
-#pragma unroll
-    for (int j = 0; j < BJ; ++j) {
-        const int64_t token = n0 + wn + j * 32 + r32;
-        scale[j] = a.scale[token < a.n ? token : a.n - 1];
-    }
-
     using std::integral_constant;
     using Yes = std::true_type;
     using No = std::false_type;
 
-#pragma unroll
-    for (int st = 0; st < kStages; ++st)
-        if (st < stages) {
-            before_load(st);
-#pragma unroll
-            for (int l = 0; l < kLoads; ++l) load(st, l);
-        }
-    if (stages >= 4) attn::wave_wait<3 * kLoads>();
-    else attn::wave_wait<0>();
-    meet();
-#pragma unroll
-    for (int f = 0; f < kFrags; ++f) read(place(0, 0), 0, f);
-    int st = 0;
-    for (; st + kStages < stages; ++st) stage(st, integral_constant<int, 2>(), Yes(), Yes());
-    if (stages - st >= 4) stage(st++, integral_constant<int, 2>(), No(), Yes());
-    if (stages - st >= 3) stage(st++, integral_constant<int, 1>(), No(), Yes());
-    if (stages - st >= 2) stage(st++, integral_constant<int, 0>(), No(), Yes());
-    stage(st, integral_constant<int, 0>(), No(), No());
-    tile_barrier();                     // the tiles' place is the epilogue's
+    // The epilogue: lanes of a token, tokens at once, turns of the features.
+    constexpr int kAcross = S::kTurn * 4, kDown = 64 / kAcross, kTurns = BI / S::kTurn;
+    float* turned = reinterpret_cast<float*>(lds + 2 * S::kStage) + wave * 32 * S::kPitch;
 
-    // A wave turns 32 tokens at a time in LDS, so that a token's features
-    // leave in 16-byte pieces of whole rows.
-    float* turned = reinterpret_cast<float*>(lds) + wave * 32 * S::kPitch;
+    begin(tile);
+    load_stage(0);
+    load_stage(1);
+    for (;;) {
+        // What the epilogue needs: the scales of the lane's tokens, and those of
+        // eight of its features in every turn.
+        const int d0 = m0 + wm + (lane % kAcross) * 8;
+        const int64_t token0 = n0 + wn;
+        Finish<T, Act> finish[kTurns];
 #pragma unroll
-    for (int j = 0; j < BJ; ++j) {
+        for (int h = 0; h < kTurns; ++h)
+            if (d0 + h * S::kTurn * 32 < a.out_dim) finish[h].load(a, d0 + h * S::kTurn * 32);
+        float scale[BJ];
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) {
+            const int64_t token = token0 + j * 32 + r32;
+            scale[j] = a.scale[token < a.n ? token : a.n - 1];
+        }
+        load_stage(2);
+        load_stage(3);
 #pragma unroll
         for (int i = 0; i < BI; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const i32x16& v = acc[i][j];
-                *reinterpret_cast<float4*>(turned + r32 * S::kPitch + i * 32 + q * 8 +
-                                           (lane >> 5) * 4) =
-                    make_float4((float)v[4 * q] * scale[j], (float)v[4 * q + 1] * scale[j],
-                                (float)v[4 * q + 2] * scale[j], (float)v[4 * q + 3] * scale[j]);
-            }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll 2
-        for (int r = lane / kAcross; r < 32; r += kDown) {
-            const int64_t token = n0 + wn + j * 32 + r;
-            const float* from = turned + r * S::kPitch + (lane % kAcross) * 8;
-            const float4 x = *reinterpret_cast<const float4*>(from),
-                         y = *reinterpret_cast<const float4*>(from + 4);
-            float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            if (token < a.n && d < a.out_dim) finish.write(a, token, d, f);
+            for (int j = 0; j < BJ; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+        // (older than the last two stages' loads: the first two's, the tile
+        // before's stores and the scales)
+        if (stages >= 4) attn::wave_wait<2 * kLoads>();
+        else attn::wave_wait<0>();
+        meet();
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f) read(place(0, 0), 0, f);
+        int st = 0;
+        for (; st + kStages < stages; ++st) stage(st, integral_constant<int, 2>(), Yes(), Yes());
+        if (stages - st >= 4) stage(st++, integral_constant<int, 2>(), No(), Yes());
+        if (stages - st >= 3) stage(st++, integral_constant<int, 1>(), No(), Yes());
+        if (stages - st >= 2) stage(st++, integral_constant<int, 0>(), No(), Yes());
+        stage(st, integral_constant<int, 0>(), No(), No());
+        tile_barrier();                 // nothing reads or writes the stages now
+
+        tile += turn;
+        const bool more = tile < end;
+        if (more) {
+            begin(tile);
+            load_stage(0);
+            load_stage(1);
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        // A wave turns 32 tokens and kTurn blocks of features at a time in LDS, so
+        // that a token's features leave in 16-byte pieces of whole lines.
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+#pragma unroll
+            for (int h = 0; h < kTurns; ++h) {
+#pragma unroll
+                for (int i = 0; i < S::kTurn; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const i32x16& v = acc[h * S::kTurn + i][j];
+                        *reinterpret_cast<float4*>(turned + r32 * S::kPitch + i * 32 + q * 8 +
+                                                   (lane >> 5) * 4) =
+                            make_float4((float)v[4 * q] * scale[j], (float)v[4 * q + 1] * scale[j],
+                                        (float)v[4 * q + 2] * scale[j],
+                                        (float)v[4 * q + 3] * scale[j]);
+                    }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                const int d = d0 + h * S::kTurn * 32;
+#pragma unroll 2
+                for (int r = lane / kAcross; r < 32; r += kDown) {
+                    const int64_t token = token0 + j * 32 + r;
+                    const float* from = turned + r * S::kPitch + (lane % kAcross) * 8;
+                    const float4 x = *reinterpret_cast<const float4*>(from),
+                                 y = *reinterpret_cast<const float4*>(from + 4);
+                    float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                    if (token < a.n && d < a.out_dim) finish[h].write(a, token, d, f);
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+        if (!more) return;
+        meet();                         // the turned tile's place is the stages' again
     }
 }
 
@@ -364,12 +403,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinearArgs a
 }
 
 // ----------------------------------------------------------------- launch ---
+template <typename S>
+int64_t tiles_in(const LinearArgs& a) {
+    return ((a.out_dim + S::M - 1) / S::M) * ((a.n + S::N - 1) / S::N);
+}
+
 template <typename T, int Act, typename S>
 hipError_t tiles_of(const LinearArgs& a, hipStream_t s) {
-    const int64_t tiles_m = (a.out_dim + S::M - 1) / S::M, tiles_n = (a.n + S::N - 1) / S::N;
-    const int64_t tiles = tiles_m * tiles_n;
-    const unsigned grid = (unsigned)((tiles + 7) / 8 * 8);
-    linear_kernel<T, Act, S><<<grid, S::kThreads, S::kLds, s>>>(a, (int)tiles_m, (int)tiles);
+    const int64_t tiles = tiles_in<S>(a);
+    const int64_t grid = std::min<int64_t>((tiles + 7) / 8 * 8, S::kPerCu * kComputeUnits);
+    linear_kernel<T, Act, S><<<(unsigned)grid, S::kThreads, S::kLds, s>>>(
+        a, (a.out_dim + S::M - 1) / S::M, (int)tiles);
     return hipGetLastError();
 }
 
@@ -380,12 +424,28 @@ hipError_t linear_of(const LinearArgs& a, hipStream_t s) {
     else if (a.n <= 32) linear_few_kernel<T, Act, 2><<<few, 64 * kFewWaves, 0, s>>>(a);
     else if (a.n <= 64) linear_few_kernel<T, Act, 4><<<few, 64 * kFewWaves, 0, s>>>(a);
     else {
-        const auto tiles = [&](int m) {
-            return ((a.out_dim + m - 1) / m) * ((a.n + m - 1) / m);
-        };
-        if (tiles(256) >= kComputeUnits) return tiles_of<T, Act, Shape<4, 2, 2, 4>>(a, s);
-        if (tiles(128) >= kComputeUnits / 2) return tiles_of<T, Act, Shape<2, 2, 2, 2>>(a, s);
-        return tiles_of<T, Act, Shape<1, 1, 2, 2>>(a, s);
+#ifdef FORCE
+        return tiles_of<T, Act, Shape<FORCE>>(a, s);
+#endif
+        // Rounds of tiles over the chip, times a round's length (us where K is
+        // 2048, measured; the lengths' ratios hardly change with K).
+        using A = Shape<4, 2, 2, 4>;        // 256 features x 256 tokens
+        using B = Shape<2, 3, 4, 2>;        // 256 x 192
+        using C = Shape<4, 1, 2, 4>;        // 256 x 128
+        using D = Shape<2, 2, 2, 2>;        // 128 x 128
+        using E = Shape<2, 1, 2, 2>;        // 128 x 64
+        const auto rounds = [](int64_t tiles) { return (tiles + kComputeUnits - 1) / kComputeUnits; };
+        const double times[] = {
+            rounds(tiles_in<A>(a)) * 32., rounds(tiles_in<B>(a)) * 27.5,
+            rounds(tiles_in<C>(a)) * 18., rounds(tiles_in<D>(a)) * 10.8,
+            rounds(tiles_in<E>(a)) * 7.4};
+        switch (std::min_element(times, times + 5) - times) {
+            case 0: return tiles_of<T, Act, A>(a, s);
+            case 1: return tiles_of<T, Act, B>(a, s);
+            case 2: return tiles_of<T, Act, C>(a, s);
+            case 3: return tiles_of<T, Act, D>(a, s);
+            default: return tiles_of<T, Act, E>(a, s);
+        }
     }
     return hipGetLastError();
 }
