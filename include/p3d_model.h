@@ -91,7 +91,7 @@ p3d_status p3d_group_norm_backward(const p3d_group_desc* desc, const void* dout,
 
 /* ------------------------------------------------------------------------
  * p3d_quantize_rows -- rows in 8-bit integers, a scale for each:
- *   scale[i] = max_k |x[i, k]| / 127   (binary32, rounded to nearest)
+ *   scale[i] = max_k |x[i, k]| * c    (binary32; c: the number nearest to 1 / 127)
  *   q[i, k]  = x[i, k] / scale[i] to the nearest integer, ties to even
  * exactly (no rounding on the way). Tokens before a linear layer, or a weight
  * [out, in], whose scales are then its output channels'.
@@ -152,7 +152,9 @@ p3d_status p3d_linear_i8(const p3d_linear_i8_desc* desc, const int8_t* q, int64_
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   w = w (1 - lr weight_decay)
  *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in binary32 (the factors in binary64, rounded once).
+ * in binary32 (the factors in binary64, rounded once). States in 8 bits are
+ * reproducible bit for bit: m = (b1 m) + (c1 g), v = (b2 v) + ((c2 g) g) and
+ * sqrt(v) take one rounding an operation, c = 1 - b.
  *
  * weights      param, of param_dtype. With a master (binary32, same size; for
  *              BF16 params), the step updates the master and param is the
@@ -161,11 +163,13 @@ p3d_status p3d_linear_i8(const p3d_linear_i8_desc* desc, const int8_t* q, int64_
  *              sqrt(v), as e4m3 numbers [size] (1 sign, 4 exponent bits of
  *              bias 7, 3 mantissa bits) of which each block of 256 elements
  *              shares a scale, m_scale and v_scale, float [(size + 255) / 256]:
- *              the state is number * scale. After a step a block's scale is
- *              its largest state / 448, and a state between two numbers goes
- *              to the upper one where 16 random bits say so (the one below
- *              otherwise): on average the state is kept, which rounding to
- *              nearest would not do for changes smaller than half a step. A
+ *              the state is number * scale (v: its square). After a step a
+ *              block's scale is its largest state times the number nearest to
+ *              1 / 448, its states are multiplied by (1 / largest) 448, and one
+ *              between two numbers goes to the upper one where 16 random bits
+ *              say so (the one below otherwise): on average the state is kept,
+ *              which rounding to nearest would not do for changes smaller than
+ *              half a step. A
  *              sqrt(v) that is not 0 never becomes 0. A block whose largest
  *              state is below 2^-100 holds zeros; one with an element that is
  *              not finite holds none that is. The step itself uses m and v

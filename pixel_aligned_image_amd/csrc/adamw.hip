@@ -182,8 +182,32 @@ __device__ __forceinline__ uint32_t half_max(uint32_t v) {
 __device__ __forceinline__ void block_scale(uint32_t largest, float& scale, float& by) {
     float top = __uint_as_float(largest);
     if (top < 0x1p-100f) top = 0.f;
-    scale = top / 448.f;
-    by = top == 0.f ? 0.f : 448.f / top;
+    scale = top * (1.f / 448.f);
+    by = top == 0.f ? 0.f : (1.f / top) * 448.f;
+}
+
+// The correctly rounded root of v in [2^-100, inf): a hardware reciprocal root,
+// one step of its refinement, and the remainder's correction. (The compiler's
+// own handles every number, in twice the operations.)
+__device__ __forceinline__ float normal_root(float v) {
+    const float y = __builtin_amdgcn_rsqf(v);
+    float s = v * y, h = 0.5f * y;
+    const float r = fmaf(-h, s, 0.5f);
+    s = fmaf(s, r, s);
+    h = fmaf(h, r, h);
+    return fmaf(fmaf(-s, s, v), h, s);
+}
+
+// The states' update as the interface words it: one rounding an operation, so
+// that states in 8 bits come out the same bit for bit wherever they are computed
+// (a last place would move one in a million over a border).
+__device__ __forceinline__ void moments(const Step& s, float x, float& m, float& v) {
+#pragma clang fp contract(off)
+    const float a = s.b1 * m, b = s.c1 * x;
+    m = a + b;
+    const float c = s.b2 * v, d = s.c2 * x;
+    const float e = d * x;
+    v = c + e;
 }
 
 template <typename P, typename G, bool Master, int Bits>
@@ -226,21 +250,35 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table table, Step s) {
         for (int e = 0; e < 8; ++e) v[e] *= v[e];
     }
     float root[8];
+    if constexpr (Bits == 32) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float x = g[e] * by;
-        m[e] = s.b1 * m[e] + s.c1 * x;
-        v[e] = s.b2 * v[e] + s.c2 * x * x;
-        if constexpr (Bits == 32) {
+        for (int e = 0; e < 8; ++e) {
+            const float x = g[e] * by;
+            m[e] = s.b1 * m[e] + s.c1 * x;
+            v[e] = s.b2 * v[e] + s.c2 * x * x;
             root[e] = sqrtf(v[e]);
             w[e] = w[e] * keep - s.rate * m[e] / (root[e] * s.norm + s.eps);
+        }
+    } else {
+        float least = INFINITY, most = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            moments(s, g[e] * by, m[e], v[e]);
+            least = fminf(least, v[e]);
+            most = fmaxf(most, v[e]);
+        }
+        // (a NaN, which these two pass over, stays one in either root)
+        if (__ballot(least < 0x1p-100f || most == INFINITY) == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) root[e] = normal_root(v[e]);
         } else {
-            // (hardware root and reciprocal, each good to its last place: the
-            // exact ones are 20 operations more of the 60 a state may cost)
-            root[e] = __builtin_amdgcn_sqrtf(v[e]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) root[e] = sqrtf(v[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
             w[e] = w[e] * keep -
                    s.rate * m[e] * __builtin_amdgcn_rcpf(root[e] * s.norm + s.eps);
-        }
     }
     if constexpr (Master) write8<float>(t.master, i, live, w);
     write8<P>(t.param, i, live, w);

@@ -1,6 +1,6 @@
 // quantize.hip -- p3d_quantize_rows: rows in 8-bit integers with a scale each.
 //
-//   s = max |x| / 127,  q = x / s to the nearest integer, ties to even
+//   s = max |x| * (1 / 127),  q = x / s to the nearest integer, ties to even
 //
 // A row is read once: it stays in registers between its maximum and its
 // quotients. Memory bound (3 bytes a bf16 element) only if an element costs
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(Waves > 4 ? 64 * Waves : kThreads) void quantize_ke
         }
         if (!live) continue;
         const bool finite = top < 0x7f800000u;
-        const float s = finite ? __uint_as_float(top) / 127.f : NAN;
+        const float s = finite ? __uint_as_float(top) * (1.f / 127.f) : NAN;
         if (t == 0) a.scale[row] = s;
         const bool some = s > 0.f;
         // (a reciprocal needs s well above the smallest numbers; else the

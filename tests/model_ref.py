@@ -79,9 +79,10 @@ def group_norm_backward(dout, x, offsets, groups, weight=None, bias=None, kind="
 
 # ------------------------------------------------------------------ linear ---
 def quantize(x):
-    """(q, scale): the scale as binary32 holds it, the quotients exact."""
+    """(q, scale): the scale as binary32 holds it (the product of two of its
+    numbers is exact here, and rounded once), the quotients exact."""
     top = x.abs().amax(1)
-    scale = (top / 127).float().double()
+    scale = (top * (torch.ones(1) / 127).double()).float().double()
     scale[~torch.isfinite(top)] = math.nan
     by = torch.where(scale > 0, scale, torch.ones_like(scale))[:, None]
     q = (x / by).round().clamp(-127, 127)
