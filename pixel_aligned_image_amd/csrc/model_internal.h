@@ -63,6 +63,7 @@ struct GroupArgs {
 // chunk.start[b] .. chunk.start[b + 1] are item b's, `rows` rows each but for an
 // item's last.
 struct GroupPlan {
+    int32_t small;                  // slices of the one-launch kernels, or 0: items too long
     int32_t slices;
     int64_t rows;
     ItemTable chunk;

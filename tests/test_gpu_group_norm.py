@@ -113,13 +113,16 @@ def check(n, c, groups, dtype, kind, off=None, s=None, seed=0, affine=True, eps=
 @pytest.mark.parametrize("n,c,groups", [
     (1, 8, 1), (2, 8, 8), (3, 24, 3), (7, 40, 5), (5, 104, 13), (33, 64, 32), (100, 320, 32),
     (257, 96, 1), (1000, 512, 32), (64, 2056, 8), (130, 4096, 32), (9, 4096, 4096),
-    (4097, 72, 9)])
+    (4097, 72, 9), (904, 72, 9), (2728, 72, 9), (2729, 72, 9), (4096, 512, 32), (4100, 512, 32),
+    (9000, 104, 13), (33000, 8, 1), (33000, 8, 8), (5000, 2056, 8), (3000, 4096, 64),
+    (2000, 4096, 4096), (20000, 40, 40)])
 def test_sizes(n, c, groups, dtype, kind):
     check(n, c, groups, TYPES[dtype], kind, seed=n + c)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("n,items", [(1, 3), (40, 7), (3000, 5), (20000, 17), (700, 256)])
+@pytest.mark.parametrize("n,items", [(1, 3), (40, 7), (3000, 5), (20000, 17), (700, 256),
+                                     (60000, 3), (90000, 20)])
 def test_ragged_items(n, items, dtype):
     check(n, 64, 16, TYPES[dtype], "silu", uneven(n, items), seed=items)
 
@@ -132,45 +135,50 @@ def test_one_channel_a_group_and_no_affine():
 @pytest.mark.parametrize("dtype", TYPES)
 def test_strided_rows_keep_what_lies_between(dtype):
     check(301, 72, 9, TYPES[dtype], "silu", uneven(301, 4), stride=16)
+    check(12000, 72, 9, TYPES[dtype], "silu", uneven(12000, 4), stride=16)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
 def test_in_place(dtype):
     check(1500, 128, 8, TYPES[dtype], "silu", uneven(1500, 3), in_place=True)
+    check(30000, 128, 8, TYPES[dtype], "silu", uneven(30000, 3), in_place=True)
 
 
 def test_a_large_mean_keeps_the_digits():
     """Channels a thousand deviations from 0: the deviations come out as the
     input holds them."""
-    s = made(5000, 64, torch.float32, 5)
-    s["x"] = (torch.randn(5000, 64, generator=torch.Generator().manual_seed(6)) + 1000).cuda()
-    check(5000, 64, 8, torch.float32, "none", s=s)
+    for n in (500, 5000, 50000):
+        s = made(n, 64, torch.float32, 5)
+        s["x"] = (torch.randn(n, 64, generator=torch.Generator().manual_seed(6)) + 1000).cuda()
+        check(n, 64, 8, torch.float32, "none", s=s)
 
 
-def test_constant_rows():
+@pytest.mark.parametrize("n", [500, 50000])
+def test_constant_rows(n):
     """A variance of 0: out is act(bias), rstd is 1 / sqrt(eps)."""
-    s = made(500, 32, torch.float32, 7)
-    s["x"] = torch.full((500, 32), 3.25, device="cuda")
+    s = made(n, 32, torch.float32, 7)
+    s["x"] = torch.full((n, 32), 3.25, device="cuda")
     out, mean, rstd = torch.empty_like(s["x"]), torch.empty(1, 4, device="cuda"), torch.empty(
         1, 4, device="cuda")
     p3d.p3d_group_norm(s["x"], out, 4, weight=s["w"], bias=s["b"], mean=mean, rstd=rstd)
-    assert torch.equal(out, s["b"].expand(500, 32)) and (mean == 3.25).all()
+    assert torch.equal(out, s["b"].expand(n, 32)) and (mean == 3.25).all()
     assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
 
 
+@pytest.mark.parametrize("by", [1, 100])
 @pytest.mark.parametrize("dtype", TYPES)
-def test_values_that_are_not_finite_stay_in_their_group(dtype):
-    n, c, groups, off = 300, 64, 8, [0, 100, 250, 300]
+def test_values_that_are_not_finite_stay_in_their_group(dtype, by):
+    n, c, groups, off = 300 * by, 64, 8, [0, 100 * by, 250 * by, 300 * by]
     s = made(n, c, TYPES[dtype], 8)
     clean = torch.empty_like(s["x"])
     p3d.p3d_group_norm(s["x"], clean, groups, off, s["w"], s["b"], "silu")
-    s["x"][120, 10] = float("nan")
-    s["x"][220, 63] = float("inf")
+    s["x"][120 * by, 10] = float("nan")
+    s["x"][220 * by, 63] = float("inf")
     out = torch.empty_like(clean)
     p3d.p3d_group_norm(s["x"], out, groups, off, s["w"], s["b"], "silu")
     bad = torch.zeros(n, c, dtype=torch.bool, device="cuda")
-    bad[100:250, 8:16] = True
-    bad[100:250, 56:64] = True
+    bad[100 * by:250 * by, 8:16] = True
+    bad[100 * by:250 * by, 56:64] = True
     assert out[bad].isnan().all() and torch.equal(out[~bad], clean[~bad])
 
 
@@ -184,23 +192,27 @@ def test_no_rows():
     assert not dw.any() and not db.any()
 
 
-def test_only_the_gradients_that_are_wanted():
-    s = made(400, 64, torch.bfloat16, 9)
-    mean, rstd = torch.empty(1, 8, device="cuda"), torch.empty(1, 8, device="cuda")
-    p3d.p3d_group_norm(s["x"], torch.empty_like(s["x"]), 8, mean=mean, rstd=rstd)
+@pytest.mark.parametrize("n,off", [(400, [0, 400]), (400, [0, 1, 399, 400]), (40000, [0, 40000]),
+                                   (40000, [0, 1, 39999, 40000])])
+def test_only_the_gradients_that_are_wanted(n, off):
+    s = made(n, 64, torch.bfloat16, 9)
+    mean, rstd = (torch.empty(len(off) - 1, 8, device="cuda") for _ in range(2))
+    p3d.p3d_group_norm(s["x"], torch.empty_like(s["x"]), 8, off, mean=mean, rstd=rstd)
     got = []
     for dw, db in ((1, 1), (1, 0), (0, 1), (0, 0)):
         dx = torch.empty_like(s["x"])
         dw, db = (torch.empty(64, device="cuda") if k else None for k in (dw, db))
-        p3d.p3d_group_norm_backward(s["dout"], s["x"], mean, rstd, dx, 8, dweight=dw, dbias=db)
+        p3d.p3d_group_norm_backward(s["dout"], s["x"], mean, rstd, dx, 8, off, dweight=dw,
+                                    dbias=db)
         got.append((dx, dw, db))
     assert all(torch.equal(g[0], got[0][0]) for g in got)
     assert torch.equal(got[1][1], got[0][1]) and torch.equal(got[2][2], got[0][2])
 
 
-def test_the_same_call_gives_the_same_bytes():
-    s = made(30000, 256, torch.bfloat16, 10)
-    off = uneven(30000, 5)
+@pytest.mark.parametrize("n", [300, 30000])
+def test_the_same_call_gives_the_same_bytes(n):
+    s = made(n, 256, torch.bfloat16, 10)
+    off = uneven(n, 5)
     runs = []
     for _ in range(3):
         mean, rstd = torch.empty(5, 32, device="cuda"), torch.empty(5, 32, device="cuda")
