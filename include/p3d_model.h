@@ -190,7 +190,7 @@ p3d_status p3d_linear_i8(const p3d_linear_i8_desc* desc, const int8_t* q, int64_
  *              their values of the time. A device step below 1 counts as 1.
  *
  *   count        tensors, 0..65536; their table is a HOST array and travels in
- *                kernel arguments, 40 tensors a launch
+ *                kernel arguments, 64 tensors a launch
  *   tensors      size >= 0 elements each, below 2^34; no two tensors of the
  *                table, nor two parts of one, may overlap in what a step
  *                writes, nor overlap a gradient

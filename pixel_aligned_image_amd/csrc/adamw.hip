@@ -24,7 +24,7 @@ namespace p3d {
 namespace {
 
 constexpr int kThreads = 256, kPer = 8;             // elements of a thread, neighbours
-constexpr int kTensors = 40;                        // of a launch
+constexpr int kTensors = 64;                        // of a launch: 5 KB of arguments
 constexpr int64_t kChunk = (int64_t)kThreads * kPer;
 constexpr int kNormLoads = 8;                       // 16 bytes each, of a thread and a chunk
 constexpr int64_t kMaxGrid = int64_t(1) << 23;      // (a grid has fewer than 2^32 threads)
