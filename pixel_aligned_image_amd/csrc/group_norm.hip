@@ -242,7 +242,7 @@ __device__ __forceinline__ Joined join_chunks(const float2* __restrict__ p, int 
     // (only the last chunk's count is another; its mean's excess is taken back)
     // The quotient is made while the loads are on their way.
     const double count = 1. / ((double)rows * per), full = (double)(each * per);
-    const float over = (float)((each * n - rows) * per);
+    const double over = (double)((each * n - rows) * per);
     float2 u[kHeld];
     double sum[4] = {0., 0., 0., 0.};
     float m2[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f};
@@ -265,7 +265,7 @@ __device__ __forceinline__ Joined join_chunks(const float2* __restrict__ p, int 
     Joined j{0., 0.};
     if (n == 0) return j;
     const double all = over_lanes((sum[0] + sum[1]) + (sum[2] + sum[3]), lanes);
-    j.mean = (full * all - (double)over * (double)last) * count;
+    j.mean = (full * all - over * (double)last) * count;
     // deviations of the chunks' means: the difference is taken in two parts, so
     // binary32 holds it
     const float hi = (float)j.mean, lo = (float)(j.mean - (double)hi);
@@ -281,7 +281,7 @@ __device__ __forceinline__ Joined join_chunks(const float2* __restrict__ p, int 
     const double dl = (double)((last - hi) - lo);
     const double within = over_lanes((double)((m2[0] + m2[1]) + (m2[2] + m2[3])), lanes);
     const double between = over_lanes((double)((d2[0] + d2[1]) + (d2[2] + d2[3])), lanes);
-    j.var = (within + full * between - (double)over * (dl * dl)) * count;
+    j.var = (within + full * between - over * (dl * dl)) * count;
     if (j.var < 0.) j.var = 0.;
     return j;
 }
@@ -548,17 +548,63 @@ __global__ __launch_bounds__(kTotalCols * kTotalLanes) void group_totals_kernel(
     }
 }
 
-// dx; and, by the workgroups behind the chunks', dweight and dbias from the
-// items' sums.
-template <typename T, int Act, bool Whole>
+// Sums over chunks [first, last) of `count` neighbouring columns from p on, rows
+// `pitch` apart, into LDS, by the whole workgroup: sum[count] at its start. The
+// chunks were written by other dies: 8 loads of a thread are on their way at once.
+__device__ __forceinline__ void sum_chunks(const float* __restrict__ p, int64_t pitch, int count,
+                                           int first, int last, double* part, float* sum) {
+    const int across = count < kThreads ? count : kThreads, down = kThreads / across;
+    const int x = threadIdx.x % across, y = threadIdx.x / across;
+    for (int c0 = 0; c0 < count; c0 += across) {
+        const bool on = c0 + x < count && y < down;
+        double s = 0.;
+        if (on) {
+            const float* q = p + c0 + x;
+#pragma unroll 8
+            for (int c = first + y; c < last; c += down) s += q[(int64_t)c * pitch];
+        }
+        __syncthreads();
+        part[threadIdx.x] = s;
+        __syncthreads();
+        if (on && y == 0) {
+            for (int k = 1; k < down; ++k) s += part[k * across + x];
+            sum[c0 + x] = (float)s;
+        }
+    }
+    __syncthreads();
+}
+
+// dx; and, by the workgroups behind the chunks', dweight and dbias, of kThreads
+// channels each from the items' sums, or (`Here`: the workgroups join the chunks
+// themselves) of kHereCols from the chunks'.
+constexpr int kHereCols = 32;
+
+template <typename T, int Act, bool Whole, bool Here>
 __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, ItemTable chunk,
                                                                int64_t each, int chunks,
+                                                               const float* __restrict__ partial,
                                                                const float* __restrict__ total) {
     constexpr int N = Vec<T>::N, U = 4;
-    extern __shared__ float2 avg[];         // [groups]: A and B of the item, with -1 / count
+    // [groups]: A and B of the item, with -1 / count; Here: then the sums of the
+    // slice's channels
+    extern __shared__ float2 avg[];
+    __shared__ double part[Here ? kThreads : 1];
     if ((int)blockIdx.x >= chunks) {
         if (blockIdx.y) return;
-        const int col = ((int)blockIdx.x - chunks) * kThreads + threadIdx.x;
+        const int block = (int)blockIdx.x - chunks;
+        if constexpr (Here) {
+            float* sum = reinterpret_cast<float*>(avg);
+            const int col = block * kHereCols, count = min(kHereCols, a.channels - col);
+            for (int half = 0; half < 2; ++half) {
+                sum_chunks(partial + half * a.channels + col, 2 * a.channels, count, 0,
+                           chunk.start[a.batch], part, sum);
+                float* to = half ? a.dweight : a.dbias;
+                if (to && (int)threadIdx.x < count) to[col + threadIdx.x] = sum[threadIdx.x];
+                __syncthreads();
+            }
+            return;
+        }
+        const int col = block * kThreads + threadIdx.x;
         if (col >= a.channels) return;
         double s1 = 0., s2 = 0.;
 #pragma unroll 8
@@ -572,11 +618,21 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
         return;
     }
     const Lay lay(a.channels / N / gridDim.y);
-    const int v0 = blockIdx.y * lay.nv, groups = a.groups / gridDim.y;
+    const int v0 = blockIdx.y * lay.nv, groups = a.groups / gridDim.y, width = lay.nv * N;
     const Chunk c(a.items, chunk, a.batch, each, chunks - 1 - (int)blockIdx.x);
     const int per = a.channels / a.groups;
     {
-        const float* t = total + (int64_t)c.item * 2 * a.channels;
+        // the item's sums of the slice's channels: du's, and du x^'s `apart` on
+        const float* t = total + (int64_t)c.item * 2 * a.channels + v0 * N;
+        int apart = a.channels;
+        if constexpr (Here) {
+            float* sum = reinterpret_cast<float*>(avg + groups);
+            for (int half = 0; half < 2; ++half)
+                sum_chunks(partial + half * a.channels + v0 * N, 2 * a.channels, width,
+                           chunk.start[c.item], chunk.start[c.item + 1], part, sum + half * width);
+            t = sum;
+            apart = width;
+        }
         const int64_t count = (int64_t)(a.items.start[c.item + 1] - a.items.start[c.item]) * per;
         const float by = (float)(-1. / (double)count);
         const int lanes = lanes_of(groups), lane = threadIdx.x & (lanes - 1);
@@ -585,10 +641,10 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
             float s1 = 0.f, s2 = 0.f;
             if (g < groups) {
                 for (int e = lane; e < per; e += lanes) {
-                    const int col = v0 * N + g * per + e;
-                    const float w = weight_of<T>(a.weight, col);
+                    const int col = g * per + e;
+                    const float w = weight_of<T>(a.weight, v0 * N + col);
                     s1 += w * t[col];
-                    s2 += w * t[a.channels + col];
+                    s2 += w * t[apart + col];
                 }
             }
             for (int off = 1; off < lanes; off <<= 1) {
@@ -891,17 +947,17 @@ __global__ __launch_bounds__(kSmallThreads) void group_small_backward_kernel(
 }
 
 // ----------------------------------------------------------------- launch ---
-// Whether the apply kernel's workgroups join their item's chunks themselves: what
-// they read for it, all together, against a launch of 4 us (a map of 4096 rows
-// in 256 chunks of 32 groups: 16 MB).
-bool join_in_apply(const GroupArgs& a, const GroupPlan& p) {
+// Whether the second kernel's workgroups join their item's chunks, of `bytes`
+// each, themselves: what they read for it, all together, against a launch of 4 us
+// (a map of 4096 rows in 32 chunks of 32 groups: a quarter of a megabyte).
+bool join_in_apply(const GroupArgs& a, const GroupPlan& p, size_t bytes) {
     int64_t pairs = 0;
     for (int b = 0; b < a.batch; ++b) {
         const int64_t n = p.chunk.start[b + 1] - p.chunk.start[b];
         if (n == 0) return false;                   // (nothing would write its mean and rstd)
         pairs += n * n;
     }
-    return pairs * a.groups * (int64_t)sizeof(float2) <= (int64_t(16) << 20);
+    return pairs * (int64_t)bytes <= (int64_t(16) << 20);
 }
 
 // x of more bytes than this is loaded past the caches in its second pass.
@@ -929,7 +985,7 @@ hipError_t forward_of(const GroupArgs& a, const GroupPlan& p, float2* partial, f
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const bool here = join_in_apply(a, p);
+    const bool here = join_in_apply(a, p, a.groups * sizeof(float2));
     if (!here) {
         const int64_t waves = (int64_t)a.batch * a.groups;
         group_join_kernel<<<(unsigned)((waves + 3) / 4), kThreads, 0, s>>>(a, p.chunk, p.rows,
@@ -965,7 +1021,8 @@ hipError_t backward_act(const GroupArgs& a, const GroupPlan& p, float* partial, 
             <<<dim3(p.small, a.batch), kSmallThreads, lds, s>>>(a, total);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || a.batch == 1 || more == 0) return e;
-        group_dx_kernel<T, Act, Whole><<<more, kThreads, 0, s>>>(a, p.chunk, p.rows, 0, total);
+        group_dx_kernel<T, Act, Whole, false>
+            <<<more, kThreads, 0, s>>>(a, p.chunk, p.rows, 0, nullptr, total);
         return hipGetLastError();
     }
     const int chunks = p.chunk.start[a.batch];
@@ -975,15 +1032,24 @@ hipError_t backward_act(const GroupArgs& a, const GroupPlan& p, float* partial, 
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
+    const size_t lds = a.groups / p.slices * sizeof(float2);
+    if (join_in_apply(a, p, 2 * a.channels * sizeof(float))) {
+        const int here = more ? (a.channels + kHereCols - 1) / kHereCols : 0;
+        group_dx_kernel<T, Act, Whole, true>
+            <<<dim3(chunks + here, p.slices), kThreads,
+               std::max(lds + 2 * a.channels / p.slices * sizeof(float), kHereCols * sizeof(float)),
+               s>>>(a, p.chunk, p.rows, chunks, partial, total);
+        return hipGetLastError();
+    }
     const dim3 grid((unsigned)((2 * a.channels + kTotalCols - 1) / kTotalCols), (unsigned)a.batch);
     group_totals_kernel<<<grid, kTotalCols * kTotalLanes, 0, s>>>(2 * a.channels, p.chunk, partial,
                                                                   total);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (chunks + more == 0) return hipSuccess;
-    group_dx_kernel<T, Act, Whole>
-        <<<dim3(chunks + more, p.slices), kThreads, a.groups / p.slices * sizeof(float2), s>>>(
-            a, p.chunk, p.rows, chunks, total);
+    group_dx_kernel<T, Act, Whole, false>
+        <<<dim3(chunks + more, p.slices), kThreads, lds, s>>>(a, p.chunk, p.rows, chunks, partial,
+                                                              total);
     return hipGetLastError();
 }
 

@@ -420,13 +420,11 @@ hipError_t tiles_of(const LinearArgs& a, hipStream_t s) {
 template <typename T, int Act>
 hipError_t linear_of(const LinearArgs& a, hipStream_t s) {
     const unsigned few = (unsigned)((a.out_dim + 15) / 16);
-    if (a.n <= 16) linear_few_kernel<T, Act, 1><<<few, 64 * kFewWaves, 0, s>>>(a);
-    else if (a.n <= 32) linear_few_kernel<T, Act, 2><<<few, 64 * kFewWaves, 0, s>>>(a);
-    else if (a.n <= 64) linear_few_kernel<T, Act, 4><<<few, 64 * kFewWaves, 0, s>>>(a);
+    const bool fits = few <= (1u << 22);            // (a grid has fewer than 2^32 threads)
+    if (fits && a.n <= 16) linear_few_kernel<T, Act, 1><<<few, 64 * kFewWaves, 0, s>>>(a);
+    else if (fits && a.n <= 32) linear_few_kernel<T, Act, 2><<<few, 64 * kFewWaves, 0, s>>>(a);
+    else if (fits && a.n <= 64) linear_few_kernel<T, Act, 4><<<few, 64 * kFewWaves, 0, s>>>(a);
     else {
-#ifdef FORCE
-        return tiles_of<T, Act, Shape<FORCE>>(a, s);
-#endif
         // Rounds of tiles over the chip, times a round's length (us where K is
         // 2048, measured; the lengths' ratios hardly change with K).
         using A = Shape<4, 2, 2, 4>;        // 256 features x 256 tokens

@@ -234,6 +234,8 @@ p3d_status p3d_group_norm(const p3d_group_desc* desc, const void* x, int64_t x_s
     P3D_TRY(check_pitch(fn, "out_stride", out_stride, a.channels, unit, kMaxStride));
     P3D_TRY(check_tensor(fn, "mean", mean, false, 4));
     P3D_TRY(check_tensor(fn, "rstd", rstd, false, 4));
+    if (mean && mean == rstd)
+        return set_error(P3D_ERR_INVALID_ARG, "%s: mean and rstd must be different tensors", fn);
     const int64_t width = (int64_t)a.channels * e;
     P3D_TRY(check_in_place(fn, {"out", out, desc->n, width, out_stride * e},
                            {"x", x, desc->n, width, x_stride * e}));
@@ -271,6 +273,9 @@ p3d_status p3d_group_norm_backward(const p3d_group_desc* desc, const void* dout,
     P3D_TRY(check_pitch(fn, "dx_stride", dx_stride, a.channels, unit, kMaxStride));
     P3D_TRY(check_tensor(fn, "dweight", dweight, false, 4));
     P3D_TRY(check_tensor(fn, "dbias", dbias, false, 4));
+    if (dweight && dweight == dbias)
+        return set_error(P3D_ERR_INVALID_ARG, "%s: dweight and dbias must be different tensors",
+                         fn);
     const int64_t width = (int64_t)a.channels * e;
     const Rows to{"dx", dx, desc->n, width, dx_stride * e};
     P3D_TRY(check_in_place(fn, to, {"dout", dout, desc->n, width, dout_stride * e}));
@@ -333,8 +338,7 @@ p3d_status p3d_linear_i8(const p3d_linear_i8_desc* desc, const int8_t* q, int64_
     if (d % 8)
         return set_error(P3D_ERR_UNSUPPORTED, "%s: out_dim must be a multiple of 8, got %lld", fn,
                          (long long)d);
-    // (64 x 64 tiles are the smallest, their number an int32 in a grid of
-    // fewer than 2^32 threads)
+    // (the kernels number their tiles, of 128 x 64 or more, in 32 bits)
     if (((n + 63) / 64) * ((d + 63) / 64) >= int64_t(1) << 24)
         return set_error(P3D_ERR_UNSUPPORTED, "%s: n * out_dim must be below 2^36, got %lld * %lld",
                          fn, (long long)n, (long long)d);

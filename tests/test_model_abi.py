@@ -100,6 +100,7 @@ def test_group_tensor_checks(p3d):
     forward(UNSUPPORTED, "out_stride", os=(1 << 30) + 8)
     forward(UNSUPPORTED, "mean", mean=FAKE + 2)
     forward(UNSUPPORTED, "rstd", rstd=FAKE + 1)
+    forward(INVALID, "mean and rstd", mean=FAKE, rstd=FAKE)
     forward(INVALID, "workspace", ws=None)
     forward(INVALID, "workspace", size=16)
     forward(UNSUPPORTED, "256-byte", ws=W + 16)
@@ -123,6 +124,7 @@ def test_group_tensor_checks(p3d):
     backward(UNSUPPORTED, "dx_stride", dxs=70)
     backward(UNSUPPORTED, "dweight", dw=FAKE + 1)
     backward(UNSUPPORTED, "dbias", db=FAKE + 3)
+    backward(INVALID, "dweight and dbias", dw=FAKE, db=FAKE)
     backward(INVALID, "workspace", size=255)
     backward(INVALID, "dx must not overlap dout", dx=X + 128)
     backward(INVALID, "dx must not overlap x", dx=X + MB // 2 + 128)
