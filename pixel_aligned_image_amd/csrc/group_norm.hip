@@ -40,24 +40,28 @@ __device__ __forceinline__ int range_of(const ItemTable& t, int batch, int at) {
     return lo;
 }
 
-// The item and rows of a chunk.
-struct Chunk {
-    int item;
-    int64_t row0;
-    int rows;
-    __device__ __forceinline__ Chunk(const ItemTable& items, const ItemTable& chunk, int batch,
-                                     int64_t each, int at) {
-        item = range_of(chunk, batch, at);
-        row0 = items.start[item] + (int64_t)(at - chunk.start[item]) * each;
-        const int64_t left = items.start[item + 1] - row0;
-        rows = (int)(left < each ? left : each);
-    }
-};
-
 // Rows that thread row `ty` of `step` takes of `rows`.
 __device__ __forceinline__ int rows_of(int rows, int ty, int step) {
     return ty < rows ? (rows - ty + step - 1) / step : 0;
 }
+
+// A chunk: of its item's blocks of `ty` rows every `of`-th from the `at`-th on, so
+// that the workgroups that run side by side read side by side. (Chunks of
+// neighbouring rows, 516 KB of them, met in one memory channel: 361 us for 263
+// where 264,000 rows have 1024 channels.)
+struct Chunk {
+    int item, at, of, rows, ty;
+    int64_t row0;               // of the item
+    __device__ __forceinline__ Chunk(const ItemTable& items, const ItemTable& chunk, int batch,
+                                     int number, int ty_)
+        : item(range_of(chunk, batch, number)), at(number - chunk.start[item]),
+          of(chunk.start[item + 1] - chunk.start[item]),
+          rows(items.start[item + 1] - items.start[item]), ty(ty_), row0(items.start[item]) {}
+    // of thread row y: its first row, how many, and how far apart
+    __device__ __forceinline__ int64_t first(int y) const { return row0 + (int64_t)at * ty + y; }
+    __device__ __forceinline__ int count(int y) const { return rows_of(rows, at * ty + y, of * ty); }
+    __device__ __forceinline__ int64_t step() const { return (int64_t)of * ty; }
+};
 
 template <typename T>
 __device__ __forceinline__ const uint4* vectors(const void* base, int64_t row, int64_t stride) {
@@ -108,27 +112,27 @@ struct Moments {
     }
 };
 
-constexpr int kBatch = 8;       // rows that a thread loads before it uses them
 
 // The chunk's moments of every group. Where a vector's channels are of one
 // group (Whole), a thread keeps one pair for it, else a pair per channel.
-// One batch of 8 rows is centred on its own mean in registers and then joined
+// One batch of 8 (4) rows is centred on its own mean in registers and then joined
 // to the thread's: 4 operations a value in all, below the 13 that a bf16
 // stream at the memory's rate leaves.
 template <typename T, bool Whole>
 __global__ __launch_bounds__(kThreads, 4) void group_stats_kernel(
-    GroupArgs a, ItemTable chunk, int64_t each, float2* __restrict__ partial) {
+    GroupArgs a, ItemTable chunk, float2* __restrict__ partial) {
     constexpr int N = Vec<T>::N, K = Whole ? 1 : N, PerUnit = Whole ? N : 1;
+    constexpr int kBatch = Whole ? 8 : 4;   // rows that a thread loads before it uses them
     __shared__ float2 unit[(Whole ? 1 : N) * 4096 / N];
     const Lay lay(a.channels / N / gridDim.y);
     const int v0 = blockIdx.y * lay.nv, groups = a.groups / gridDim.y, group0 = blockIdx.y * groups;
-    const Chunk c(a.items, chunk, a.batch, each, blockIdx.x);
+    const Chunk c(a.items, chunk, a.batch, blockIdx.x, lay.ty);
     const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
-    const int mine = ty < lay.ty ? rows_of(c.rows, ty, lay.ty) : 0;
-    const int64_t step = a.x_stride * (16 / N) * lay.ty;       // bytes
+    const int mine = ty < lay.ty ? c.count(ty) : 0;
+    const int64_t step = a.x_stride * (16 / N) * c.step();      // bytes
     for (int v = tx; v < lay.nv && ty < lay.ty; v += lay.tx) {
         const char* p =
-            reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v0 + v);
+            reinterpret_cast<const char*>(vectors<T>(a.x, c.first(ty), a.x_stride) + v0 + v);
         float mean[K], m2[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) mean[k] = m2[k] = 0.f;
@@ -207,7 +211,7 @@ __global__ __launch_bounds__(kThreads, 4) void group_stats_kernel(
         if (g < groups) {
             for (int e = lane; e < per * lay.ty; e += lanes) {
                 const int y = e / per;
-                const int n = rows_of(c.rows, y, lay.ty);
+                const int n = c.count(y);
                 const float2 u = unit[y * width + g * per + (e - y * per)];
                 m.join((float)(n * PerUnit), u.x, u.y);
             }
@@ -238,50 +242,58 @@ __device__ __forceinline__ double over_lanes(double v, int lanes) {
 }
 
 __device__ __forceinline__ Joined join_chunks(const float2* __restrict__ p, int n, int lane,
-                                              int lanes, int64_t rows, int64_t each, int per) {
-    // (only the last chunk's count is another; its mean's excess is taken back)
-    // The quotient is made while the loads are on their way.
-    const double count = 1. / ((double)rows * per), full = (double)(each * per);
-    const double over = (double)((each * n - rows) * per);
+                                              int lanes, int rows, int ty, int per) {
+    Joined j{0., 0.};
+    if (n == 0) return j;
+    // `whole` blocks of ty rows a chunk, one more in the first `more` chunks, and
+    // the last block, in chunk `last`, short of `miss` rows. (The quotient is made
+    // while the loads are on their way.)
+    const int blocks = (rows + ty - 1) / ty, whole = blocks / n, more = blocks - whole * n;
+    const int last = (blocks - 1) % n;
+    const double block = (double)ty * per, miss = ((double)blocks * ty - rows) * per;
+    const double base = block * whole, count = 1. / ((double)rows * per);
     float2 u[kHeld];
-    double sum[4] = {0., 0., 0., 0.};
-    float m2[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f};
-    const auto load = [&](int base) {
+    double sum[4] = {0., 0., 0., 0.}, first = 0.;
+    float m2[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f}, e2 = 0.f;
+    const auto load = [&](int from) {
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
-            const int c = base + k * lanes + lane;
+            const int c = from + k * lanes + lane;
             u[k] = c < n ? p[c] : make_float2(0.f, 0.f);
         }
     };
-    const float last = n > 0 ? p[n - 1].x : 0.f;
-    for (int base = 0; base < n; base += kHeld * lanes) {
-        load(base);
+    const float xl = p[last].x;
+    for (int from = 0; from < n; from += kHeld * lanes) {
+        load(from);
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
             sum[k & 3] += (double)u[k].x;
+            if (from + k * lanes + lane < more) first += (double)u[k].x;
             m2[k & 3] += u[k].y;
         }
     }
-    Joined j{0., 0.};
-    if (n == 0) return j;
     const double all = over_lanes((sum[0] + sum[1]) + (sum[2] + sum[3]), lanes);
-    j.mean = (full * all - over * (double)last) * count;
+    if (more) first = over_lanes(first, lanes);
+    j.mean = (base * all + block * first - miss * (double)xl) * count;
     // deviations of the chunks' means: the difference is taken in two parts, so
     // binary32 holds it
     const float hi = (float)j.mean, lo = (float)(j.mean - (double)hi);
-    for (int base = 0; base < n; base += kHeld * lanes) {
-        if (n > kHeld * lanes) load(base);
+    for (int from = 0; from < n; from += kHeld * lanes) {
+        if (n > kHeld * lanes) load(from);
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
-            const int c = base + k * lanes + lane;
-            const float d = c < n ? (u[k].x - hi) - lo : 0.f;
-            d2[k & 3] += d * d;
+            const int c = from + k * lanes + lane;
+            float d = c < n ? (u[k].x - hi) - lo : 0.f;
+            d *= d;
+            d2[k & 3] += d;
+            if (c < more) e2 += d;
         }
     }
-    const double dl = (double)((last - hi) - lo);
+    const double dl = (double)((xl - hi) - lo);
     const double within = over_lanes((double)((m2[0] + m2[1]) + (m2[2] + m2[3])), lanes);
-    const double between = over_lanes((double)((d2[0] + d2[1]) + (d2[2] + d2[3])), lanes);
-    j.var = (within + full * between - over * (dl * dl)) * count;
+    const double between = over_lanes(
+        base * (double)((d2[0] + d2[1]) + (d2[2] + d2[3])) + block * (double)e2, lanes);
+    j.var = (within + between - miss * (dl * dl)) * count;
     if (j.var < 0.) j.var = 0.;
     return j;
 }
@@ -296,7 +308,7 @@ __device__ __forceinline__ float4 stat_of(const Joined& j, float eps) {
 
 // A wave joins the chunks of a group of an item.
 __global__ __launch_bounds__(kThreads) void group_join_kernel(GroupArgs a, ItemTable chunk,
-                                                              int64_t each,
+                                                              int ty,
                                                               const float2* __restrict__ partial,
                                                               float4* __restrict__ stat) {
     const int64_t at = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
@@ -305,7 +317,7 @@ __global__ __launch_bounds__(kThreads) void group_join_kernel(GroupArgs a, ItemT
     const int first = chunk.start[b];
     const Joined j = join_chunks(partial + (int64_t)g * chunk.start[a.batch] + first,
                                  chunk.start[b + 1] - first, lane, 64,
-                                 a.items.start[b + 1] - a.items.start[b], each,
+                                 a.items.start[b + 1] - a.items.start[b], ty,
                                  a.channels / a.groups);
     if (lane) return;
     const float4 s = stat_of(j, a.eps);
@@ -316,7 +328,7 @@ __global__ __launch_bounds__(kThreads) void group_join_kernel(GroupArgs a, ItemT
 
 // The same by a workgroup for `groups` groups of item b from group0 on, into LDS;
 // `write` as well into mean and rstd.
-__device__ __forceinline__ void join_here(const GroupArgs& a, const ItemTable& chunk, int64_t each,
+__device__ __forceinline__ void join_here(const GroupArgs& a, const ItemTable& chunk, int ty,
                                           const float2* __restrict__ partial, int b, int group0,
                                           int groups, bool write, float4* __restrict__ stat) {
     const int lanes = lanes_of(groups), lane = threadIdx.x & (lanes - 1);
@@ -325,8 +337,8 @@ __device__ __forceinline__ void join_here(const GroupArgs& a, const ItemTable& c
         const int g = g0 + threadIdx.x / lanes;
         const bool on = g < groups;
         const Joined j = join_chunks(
-            partial + (int64_t)(group0 + (on ? g : 0)) * chunk.start[a.batch] + first, n, lane, lanes, a.items.start[b + 1] - a.items.start[b], each,
-                                     a.channels / a.groups);
+            partial + (int64_t)(group0 + (on ? g : 0)) * chunk.start[a.batch] + first, n, lane,
+            lanes, a.items.start[b + 1] - a.items.start[b], ty, a.channels / a.groups);
         if (on && lane == 0) {
             const float4 s = stat_of(j, a.eps);
             stat[g] = s;
@@ -347,25 +359,27 @@ __device__ __forceinline__ uint4 load16(const char* p) {
         return *reinterpret_cast<const uint4*>(p);
 }
 
-// out = act((x - hi) k + o) with k = rstd w and o = b - lo k. The chunks run
-// last to first: what the statistics read last is still in the caches. `Past`:
+// out = act((x - hi) k + o) with k = rstd w and o = b - lo k. Rows run last to
+// first: what the statistics read last is still in the caches. `Past`:
 // a map larger than those is loaded past them here, so that what was just read
 // does not drive out what was read before and is wanted next (269 us for 310
 // where x has 537 MB; 168 for 163 with the gradient where it has 102 MB).
 // `Here`: the workgroup joins its item's chunks itself.
 template <typename T, int Act, bool Whole, bool Past, bool Here>
 __global__ __launch_bounds__(kThreads, 4) void group_apply_kernel(
-    GroupArgs a, ItemTable chunk, int64_t each, const float2* __restrict__ partial,
+    GroupArgs a, ItemTable chunk, const float2* __restrict__ partial,
     const float4* __restrict__ stats) {
-    constexpr int N = Vec<T>::N, K = Whole ? 1 : N, U = 4;
+    constexpr int N = Vec<T>::N, K = Whole ? 1 : N, U = Whole ? 4 : 2;
     extern __shared__ float4 joined[];              // Here: [groups]
     const Lay lay(a.channels / N / gridDim.y);
     const int v0 = blockIdx.y * lay.nv, groups = a.groups / gridDim.y, group0 = blockIdx.y * groups;
-    const int at = gridDim.x - 1 - blockIdx.x;
-    const Chunk c(a.items, chunk, a.batch, each, at);
+    const int at = blockIdx.x;
+    const Chunk c(a.items, chunk, a.batch, at, lay.ty);
     const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
-    const int mine = ty < lay.ty ? rows_of(c.rows, ty, lay.ty) : 0;
-    const int64_t step = a.x_stride * (16 / N) * lay.ty, ostep = a.out_stride * (16 / N) * lay.ty;
+    const int mine = ty < lay.ty ? c.count(ty) : 0;
+    const int64_t step = -a.x_stride * (16 / N) * c.step(),
+                  ostep = -a.out_stride * (16 / N) * c.step();
+    const int64_t row = c.first(ty) + (mine - 1) * c.step();        // the last, and on to the first
     const int per = a.channels / a.groups;
     // The first rows are on their way before the statistics are there.
     uint4 q[U];
@@ -374,13 +388,13 @@ __global__ __launch_bounds__(kThreads, 4) void group_apply_kernel(
         for (int i = 0; i < U; ++i)
             if (i < rows) q[i] = load16<Past>(p + i * step);
     };
-    const char* x0 = reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v0);
+    const char* x0 = reinterpret_cast<const char*>(vectors<T>(a.x, row, a.x_stride) + v0);
     char* o0 = const_cast<char*>(
-        reinterpret_cast<const char*>(vectors<T>(a.out, c.row0 + ty, a.out_stride) + v0));
+        reinterpret_cast<const char*>(vectors<T>(a.out, row, a.out_stride) + v0));
     load(x0 + tx * 16, mine);
     const float4* stat = joined;
     if constexpr (Here)
-        join_here(a, chunk, each, partial, c.item, group0, groups, at == chunk.start[c.item],
+        join_here(a, chunk, lay.ty, partial, c.item, group0, groups, at == chunk.start[c.item],
                   joined);
     else
         stat = stats + (int64_t)c.item * a.groups + group0;
@@ -450,22 +464,22 @@ struct Channels {
 // Sums of du and of du x^ of every channel over the chunk: [2][channels].
 template <typename T, int Act, bool Whole>
 __global__ __launch_bounds__(kThreads, 4) void group_sums_kernel(GroupArgs a, ItemTable chunk,
-                                                                 int64_t each,
                                                                  float* __restrict__ partial) {
-    constexpr int N = Vec<T>::N, U = 4;
+    constexpr int N = Vec<T>::N, U = Whole ? 4 : 2;
     __shared__ float sums[2 * kThreads * N];
     const Lay lay(a.channels / N / gridDim.y);
     const int v0 = blockIdx.y * lay.nv, width = lay.nv * N;
-    const Chunk c(a.items, chunk, a.batch, each, blockIdx.x);
+    const Chunk c(a.items, chunk, a.batch, blockIdx.x, lay.ty);
     const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
-    const int mine = ty < lay.ty ? rows_of(c.rows, ty, lay.ty) : 0;
-    const int64_t step = a.x_stride * (16 / N) * lay.ty, dstep = a.dout_stride * (16 / N) * lay.ty;
+    const int mine = ty < lay.ty ? c.count(ty) : 0;
+    const int64_t step = a.x_stride * (16 / N) * c.step(),
+                  dstep = a.dout_stride * (16 / N) * c.step();
     float* to = partial + (int64_t)blockIdx.x * 2 * a.channels + v0 * N;
     for (int v = tx; v < lay.nv && ty < lay.ty; v += lay.tx) {
         const char* p =
-            reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v0 + v);
+            reinterpret_cast<const char*>(vectors<T>(a.x, c.first(ty), a.x_stride) + v0 + v);
         const char* d = reinterpret_cast<const char*>(
-            vectors<T>(a.dout, c.row0 + ty, a.dout_stride) + v0 + v);
+            vectors<T>(a.dout, c.first(ty), a.dout_stride) + v0 + v);
         Channels<T, Whole> ch;
         ch.load(a, c.item, v0 + v);
         float s1[N], s2[N];
@@ -581,10 +595,10 @@ constexpr int kHereCols = 32;
 
 template <typename T, int Act, bool Whole, bool Here>
 __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, ItemTable chunk,
-                                                               int64_t each, int chunks,
+                                                               int chunks,
                                                                const float* __restrict__ partial,
                                                                const float* __restrict__ total) {
-    constexpr int N = Vec<T>::N, U = 4;
+    constexpr int N = Vec<T>::N, U = Whole ? 4 : 2;
     // [groups]: A and B of the item, with -1 / count; Here: then the sums of the
     // slice's channels
     extern __shared__ float2 avg[];
@@ -619,7 +633,7 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
     }
     const Lay lay(a.channels / N / gridDim.y);
     const int v0 = blockIdx.y * lay.nv, groups = a.groups / gridDim.y, width = lay.nv * N;
-    const Chunk c(a.items, chunk, a.batch, each, chunks - 1 - (int)blockIdx.x);
+    const Chunk c(a.items, chunk, a.batch, (int)blockIdx.x, lay.ty);
     const int per = a.channels / a.groups;
     {
         // the item's sums of the slice's channels: du's, and du x^'s `apart` on
@@ -657,16 +671,17 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
     __syncthreads();
     const int tx = threadIdx.x % lay.tx, ty = threadIdx.x / lay.tx;
     if (ty >= lay.ty) return;
-    const int mine = rows_of(c.rows, ty, lay.ty);
-    const int64_t step = a.x_stride * (16 / N) * lay.ty, dstep = a.dout_stride * (16 / N) * lay.ty,
-                  ostep = a.out_stride * (16 / N) * lay.ty;
+    const int mine = c.count(ty);
+    const int64_t step = -a.x_stride * (16 / N) * c.step(),
+                  dstep = -a.dout_stride * (16 / N) * c.step(),
+                  ostep = -a.out_stride * (16 / N) * c.step();
+    const int64_t row = c.first(ty) + (mine - 1) * c.step();        // the last, and on to the first
     for (int v = tx; v < lay.nv; v += lay.tx) {
-        const char* p =
-            reinterpret_cast<const char*>(vectors<T>(a.x, c.row0 + ty, a.x_stride) + v0 + v);
-        const char* d = reinterpret_cast<const char*>(
-            vectors<T>(a.dout, c.row0 + ty, a.dout_stride) + v0 + v);
+        const char* p = reinterpret_cast<const char*>(vectors<T>(a.x, row, a.x_stride) + v0 + v);
+        const char* d =
+            reinterpret_cast<const char*>(vectors<T>(a.dout, row, a.dout_stride) + v0 + v);
         char* o = const_cast<char*>(
-            reinterpret_cast<const char*>(vectors<T>(a.dx, c.row0 + ty, a.out_stride) + v0 + v));
+            reinterpret_cast<const char*>(vectors<T>(a.dx, row, a.out_stride) + v0 + v));
         Channels<T, Whole> ch;
         ch.load(a, c.item, v0 + v);
         constexpr int K = Channels<T, Whole>::K;
@@ -981,14 +996,14 @@ hipError_t forward_of(const GroupArgs& a, const GroupPlan& p, float2* partial, f
     }
     const int chunks = p.chunk.start[a.batch];
     if (chunks) {
-        group_stats_kernel<T, Whole><<<dim3(chunks, p.slices), kThreads, 0, s>>>(a, p.chunk, p.rows, partial);
+        group_stats_kernel<T, Whole><<<dim3(chunks, p.slices), kThreads, 0, s>>>(a, p.chunk, partial);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     const bool here = join_in_apply(a, p, a.groups * sizeof(float2));
     if (!here) {
         const int64_t waves = (int64_t)a.batch * a.groups;
-        group_join_kernel<<<(unsigned)((waves + 3) / 4), kThreads, 0, s>>>(a, p.chunk, p.rows,
+        group_join_kernel<<<(unsigned)((waves + 3) / 4), kThreads, 0, s>>>(a, p.chunk, p.ty,
                                                                            partial, stat);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !chunks) return e;
@@ -1000,13 +1015,13 @@ hipError_t forward_of(const GroupArgs& a, const GroupPlan& p, float2* partial, f
         const dim3 grid(chunks, p.slices);
         if (here)
             group_apply_kernel<T, A, Whole, false, true>
-                <<<grid, kThreads, lds, s>>>(a, p.chunk, p.rows, partial, stat);
+                <<<grid, kThreads, lds, s>>>(a, p.chunk, partial, stat);
         else if (past)
             group_apply_kernel<T, A, Whole, true, false>
-                <<<grid, kThreads, 0, s>>>(a, p.chunk, p.rows, partial, stat);
+                <<<grid, kThreads, 0, s>>>(a, p.chunk, partial, stat);
         else
             group_apply_kernel<T, A, Whole, false, false>
-                <<<grid, kThreads, 0, s>>>(a, p.chunk, p.rows, partial, stat);
+                <<<grid, kThreads, 0, s>>>(a, p.chunk, partial, stat);
     });
 }
 
@@ -1022,13 +1037,13 @@ hipError_t backward_act(const GroupArgs& a, const GroupPlan& p, float* partial, 
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || a.batch == 1 || more == 0) return e;
         group_dx_kernel<T, Act, Whole, false>
-            <<<more, kThreads, 0, s>>>(a, p.chunk, p.rows, 0, nullptr, total);
+            <<<more, kThreads, 0, s>>>(a, p.chunk, 0, nullptr, total);
         return hipGetLastError();
     }
     const int chunks = p.chunk.start[a.batch];
     if (chunks) {
         group_sums_kernel<T, Act, Whole>
-            <<<dim3(chunks, p.slices), kThreads, 0, s>>>(a, p.chunk, p.rows, partial);
+            <<<dim3(chunks, p.slices), kThreads, 0, s>>>(a, p.chunk, partial);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -1038,7 +1053,7 @@ hipError_t backward_act(const GroupArgs& a, const GroupPlan& p, float* partial, 
         group_dx_kernel<T, Act, Whole, true>
             <<<dim3(chunks + here, p.slices), kThreads,
                std::max(lds + 2 * a.channels / p.slices * sizeof(float), kHereCols * sizeof(float)),
-               s>>>(a, p.chunk, p.rows, chunks, partial, total);
+               s>>>(a, p.chunk, chunks, partial, total);
         return hipGetLastError();
     }
     const dim3 grid((unsigned)((2 * a.channels + kTotalCols - 1) / kTotalCols), (unsigned)a.batch);
@@ -1048,7 +1063,7 @@ hipError_t backward_act(const GroupArgs& a, const GroupPlan& p, float* partial, 
     if (e != hipSuccess) return e;
     if (chunks + more == 0) return hipSuccess;
     group_dx_kernel<T, Act, Whole, false>
-        <<<dim3(chunks + more, p.slices), kThreads, lds, s>>>(a, p.chunk, p.rows, chunks, partial,
+        <<<dim3(chunks + more, p.slices), kThreads, lds, s>>>(a, p.chunk, chunks, partial,
                                                               total);
     return hipGetLastError();
 }
@@ -1094,12 +1109,16 @@ GroupPlan group_norm_plan(const GroupArgs& a, p3d_dtype dt) {
         }
     const Lay lay(a.channels / unit / p.slices);
     const int64_t n = a.items.start[a.batch] * (int64_t)p.slices;
-    p.rows = std::max<int64_t>((n + most - 1) / most, 4 * lay.ty);
-    p.rows = (p.rows + lay.ty - 1) / lay.ty * lay.ty;
+    const int64_t rows = std::max<int64_t>((n + most - 1) / most, 4 * lay.ty);
+    p.ty = lay.ty;
+    // (Odd numbers of chunks: workgroups go round 8 dies, and of an even number a
+    // die would come back to the same memory channels in every round: 320 us for
+    // 263 where 262,144 rows have 1024 channels.)
     int32_t at = 0;
     for (int b = 0; b < a.batch; ++b) {
         p.chunk.start[b] = at;
-        at += (int32_t)((a.items.start[b + 1] - a.items.start[b] + p.rows - 1) / p.rows);
+        const int32_t of = (int32_t)((a.items.start[b + 1] - a.items.start[b] + rows - 1) / rows);
+        at += of > 0 ? (of - 1) | 1 : 0;
     }
     for (int b = a.batch; b <= P3D_MAX_BATCH; ++b) p.chunk.start[b] = at;
     const size_t chunks = at, batch = a.batch;

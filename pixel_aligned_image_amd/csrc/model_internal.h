@@ -59,13 +59,11 @@ struct GroupArgs {
     ItemTable items;
 };
 
-// How a call is cut: its channels into `slices`, its rows into chunks.
-// chunk.start[b] .. chunk.start[b + 1] are item b's, `rows` rows each but for an
-// item's last.
+// How a call is cut: its channels into `slices`, every item's rows into chunks,
+// chunk.start[b] .. chunk.start[b + 1] item b's.
 struct GroupPlan {
     int32_t small;                  // slices of the one-launch kernels, or 0: items too long
-    int32_t slices;
-    int64_t rows;
+    int32_t slices, ty;             // rows of a chunk's blocks
     ItemTable chunk;
     size_t bytes;                   // of the workspace
 };
