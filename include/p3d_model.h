@@ -49,7 +49,7 @@ typedef enum p3d_act {
  *                needs no copy); out may be x with equal strides and must not
  *                overlap it otherwise
  *   mean, rstd   float [batch, groups], or NULL; 0 and 1 / sqrt(eps) for an
- *                item without rows. The gradient needs both.
+ *                item without rows. The gradient needs both, of every item.
  *   Alignment: 16 bytes (mean, rstd: 4).
  *   workspace    p3d_group_norm_workspace_size(desc) bytes, for the forward
  *                call and the gradient alike

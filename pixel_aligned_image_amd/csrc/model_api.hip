@@ -265,8 +265,8 @@ p3d_status p3d_group_norm_backward(const p3d_group_desc* desc, const void* dout,
     const bool some = desc->n > 0;
     P3D_TRY(check_tensor(fn, "dout", dout, some));
     P3D_TRY(check_tensor(fn, "x", x, some));
-    P3D_TRY(check_tensor(fn, "mean", mean, some, 4));
-    P3D_TRY(check_tensor(fn, "rstd", rstd, some, 4));
+    P3D_TRY(check_tensor(fn, "mean", mean, true, 4));
+    P3D_TRY(check_tensor(fn, "rstd", rstd, true, 4));
     P3D_TRY(check_tensor(fn, "dx", dx, some));
     P3D_TRY(check_pitch(fn, "dout_stride", dout_stride, a.channels, unit, kMaxStride));
     P3D_TRY(check_pitch(fn, "x_stride", x_stride, a.channels, unit, kMaxStride));

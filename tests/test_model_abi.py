@@ -129,6 +129,10 @@ def test_group_tensor_checks(p3d):
     backward(INVALID, "dx must not overlap dout", dx=X + 128)
     backward(INVALID, "dx must not overlap x", dx=X + MB // 2 + 128)
     backward(SHAPE, "in place", dx=X, dxs=128)
+    # every item has a mean and an rstd, also one without rows
+    d = group(p3d, (0, 0, 0))
+    backward(INVALID, "mean is NULL", dout=None, x=None, dx=None, mean=None)
+    backward(INVALID, "rstd is NULL", dout=None, x=None, dx=None, rstd=None)
 
 
 def test_group_workspace_holds_the_partial_sums(p3d):
