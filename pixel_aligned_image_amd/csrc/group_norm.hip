@@ -6,12 +6,14 @@
 //
 // Both directions are memory bound: statistics over a whole map stand between
 // the first and the last use of a row, so x (and dout) is read twice, from the
-// caches where it fits. A call is cut into chunks of rows and slices of whole
-// groups; a thread owns 16-byte vectors of channels and walks the chunk's rows,
-// so per-channel factors stay in registers. Slices are as narrow as whole cache
-// lines allow: the narrower, the more rows a chunk has, and the fewer chunks
-// there are to join. Chunk results go to the workspace and are joined in a
-// fixed order.
+// caches where it fits: 3 (5) times the map's bytes in all, and 265 us where x has
+// 537 MB, 6.1 TB/s of them, a large copy's rate. A small map takes as long as its
+// launches do (12 to 18 us).
+//
+// A call is cut into chunks of rows and slices of whole groups; a thread owns
+// 16-byte vectors of channels and walks the chunk's rows, so per-channel factors
+// stay in registers. Chunk results go to the workspace and are joined in a fixed
+// order.
 #include <algorithm>
 
 #include "model_internal.h"
@@ -46,9 +48,9 @@ __device__ __forceinline__ int rows_of(int rows, int ty, int step) {
 }
 
 // A chunk: of its item's blocks of `ty` rows every `of`-th from the `at`-th on, so
-// that the workgroups that run side by side read side by side. (Chunks of
-// neighbouring rows, 516 KB of them, met in one memory channel: 361 us for 263
-// where 264,000 rows have 1024 channels.)
+// that the workgroups that run side by side read side by side: 263 us where 264,000
+// rows have 1024 channels, and 361 with chunks of neighbouring rows, 516 KB of
+// them, that meet in one memory channel.
 struct Chunk {
     int item, at, of, rows, ty;
     int64_t row0;               // of the item
@@ -111,7 +113,6 @@ struct Moments {
         n = all;
     }
 };
-
 
 // The chunk's moments of every group. Where a vector's channels are of one
 // group (Whole), a thread keeps one pair for it, else a pair per channel.
@@ -230,17 +231,17 @@ __global__ __launch_bounds__(kThreads, 4) void group_stats_kernel(
 // binary64, by `lanes` neighbouring lanes (a power of two, 64 at most). The
 // chunks' counts are known, so the mean comes first and the deviations are about
 // it: no division a chunk. The chunks were written by other dies, so a load
-// takes a microsecond: kHeld of a lane are on their way at once.
+// takes a microsecond: `Held` of a lane are on their way at once.
 struct Joined {
     double mean, var;
 };
-constexpr int kHeld = 16;
 
 __device__ __forceinline__ double over_lanes(double v, int lanes) {
     for (int off = 1; off < lanes; off <<= 1) v += __shfl_xor(v, off);
     return v;
 }
 
+template <int Held>
 __device__ __forceinline__ Joined join_chunks(const float2* __restrict__ p, int n, int lane,
                                               int lanes, int rows, int ty, int per) {
     Joined j{0., 0.};
@@ -252,21 +253,21 @@ __device__ __forceinline__ Joined join_chunks(const float2* __restrict__ p, int 
     const int last = (blocks - 1) % n;
     const double block = (double)ty * per, miss = ((double)blocks * ty - rows) * per;
     const double base = block * whole, count = 1. / ((double)rows * per);
-    float2 u[kHeld];
+    float2 u[Held];
     double sum[4] = {0., 0., 0., 0.}, first = 0.;
     float m2[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f}, e2 = 0.f;
     const auto load = [&](int from) {
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
+        for (int k = 0; k < Held; ++k) {
             const int c = from + k * lanes + lane;
             u[k] = c < n ? p[c] : make_float2(0.f, 0.f);
         }
     };
     const float xl = p[last].x;
-    for (int from = 0; from < n; from += kHeld * lanes) {
+    for (int from = 0; from < n; from += Held * lanes) {
         load(from);
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
+        for (int k = 0; k < Held; ++k) {
             sum[k & 3] += (double)u[k].x;
             if (from + k * lanes + lane < more) first += (double)u[k].x;
             m2[k & 3] += u[k].y;
@@ -278,10 +279,10 @@ __device__ __forceinline__ Joined join_chunks(const float2* __restrict__ p, int 
     // deviations of the chunks' means: the difference is taken in two parts, so
     // binary32 holds it
     const float hi = (float)j.mean, lo = (float)(j.mean - (double)hi);
-    for (int from = 0; from < n; from += kHeld * lanes) {
-        if (n > kHeld * lanes) load(from);
+    for (int from = 0; from < n; from += Held * lanes) {
+        if (n > Held * lanes) load(from);
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
+        for (int k = 0; k < Held; ++k) {
             const int c = from + k * lanes + lane;
             float d = c < n ? (u[k].x - hi) - lo : 0.f;
             d *= d;
@@ -306,7 +307,7 @@ __device__ __forceinline__ float4 stat_of(const Joined& j, float eps) {
                        1.f / sqrtf((float)(j.var + (double)eps)), 0.f);
 }
 
-// A wave joins the chunks of a group of an item.
+// A wave joins the chunks of a group of an item (16 a lane: a large map's 1023 at once).
 __global__ __launch_bounds__(kThreads) void group_join_kernel(GroupArgs a, ItemTable chunk,
                                                               int ty,
                                                               const float2* __restrict__ partial,
@@ -315,7 +316,7 @@ __global__ __launch_bounds__(kThreads) void group_join_kernel(GroupArgs a, ItemT
     if (at >= (int64_t)a.batch * a.groups) return;
     const int b = (int)(at / a.groups), g = (int)(at % a.groups), lane = threadIdx.x & 63;
     const int first = chunk.start[b];
-    const Joined j = join_chunks(partial + (int64_t)g * chunk.start[a.batch] + first,
+    const Joined j = join_chunks<16>(partial + (int64_t)g * chunk.start[a.batch] + first,
                                  chunk.start[b + 1] - first, lane, 64,
                                  a.items.start[b + 1] - a.items.start[b], ty,
                                  a.channels / a.groups);
@@ -336,7 +337,8 @@ __device__ __forceinline__ void join_here(const GroupArgs& a, const ItemTable& c
     for (int g0 = 0; g0 < groups; g0 += kThreads / lanes) {
         const int g = g0 + threadIdx.x / lanes;
         const bool on = g < groups;
-        const Joined j = join_chunks(
+        // (12: with 16 the apply kernel spills registers)
+        const Joined j = join_chunks<12>(
             partial + (int64_t)(group0 + (on ? g : 0)) * chunk.start[a.batch] + first, n, lane,
             lanes, a.items.start[b + 1] - a.items.start[b], ty, a.channels / a.groups);
         if (on && lane == 0) {
@@ -362,8 +364,9 @@ __device__ __forceinline__ uint4 load16(const char* p) {
 // out = act((x - hi) k + o) with k = rstd w and o = b - lo k. Rows run last to
 // first: what the statistics read last is still in the caches. `Past`:
 // a map larger than those is loaded past them here, so that what was just read
-// does not drive out what was read before and is wanted next (269 us for 310
-// where x has 537 MB; 168 for 163 with the gradient where it has 102 MB).
+// does not drive out what was read before and is wanted next (265 us with it and
+// 286 without where x has 537 MB; 161 and 156, the gradient after it, where x has
+// 102 MB).
 // `Here`: the workgroup joins its item's chunks itself.
 template <typename T, int Act, bool Whole, bool Past, bool Here>
 __global__ __launch_bounds__(kThreads, 4) void group_apply_kernel(
@@ -725,10 +728,11 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
 // Items whose slice of channels fits a workgroup's registers take one launch: a
 // workgroup holds the slice of all of an item's rows between the sums and their
 // use, so the data is read once and the statistics are about the exact mean.
-// What it saves is a launch or two on the host: 12 us for 14.5 and, with the
-// gradient's three, 13 for 18.5 (256 rows of 256 to 1024 channels). More than a
-// workgroup a CU, or longer items, and it is the slower: 18.5 us for 24 (1000
-// rows of 256, bf16, the gradient), 36 for 51 (64 items of 64 rows of 1024).
+// What it saves is a launch or two on the host: 12 us where the chunks' kernels
+// take 14.5 and, of the gradient, 13 where they take 18.5 (256 rows of 256 to 1024
+// channels). With more than a workgroup a CU, or longer items, it is the slower:
+// 24 us where they take 18.5 (1000 rows of 256, bf16, the gradient), 51 for their
+// 36 (64 items of 64 rows of 1024).
 constexpr int kSmallThreads = 1024;
 
 // Vectors that a thread holds: 32 elements.
@@ -963,8 +967,9 @@ __global__ __launch_bounds__(kSmallThreads) void group_small_backward_kernel(
 
 // ----------------------------------------------------------------- launch ---
 // Whether the second kernel's workgroups join their item's chunks, of `bytes`
-// each, themselves: what they read for it, all together, against a launch of 4 us
-// (a map of 4096 rows in 32 chunks of 32 groups: a quarter of a megabyte).
+// each, themselves: what they read for it, all together, against a launch of 4 us.
+// (4096 rows of 512 channels: 16.7 us for the gradient, 19 with a launch of its own.
+// A map cut into all of 1023 chunks is 16 times over the bound and more.)
 bool join_in_apply(const GroupArgs& a, const GroupPlan& p, size_t bytes) {
     int64_t pairs = 0;
     for (int b = 0; b < a.batch; ++b) {
@@ -1085,8 +1090,9 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // Chunks of at least 4 rows a thread, for at most 4 workgroups a CU, all of them
 // running at once. A map that does not fill those is cut into slices of whole
 // groups, the narrowest of whole cache lines (8 vectors), so that it has fewer
-// chunks to join: 11 + 5 us for 8 + 5 where 4096 rows have 512 channels. A larger
-// map is read in whole rows (265 us for 335 where 262,144 rows have 1024).
+// chunks to join: 15.9 us and the gradient 17.9, in whole rows 16.4 and 20.5, where
+// 4096 rows have 512 channels. A larger map is read in whole rows: 265 us, in slices
+// 319, where 262,144 rows have 1024.
 GroupPlan group_norm_plan(const GroupArgs& a, p3d_dtype dt) {
     GroupPlan p;
     const int unit = dt == P3D_BF16 ? 8 : 4;
@@ -1112,8 +1118,8 @@ GroupPlan group_norm_plan(const GroupArgs& a, p3d_dtype dt) {
     const int64_t rows = std::max<int64_t>((n + most - 1) / most, 4 * lay.ty);
     p.ty = lay.ty;
     // (Odd numbers of chunks: workgroups go round 8 dies, and of an even number a
-    // die would come back to the same memory channels in every round: 320 us for
-    // 263 where 262,144 rows have 1024 channels.)
+    // die would come back to the same memory channels in every round: 320 us, not
+    // 263, where 262,144 rows have 1024 channels.)
     int32_t at = 0;
     for (int b = 0; b < a.batch; ++b) {
         p.chunk.start[b] = at;
