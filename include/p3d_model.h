@@ -53,7 +53,9 @@ typedef enum p3d_act {
  *   Alignment: 16 bytes (mean, rstd: 4).
  *   workspace    p3d_group_norm_workspace_size(desc) bytes, for the forward
  *                call and the gradient alike
- * A value that is not finite makes its item's group NaN.
+ * No result overlaps another tensor of the call (out in place apart).
+ * A value that is not finite makes its item's group NaN. (Squared deviations
+ * are binary32: values beyond 2^40 may end as one that is not finite would.)
  * --------------------------------------------------------------------- */
 typedef struct p3d_group_desc {
     int64_t n;                  /* rows */
@@ -82,7 +84,8 @@ p3d_status p3d_group_norm(const p3d_group_desc* desc, const void* x, int64_t x_s
  *   dx             [n, C] of dtype; may be dout or x (with that tensor's
  *                  stride) and must not overlap them otherwise
  *   dweight, dbias float [C], each NULL where it is not wanted; overwritten,
- *                  0 where there are no rows */
+ *                  0 where there are no rows
+ * No result overlaps another tensor of the call (dx in place apart). */
 p3d_status p3d_group_norm_backward(const p3d_group_desc* desc, const void* dout,
                                    int64_t dout_stride, const void* x, int64_t x_stride,
                                    const float* mean, const float* rstd, void* dx,
@@ -104,7 +107,8 @@ p3d_status p3d_group_norm_backward(const p3d_group_desc* desc, const void* dout,
  *   x            [n, K], rows x_stride (>= K, a multiple of 8 / 4) apart
  *   q            int8 [n, K], rows q_stride (>= K, a multiple of 16) apart
  *   scale        float [n]
- *   Alignment: 16 bytes (scale: 4). q and scale must not overlap x.
+ *   Alignment: 16 bytes (scale: 4). q and scale must not overlap each other
+ *   or x.
  * --------------------------------------------------------------------- */
 p3d_status p3d_quantize_rows(const void* x, p3d_dtype dtype, int64_t n, int32_t width,
                              int64_t x_stride, int8_t* q, int64_t q_stride, float* scale,
@@ -193,7 +197,7 @@ p3d_status p3d_linear_i8(const p3d_linear_i8_desc* desc, const int8_t* q, int64_
  *                kernel arguments, 64 tensors a launch
  *   tensors      size >= 0 elements each, below 2^34; no two tensors of the
  *                table, nor two parts of one, may overlap in what a step
- *                writes, nor overlap a gradient
+ *                writes, nor overlap a gradient or a device scalar
  *   lr           finite, >= 0; beta1, beta2 in [0, 1); eps finite, > 0;
  *   step         >= 1 (its value is used without device_step)
  *   weight_decay finite, per tensor
@@ -232,7 +236,7 @@ p3d_status p3d_adamw(const p3d_adamw_desc* desc, void* stream);
  *   out[0] = norm = sqrt(sum of squares)   (summed in binary64)
  *   out[1] = norm > max_norm ? max_norm / norm : 1;  NaN where the norm is not
  *            finite, so that the step is left out
- * out: DEVICE float [2]. Of desc, count, grad_dtype and the tensors' grad and
+ * out: DEVICE float [2], no part of a gradient. Of desc, count, grad_dtype and the tensors' grad and
  * size are read. max_norm > 0 (infinity: no clipping).
  * workspace: p3d_grad_norm_workspace_size(desc) bytes. */
 size_t p3d_grad_norm_workspace_size(const p3d_adamw_desc* desc);

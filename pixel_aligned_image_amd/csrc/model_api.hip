@@ -2,9 +2,12 @@
 // validation of every argument before anything is enqueued, workspace sizes,
 // and dispatch to the kernels.
 #include <math.h>
+#include <stdio.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "api_checks.h"
@@ -42,6 +45,47 @@ p3d_status check_pitch(const char* fn, const char* name, int64_t stride, int64_t
 }
 
 constexpr int64_t kMaxStride = int64_t(1) << 30;
+
+Rows line(const char* name, const void* base, int64_t bytes) {
+    return {name, base, bytes > 0 ? 1 : 0, bytes, bytes};
+}
+
+// Whether two tensors share a byte, whatever their strides. A tensor without gaps
+// counts as one row, which overlap() decides against any; rows with gaps that are
+// differently far apart are gone through one by one.
+bool meet(Rows a, Rows b) {
+    for (Rows* t : {&a, &b}) {
+        if (!t->base || t->rows == 0) return false;
+        if (t->pitch == t->width) *t = line(t->name, t->base, t->rows * t->width);
+    }
+    if (a.rows == 1 || b.rows == 1 || a.pitch == b.pitch) return overlap(a, b);
+    const auto end = [](const Rows& t) {
+        return static_cast<const char*>(t.base) + (t.rows - 1) * t.pitch + t.width;
+    };
+    if (end(a) <= b.base || end(b) <= a.base) return false;
+    if (a.rows > b.rows) std::swap(a, b);
+    Rows row{a.name, a.base, 1, a.width, a.width};
+    for (int64_t i = 0; i < a.rows; ++i) {
+        row.base = static_cast<const char*>(a.base) + i * a.pitch;
+        if (row_meets(row, b)) return true;
+    }
+    return false;
+}
+
+// Results share nothing with each other or with what the call reads.
+p3d_status check_results(const char* fn, std::initializer_list<Rows> written,
+                         std::initializer_list<Rows> read) {
+    for (const Rows* w = written.begin(); w != written.end(); ++w) {
+        const auto refuse = [&](const Rows& other) {
+            return meet(*w, other) ? set_error(P3D_ERR_INVALID_ARG, "%s: %s must not overlap %s",
+                                               fn, w->name, other.name)
+                                   : P3D_OK;
+        };
+        for (const Rows* o = w + 1; o != written.end(); ++o) P3D_TRY(refuse(*o));
+        for (const Rows& o : read) P3D_TRY(refuse(o));
+    }
+    return P3D_OK;
+}
 
 // ------------------------------------------------------------- group norm ---
 p3d_status check_group(const char* fn, const p3d_group_desc* d, GroupArgs* a) {
@@ -85,7 +129,7 @@ p3d_status check_in_place(const char* fn, const Rows& out, const Rows& in) {
     if (out.base && out.base == in.base && out.rows > 0)
         return set_error(P3D_ERR_SHAPE, "%s: in place, the strides of %s and %s must be equal", fn,
                          out.name, in.name);
-    return check_apart(fn, out, in);
+    return check_results(fn, {out}, {in});
 }
 
 // ----------------------------------------------------------------- linear ---
@@ -102,6 +146,11 @@ struct Span {
     int32_t tensor;
     const char* name;
     bool written;
+    // "tensors[3].m", or the name alone of what belongs to none
+    void word(char (&to)[64]) const {
+        if (tensor < 0) snprintf(to, sizeof to, "%s", name);
+        else snprintf(to, sizeof to, "tensors[%d].%s", tensor, name);
+    }
 };
 
 p3d_status check_table(const char* fn, const p3d_adamw_desc* d, bool step) {
@@ -168,10 +217,15 @@ p3d_status check_table(const char* fn, const p3d_adamw_desc* d, bool step) {
     return P3D_OK;
 }
 
-// Whether nothing that a step writes is written twice or read as a gradient.
+// Whether nothing that a step writes is written twice or read as anything else.
 p3d_status check_spans(const char* fn, const p3d_adamw_desc* d) {
     std::vector<Span> spans;
-    spans.reserve((size_t)d->count * 7);
+    spans.reserve((size_t)d->count * 7 + 3);
+    for (const auto& [name, base] : {std::pair<const char*, const void*>{"grad_scale", d->grad_scale},
+                                     {"device_lr", d->device_lr}, {"device_step", d->device_step}}) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(base);
+        if (base) spans.push_back({at, at + 4, -1, name, false});
+    }
     const int p = d->param_dtype == P3D_BF16 ? 2 : 4, g = d->grad_dtype == P3D_BF16 ? 2 : 4;
     const int state = d->state_bits / 8;
     for (int32_t j = 0; j < d->count; ++j) {
@@ -196,9 +250,12 @@ p3d_status check_spans(const char* fn, const p3d_adamw_desc* d) {
     const Span *all = nullptr, *written = nullptr;
     for (const Span& s : spans) {
         const Span* other = s.written ? all : written;
-        if (other && other->to > s.from)
-            return set_error(P3D_ERR_INVALID_ARG, "%s: tensors[%d].%s must not overlap "
-                             "tensors[%d].%s", fn, s.tensor, s.name, other->tensor, other->name);
+        if (other && other->to > s.from) {
+            char a[64], b[64];
+            s.word(a);
+            other->word(b);
+            return set_error(P3D_ERR_INVALID_ARG, "%s: %s must not overlap %s", fn, a, b);
+        }
         if (!all || s.to > all->to) all = &s;
         if (s.written && (!written || s.to > written->to)) written = &s;
     }
@@ -234,11 +291,15 @@ p3d_status p3d_group_norm(const p3d_group_desc* desc, const void* x, int64_t x_s
     P3D_TRY(check_pitch(fn, "out_stride", out_stride, a.channels, unit, kMaxStride));
     P3D_TRY(check_tensor(fn, "mean", mean, false, 4));
     P3D_TRY(check_tensor(fn, "rstd", rstd, false, 4));
-    if (mean && mean == rstd)
-        return set_error(P3D_ERR_INVALID_ARG, "%s: mean and rstd must be different tensors", fn);
-    const int64_t width = (int64_t)a.channels * e;
-    P3D_TRY(check_in_place(fn, {"out", out, desc->n, width, out_stride * e},
-                           {"x", x, desc->n, width, x_stride * e}));
+    const int64_t width = (int64_t)a.channels * e, stats = (int64_t)a.batch * a.groups * 4;
+    const Rows to{"out", out, desc->n, width, out_stride * e},
+        from{"x", x, desc->n, width, x_stride * e}, m = line("mean", mean, stats),
+        r = line("rstd", rstd, stats), w = line("weight", a.weight, width),
+        b = line("bias", a.bias, width);
+    P3D_TRY(check_in_place(fn, to, from));
+    P3D_TRY(check_results(fn, {to, m, r}, {w, b}));
+    P3D_TRY(check_results(fn, {m}, {from}));
+    P3D_TRY(check_results(fn, {r}, {from}));
     const GroupPlan plan = group_norm_plan(a, desc->dtype);
     P3D_TRY(check_workspace(fn, "p3d_group_norm_workspace_size", workspace, workspace_bytes,
                             plan.bytes));
@@ -273,13 +334,19 @@ p3d_status p3d_group_norm_backward(const p3d_group_desc* desc, const void* dout,
     P3D_TRY(check_pitch(fn, "dx_stride", dx_stride, a.channels, unit, kMaxStride));
     P3D_TRY(check_tensor(fn, "dweight", dweight, false, 4));
     P3D_TRY(check_tensor(fn, "dbias", dbias, false, 4));
-    if (dweight && dweight == dbias)
-        return set_error(P3D_ERR_INVALID_ARG, "%s: dweight and dbias must be different tensors",
-                         fn);
-    const int64_t width = (int64_t)a.channels * e;
-    const Rows to{"dx", dx, desc->n, width, dx_stride * e};
-    P3D_TRY(check_in_place(fn, to, {"dout", dout, desc->n, width, dout_stride * e}));
-    P3D_TRY(check_in_place(fn, to, {"x", x, desc->n, width, x_stride * e}));
+    const int64_t width = (int64_t)a.channels * e, stats = (int64_t)a.batch * a.groups * 4,
+                  sums = (int64_t)a.channels * 4;
+    const Rows to{"dx", dx, desc->n, width, dx_stride * e},
+        grad{"dout", dout, desc->n, width, dout_stride * e},
+        from{"x", x, desc->n, width, x_stride * e}, m = line("mean", mean, stats),
+        r = line("rstd", rstd, stats), w = line("weight", a.weight, width),
+        b = line("bias", a.bias, width), dw = line("dweight", dweight, sums),
+        db = line("dbias", dbias, sums);
+    P3D_TRY(check_in_place(fn, to, grad));
+    P3D_TRY(check_in_place(fn, to, from));
+    P3D_TRY(check_results(fn, {to, dw, db}, {m, r, w, b}));
+    P3D_TRY(check_results(fn, {dw}, {grad, from}));
+    P3D_TRY(check_results(fn, {db}, {grad, from}));
     const GroupPlan plan = group_norm_plan(a, desc->dtype);
     P3D_TRY(check_workspace(fn, "p3d_group_norm_workspace_size", workspace, workspace_bytes,
                             plan.bytes));
@@ -311,11 +378,8 @@ p3d_status p3d_quantize_rows(const void* x, p3d_dtype dtype, int64_t n, int32_t 
     P3D_TRY(check_tensor(fn, "scale", scale, n > 0, 4));
     P3D_TRY(check_pitch(fn, "x_stride", x_stride, width, unit, kMaxStride));
     P3D_TRY(check_pitch(fn, "q_stride", q_stride, width, 16, kMaxStride));
-    const Rows in{"x", x, n, (int64_t)width * e, x_stride * e}, out{"q", q, n, width, q_stride},
-        by{"scale", scale, n, 4, 4};
-    P3D_TRY(check_apart(fn, out, in));
-    P3D_TRY(check_apart(fn, by, in));
-    P3D_TRY(check_apart(fn, by, out));
+    P3D_TRY(check_results(fn, {{"q", q, n, width, q_stride}, line("scale", scale, n * 4)},
+                          {{"x", x, n, (int64_t)width * e, x_stride * e}}));
     if (n == 0) return set_ok();
     QuantizeArgs a{x, n, x_stride, q_stride, width, q, scale};
     const hipError_t er = launch_quantize_rows(a, dtype, static_cast<hipStream_t>(stream));
@@ -356,11 +420,11 @@ p3d_status p3d_linear_i8(const p3d_linear_i8_desc* desc, const int8_t* q, int64_
     if (residual)
         P3D_TRY(check_pitch(fn, "residual_stride", residual_stride, d, unit, kMaxStride));
     const Rows to{"out", out, n, d * e, out_stride * e};
-    P3D_TRY(check_apart(fn, to, {"q", q, n, k, q_stride}));
-    P3D_TRY(check_apart(fn, to, {"weight", desc->weight, 1, d * k, d * k}));
-    P3D_TRY(check_apart(fn, to, {"scale", scale, n, 4, 4}));
-    P3D_TRY(check_apart(fn, to, {"weight_scale", desc->weight_scale, 1, d * 4, d * 4}));
-    if (desc->bias) P3D_TRY(check_apart(fn, to, {"bias", desc->bias, 1, d * e, d * e}));
+    P3D_TRY(check_results(fn, {to},
+                          {{"q", q, n, k, q_stride}, line("weight", desc->weight, d * k),
+                           line("scale", scale, n * 4),
+                           line("weight_scale", desc->weight_scale, d * 4),
+                           line("bias", desc->bias, d * e)}));
     if (residual)
         P3D_TRY(check_in_place(fn, to, {"residual", residual, n, d * e, residual_stride * e}));
     if (n == 0) return set_ok();
@@ -426,6 +490,10 @@ p3d_status p3d_grad_norm(const p3d_adamw_desc* desc, float max_norm, float* out,
         return set_error(P3D_ERR_INVALID_ARG, "%s: max_norm must be > 0, got %g", fn,
                          (double)max_norm);
     P3D_TRY(check_tensor(fn, "out", out, true, 4));
+    const int64_t e = desc->grad_dtype == P3D_BF16 ? 2 : 4;
+    for (int32_t j = 0; j < desc->count; ++j)
+        if (meet(line("out", out, 8), line("grad", desc->tensors[j].grad, desc->tensors[j].size * e)))
+            return set_error(P3D_ERR_INVALID_ARG, "%s: out must not overlap tensors[%d].grad", fn, j);
     P3D_TRY(check_workspace(fn, "p3d_grad_norm_workspace_size", workspace, workspace_bytes,
                             grad_norm_bytes(*desc)));
     const hipError_t er = launch_grad_norm(*desc, max_norm, out, static_cast<double*>(workspace),

@@ -84,7 +84,7 @@ def test_group_offsets(p3d):
 
 
 def test_group_tensor_checks(p3d):
-    d = group(p3d)
+    d = group(p3d, bias=FAKE + 4096)
     X, O, W = FAKE, FAKE + MB, FAKE + 2 * MB
 
     def forward(want, needle, x=X, xs=64, out=O, os=64, mean=None, rstd=None, ws=W, size=MB):
@@ -100,7 +100,7 @@ def test_group_tensor_checks(p3d):
     forward(UNSUPPORTED, "out_stride", os=(1 << 30) + 8)
     forward(UNSUPPORTED, "mean", mean=FAKE + 2)
     forward(UNSUPPORTED, "rstd", rstd=FAKE + 1)
-    forward(INVALID, "mean and rstd", mean=FAKE, rstd=FAKE)
+    forward(INVALID, "mean must not overlap rstd", mean=FAKE + MB // 2, rstd=FAKE + MB // 2)
     forward(INVALID, "workspace", ws=None)
     forward(INVALID, "workspace", size=16)
     forward(UNSUPPORTED, "256-byte", ws=W + 16)
@@ -124,11 +124,31 @@ def test_group_tensor_checks(p3d):
     backward(UNSUPPORTED, "dx_stride", dxs=70)
     backward(UNSUPPORTED, "dweight", dw=FAKE + 1)
     backward(UNSUPPORTED, "dbias", db=FAKE + 3)
-    backward(INVALID, "dweight and dbias", dw=FAKE, db=FAKE)
+    backward(INVALID, "dweight must not overlap dbias", dw=O + MB // 2, db=O + MB // 2)
     backward(INVALID, "workspace", size=255)
     backward(INVALID, "dx must not overlap dout", dx=X + 128)
     backward(INVALID, "dx must not overlap x", dx=X + MB // 2 + 128)
     backward(SHAPE, "in place", dx=X, dxs=128)
+    # results over what other workgroups still read, or over each other
+    forward(INVALID, "out must not overlap mean", mean=O + 4)
+    forward(INVALID, "out must not overlap weight", out=FAKE - 1024, x=X + 2 * MB)
+    forward(INVALID, "mean must not overlap rstd", mean=O + MB // 2, rstd=O + MB // 2 + 32)
+    forward(INVALID, "mean must not overlap bias", mean=FAKE + 4104, x=X + 2 * MB)
+    forward(INVALID, "rstd must not overlap x", rstd=X + 2 * MB + 200, x=X + 2 * MB, xs=128)
+    backward(INVALID, "dx must not overlap mean", mean=O + 15 * 128 + 124)
+    backward(INVALID, "dx must not overlap weight", dx=FAKE - 1024, x=X + 3 * MB, dout=X + 2 * MB,
+             mean=O, rstd=O)
+    backward(INVALID, "dx must not overlap dbias", db=O + 64, mean=O + MB // 2, rstd=O + MB // 2)
+    backward(INVALID, "dweight must not overlap dbias", dw=W - 512, db=W - 260)
+    backward(INVALID, "dweight must not overlap bias", dw=FAKE + 4096 - 128, x=X + 3 * MB, dout=X + 2 * MB,
+             mean=O + MB // 2, rstd=O + MB // 2)
+    backward(INVALID, "dweight must not overlap dout", dw=X + 512, mean=O + MB // 2,
+             rstd=O + MB // 2, x=X + MB // 2)
+    backward(INVALID, "dbias must not overlap x", db=X + MB // 2, mean=O + MB // 2,
+             rstd=O + MB // 2)
+    # rows that are differently far apart: between each other's, and not
+    forward(INVALID, "out must not overlap x", x=O, xs=128, out=O + 3 * 64, os=256)
+    forward(INVALID, "workspace", x=O, xs=256, out=O + 128, os=512, size=16)
     # every item has a mean and an rstd, also one without rows
     d = group(p3d, (0, 0, 0))
     backward(INVALID, "mean is NULL", dout=None, x=None, dx=None, mean=None)
@@ -176,7 +196,12 @@ def test_quantize_checks(p3d):
     call(INVALID, "q must not overlap x", q=X)
     call(INVALID, "q must not overlap x", q=X + 16, n=1)
     call(INVALID, "scale must not overlap x", s=X)
-    call(INVALID, "scale must not overlap q", s=Q)
+    call(INVALID, "scale must not overlap x", s=X + 2044)
+    call(INVALID, "scale must not overlap x", s=X - 4)
+    call(INVALID, "q must not overlap scale", s=Q + 1020)
+    call(INVALID, "q must not overlap x", q=X + 16 * 128 - 16)
+    call(INVALID, "q must not overlap x", q=X + 128 + 64, xs=128, qs=192)
+    call(INVALID, "q must not overlap scale", s=Q)
     assert p3d.lib.p3d_quantize_rows(None, 1, 0, 64, 64, None, 64, None, None) == 0
 
 
@@ -310,6 +335,12 @@ def test_adamw_overlaps(p3d):
     def inside(rows):
         rows[0].size = 4 * MB                # its param passes over its own gradient
     call("must not overlap", inside)
+    # the rate that every workgroup reads, inside what they write
+    for name in ("grad_scale", "device_lr", "device_step"):
+        d = table(p3d)
+        setattr(d, name, FAKE + 16)
+        refused(p3d, p3d.lib.p3d_adamw(d, None), INVALID, "overlap", "p3d_adamw")
+        assert name in p3d.p3d_last_error() and "tensors[0].param" in p3d.p3d_last_error()
     # gradients may be shared: only the size of the step is refused then
     d = table(p3d, step=0)
     d.keep[1].grad = FAKE + MB
@@ -339,6 +370,7 @@ def test_grad_norm_checks(p3d):
         call(INVALID, "max_norm", most=most)
     call(INVALID, "out is NULL", out=None)
     call(UNSUPPORTED, "out must be", out=FAKE + 2)
+    call(INVALID, "out must not overlap tensors[1].grad", out=table(p3d).keep[1].grad - 4)
     call(INVALID, "workspace", ws=None)
     call(INVALID, "workspace", size=8)
     call(UNSUPPORTED, "256-byte", ws=FAKE + 16)
