@@ -186,7 +186,9 @@ p3d_status p3d_linear_i8(const p3d_linear_i8_desc* desc, const int8_t* q, int64_
  *                x = mix(low(i) * 0x9E3779B1 ^ high(i) * 0xDDB3D743 ^ key)
  *              are x's low half for m and its high half for v: a number with
  *              20 mantissa bits to drop gets the 16 bits added into the upper
- *              ones of those. A step needs a seed of its own.
+ *              ones of those. A step needs a seed of its own: with a
+ *              device_step, the step's number is added to `seed` first, so that
+ *              a captured graph's replays have theirs.
  * grad_scale   DEVICE float or NULL (1). Where it is not finite the whole
  *              step is left out: nothing is written.
  * device_lr, device_step: DEVICE float / int32, or NULL; read by the kernels

@@ -36,7 +36,8 @@ struct Entry {
     void *m, *v;
     float *m_scale, *v_scale;
     int64_t size;
-    uint32_t key;               // of the tensor's random bits
+    uint32_t key;               // of the tensor's random bits, or its number's share of it where
+                                // t is the device's
     float keep;                 // 1 - lr decay, or decay where lr is the device's
 };
 
@@ -48,6 +49,7 @@ struct Step {
     int32_t count;
     double lr, log_b1, log_b2;  // (log2) where lr or t are the device's
     int64_t t;
+    uint64_t seed;
     const float* grad_scale;
     const float* device_lr;
     const int32_t* device_step;
@@ -73,6 +75,11 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
     x ^= x >> 13;
     x *= 0xDDB3D743u;
     return x ^ (x >> 16);
+}
+
+// What a call's seed gives to its tensors' keys.
+__host__ __device__ __forceinline__ uint32_t seed_key(uint64_t seed) {
+    return mix((uint32_t)seed) ^ (uint32_t)(seed >> 32);
 }
 
 // ------------------------------------------------- vectors of 8 elements ---
@@ -220,6 +227,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table table, Step s) {
     const int at = tensor_of(table, s.count, blockIdx.x);
     const Entry& t = table.e[at];
     float keep = t.keep;
+    uint32_t key = t.key;
     if (s.device_lr || s.device_step) {
         // (1 - b^t with t log2 b: binary64 leaves 1 - 0.999 its 13 digits)
         const double lr = s.device_lr ? (double)*s.device_lr : s.lr;
@@ -228,6 +236,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table table, Step s) {
         keep = (float)(1. - lr * (double)t.keep);
         s.rate = (float)(lr / (1. - exp2((double)n * s.log_b1)));
         s.norm = (float)(1. / sqrt(1. - exp2((double)n * s.log_b2)));
+        if (Bits == 8 && s.device_step) key = mix(key ^ seed_key(s.seed + (uint64_t)n));
     }
     const int64_t i = (int64_t)(blockIdx.x - table.first[at]) * kChunk + threadIdx.x * kPer;
     const int64_t left = t.size - i;
@@ -297,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table table, Step s) {
         block_scale(half_max(tv), sv, bv);
         uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
         const uint32_t base = (uint32_t)i * 0x9E3779B1u;
-        const uint32_t high = (uint32_t)((uint64_t)i >> 32) * 0xDDB3D743u ^ t.key;
+        const uint32_t high = (uint32_t)((uint64_t)i >> 32) * 0xDDB3D743u ^ key;
         const auto one = [&](auto at) {
             constexpr int e = decltype(at)::value;
             const uint32_t bits = mix((base + e * 0x9E3779B1u) ^ high);
@@ -422,7 +431,7 @@ hipError_t in_launches(const p3d_adamw_desc& d, int64_t chunk, Run run) {
         chunks = 0;
         return e;
     };
-    const uint32_t key = mix((uint32_t)d.seed) ^ (uint32_t)(d.seed >> 32);
+    const uint32_t key = seed_key(d.seed);
     for (int32_t j = 0; j < d.count; ++j) {
         const p3d_adamw_tensor& x = d.tensors[j];
         if (x.size == 0) continue;
@@ -441,7 +450,8 @@ hipError_t in_launches(const p3d_adamw_desc& d, int64_t chunk, Run run) {
         to.m_scale = x.m_scale;
         to.v_scale = x.v_scale;
         to.size = x.size;
-        to.key = mix((uint32_t)j * 0x9E3779B1u ^ key);
+        to.key = (uint32_t)j * 0x9E3779B1u;
+        if (!d.device_step) to.key = mix(to.key ^ key);
         to.keep = d.device_lr || d.device_step ? x.weight_decay
                                                : (float)(1. - d.lr * (double)x.weight_decay);
         chunks += more;
@@ -515,6 +525,7 @@ hipError_t launch_adamw(const p3d_adamw_desc& d, hipStream_t s) {
     step.log_b1 = std::log2(d.beta1);
     step.log_b2 = std::log2(d.beta2);
     step.t = d.step;
+    step.seed = d.seed;
     step.grad_scale = d.grad_scale;
     step.device_lr = d.device_lr;
     step.device_step = d.device_step;

@@ -248,8 +248,9 @@ def make_adamw_tensors(params, grads, m, v, masters=None, m_scales=None, v_scale
     params: float32 or bfloat16; grads: likewise; m, v: float32, or 8-bit
     (torch.float8_e4m3fn or uint8) with float32 m_scales and v_scales of
     (size + 255) // 256; masters: float32 copies of bfloat16 params, or None;
-    weight_decay: a number or one for each. The table keeps the tensors: a
-    gradient in another tensor needs another table."""
+    weight_decay: a number or one for each. The table keeps the memory
+    that the tensors have now: a gradient in another tensor, or a parameter whose
+    .data was replaced, needs another table."""
     params, grads, m, v = list(params), list(grads), list(m), list(v)
     n = len(params)
     lists = [("grads", grads), ("m", m), ("v", v)]
@@ -286,8 +287,9 @@ def make_adamw_tensors(params, grads, m, v, masters=None, m_scales=None, v_scale
             to.m_scale = _flat(m_scales[j], "m_scales[%d]" % j, f, dev, blocks)
             to.v_scale = _flat(v_scales[j], "v_scales[%d]" % j, f, dev, blocks)
         to.size, to.weight_decay = size, decay[j]
-    table = AdamWTensors(params + grads + m + v + (masters or []) + (m_scales or [])
-                         + (v_scales or []))
+    # (aliases: a parameter whose .data is replaced leaves the old memory)
+    table = AdamWTensors(t.detach() for t in params + grads + m + v + (masters or [])
+                         + (m_scales or []) + (v_scales or []))
     table.rows, table.count, table.bits = rows, n, bits
     table.param_dtype, table.grad_dtype = _core._DT[pt], _core._DT[gt]
     table.index = dev
@@ -311,9 +313,9 @@ def p3d_adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0, gra
     """Enqueue p3d_adamw: step `step` (from 1 on) on a table of
     make_adamw_tensors. grad_scale: float32 device tensor of one element (the
     second of p3d_grad_norm's result) or None; seed: of the random bits that
-    8-bit states are rounded by, another for every step; device_lr, device_step:
-    float32 / int32 device tensors of one element that are read instead of lr
-    and step when the work runs, or None."""
+    8-bit states are rounded by, another for every step (a device_step is added
+    to it); device_lr, device_step: float32 / int32 device tensors of one element
+    that are read instead of lr and step when the work runs, or None."""
     dev, d = _adamw(tensors)
     d.lr, d.beta1, d.beta2, d.eps, d.step = lr, beta1, beta2, eps, step
     d.seed = seed & 0xffffffffffffffff

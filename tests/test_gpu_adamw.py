@@ -223,7 +223,8 @@ def test_step_and_rate_on_the_device(bits):
     for step, lr in ((1, 1e-2), (2, 5e-3), (1000, 1e-4)):
         hyper = dict(lr=float(torch.tensor(lr)), beta1=0.9, beta2=0.999, eps=1e-8)
         p3d.p3d_adamw(a.table, step=step, seed=step, **hyper)
-        p3d.p3d_adamw(b.table, step=77, seed=step, **{**hyper, "lr": 3.0},
+        # (the device's step is added to the seed)
+        p3d.p3d_adamw(b.table, step=77, seed=0, **{**hyper, "lr": 3.0},
                       device_lr=torch.tensor([lr], device="cuda"),
                       device_step=torch.tensor([step], dtype=torch.int32, device="cuda"))
         for x, y in zip(a.table, b.table):
@@ -234,6 +235,37 @@ def test_step_and_rate_on_the_device(bits):
     p3d.p3d_adamw(d.table, step=5, **HYPER,
                   device_step=torch.tensor([0], dtype=torch.int32, device="cuda"))
     assert torch.allclose(c.w[0], d.w[0], rtol=1e-6)
+
+
+def test_a_table_keeps_the_memory_it_was_made_of():
+    p = torch.nn.Parameter(torch.ones(5000, device="cuda"))
+    g, m, v = (torch.ones(5000, device="cuda") for _ in range(3))
+    table, old = p3d.make_adamw_tensors([p], [g], [m], [v]), p.data_ptr()
+    p.data = torch.ones(5000, device="cuda")
+    others = [torch.zeros(5000, device="cuda") for _ in range(8)]   # none of them the old one
+    p3d.p3d_adamw(table, step=1, **HYPER)
+    assert table[0].data_ptr() == old and bool((table[0] < 1).all())
+    assert bool((p == 1).all()) and all(bool((x == 0).all()) for x in others)
+
+
+def test_replays_of_a_captured_step_round_by_bits_of_their_own():
+    """8-bit states in a graph: every replay is the call with the step's number
+    added to the seed, over 2^32 as well."""
+    a, b = Model(SIZES, "bf16", "f32", True, 8, 8), Model(SIZES, "bf16", "f32", True, 8, 8)
+    seed, step = 2 ** 32 - 3, torch.zeros(1, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step += 1
+        p3d.p3d_adamw(b.table, step=1, seed=seed, device_step=step, **HYPER)
+    for t in (1, 2, 3, 4):
+        graph.replay()
+        p3d.p3d_adamw(a.table, step=t, seed=seed + t, **HYPER)
+        torch.cuda.synchronize()
+        assert int(step) == t
+        for x, y in zip(a.m + a.v, b.m + b.v):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
 
 
 def test_eight_bit_states_keep_their_mean():
