@@ -980,8 +980,10 @@ bool join_in_apply(const GroupArgs& a, const GroupPlan& p, size_t bytes) {
     return pairs * (int64_t)bytes <= (int64_t(16) << 20);
 }
 
-// x of more bytes than this is loaded past the caches in its second pass.
-constexpr int64_t kPast = int64_t(200) << 20;
+// Whether x is so large that its second pass loads it past the caches.
+bool is_past(const GroupArgs& a, int unit) {
+    return (int64_t)a.items.start[a.batch] * a.channels * (16 / unit) > int64_t(200) << 20;
+}
 
 template <typename T, bool Whole>
 hipError_t forward_of(const GroupArgs& a, const GroupPlan& p, float2* partial, float4* stat,
@@ -1013,7 +1015,7 @@ hipError_t forward_of(const GroupArgs& a, const GroupPlan& p, float2* partial, f
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !chunks) return e;
     }
-    const bool past = (int64_t)a.items.start[a.batch] * a.channels * (16 / Vec<T>::N) > kPast;
+    const bool past = is_past(a, Vec<T>::N);
     return with_act([&](auto act) {
         constexpr int A = decltype(act)::value;
         const size_t lds = here ? a.groups / p.slices * sizeof(float4) : 0;
@@ -1091,17 +1093,22 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // running at once. A map that does not fill those is cut into slices of whole
 // groups, the narrowest of whole cache lines (8 vectors), so that it has fewer
 // chunks to join: 15.9 us and the gradient 17.9, in whole rows 16.4 and 20.5, where
-// 4096 rows have 512 channels. A larger map is read in whole rows: 265 us, in slices
-// 319, where 262,144 rows have 1024.
+// 4096 rows have 512 channels of bf16. One that the caches hold is cut as far as 512
+// bytes a row: 24 and 31 us, in whole rows 24 and 42.5, where 8192 rows have 2048. A
+// larger one is read in whole rows: 265 us where 262,144 rows have 1024, 283 so cut
+// and 319 in the narrowest slices.
 GroupPlan group_norm_plan(const GroupArgs& a, p3d_dtype dt) {
     GroupPlan p;
     const int unit = dt == P3D_BF16 ? 8 : 4;
     const int64_t most = 4 * kComputeUnits;
+    const int64_t n = a.items.start[a.batch];
+    const int narrow = n < most * 4 * Lay(a.channels / unit).ty ? 8
+                       : is_past(a, unit)                       ? a.channels
+                                                                : 32;
     p.slices = 1;
-    if (a.items.start[a.batch] < most * 4 * Lay(a.channels / unit).ty)
-        for (int d = 2; d <= a.groups; ++d)
-            if (a.groups % d == 0 && a.channels / d % unit == 0 && a.channels / d / unit >= 8)
-                p.slices = d;
+    for (int d = 2; d <= a.groups; ++d)
+        if (a.groups % d == 0 && a.channels / d % unit == 0 && a.channels / d / unit >= narrow)
+            p.slices = d;
     // The small items' kernels: a workgroup a CU at most, slices as above, every
     // item's rows in the threads' registers.
     p.small = 0;
@@ -1114,8 +1121,7 @@ GroupPlan group_norm_plan(const GroupArgs& a, p3d_dtype dt) {
             if (longest <= (int64_t)32 / unit * SmallLay(a.channels / d / unit).ty) p.small = d;
         }
     const Lay lay(a.channels / unit / p.slices);
-    const int64_t n = a.items.start[a.batch] * (int64_t)p.slices;
-    const int64_t rows = std::max<int64_t>((n + most - 1) / most, 4 * lay.ty);
+    const int64_t rows = std::max<int64_t>((n * p.slices + most - 1) / most, 4 * lay.ty);
     p.ty = lay.ty;
     // (Odd numbers of chunks: workgroups go round 8 dies, and of an even number a
     // die would come back to the same memory channels in every round: 320 us, not
