@@ -5,7 +5,9 @@
 //   w = w (1 - lr decay) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
 // One pass over the data: memory bound at 28 bytes an element (binary32
-// weights and states) down to 10 (bf16 weights, 8-bit states). The tensors'
+// weights and states) down to 10 (bf16 weights, 8-bit states): 231 us for 44
+// million elements of 28 bytes, 5.4 TB/s, and 166 us for 89 million of 10, 5.3;
+// the norm of 89 million bf16 gradients takes 30 us, 5.9 TB/s. The tensors'
 // table travels in the kernel arguments, kTensors a launch; a workgroup takes
 // one chunk of one tensor, found by a search over the chunks' first numbers,
 // so that a launch over many small tensors fills the chip as a large one does.
@@ -494,7 +496,8 @@ int64_t grad_norm_parts(const p3d_adamw_desc& d) {
 hipError_t launch_grad_norm(const p3d_adamw_desc& d, float max_norm, float* out, double* parts,
                             hipStream_t s) {
     int64_t at = 0;
-    const hipError_t e = in_launches(d, norm_chunk(d.grad_dtype), [&](const Table& t, int count, int64_t chunks) {
+    const int64_t chunk = norm_chunk(d.grad_dtype);
+    const hipError_t e = in_launches(d, chunk, [&](const Table& t, int count, int64_t chunks) {
         const int64_t grid = std::min(chunks, kNormGrid);
         if (d.grad_dtype == P3D_BF16)
             norm_parts_kernel<Bf16>

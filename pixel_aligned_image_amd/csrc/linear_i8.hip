@@ -9,7 +9,10 @@
 // results are neighbouring features of one token. K advances in stages of 64
 // integers, four of them in LDS: while one is multiplied the next has arrived
 // and two more are on their way, which covers the memory's latency with one
-// workgroup on a CU.
+// workgroup on a CU. Measured: 100,000 x 2048 x 1536 in 342 us, 1.84 PFLOP/s,
+// 12,289 x 1536 x 6144 with GELU in 137 us, 1.69 (a library's bare product: 1.72
+// to 1.83 and 1.52 to 1.61). Under this load the clock drops to about 1.6 GHz: the
+// matrix cores' power bounds it, and instructions saved elsewhere no longer show.
 #include <algorithm>
 #include <type_traits>
 
@@ -340,7 +343,9 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
 // -------------------------------------------------------------- few tokens ---
 // At most 16 B tokens: the weights are the traffic. 16 features a workgroup,
 // its 8 waves a part of K each, fragments straight from memory (a weight is
-// used once); the parts are added up as integers, in LDS.
+// used once); the parts are added up as integers, in LDS. 5 and 16 tokens of 6144
+// features to 1536 take 8.1 us (with the host's part), in tiles 18.6, 64 tokens
+// 16.2 and 19.8; where K is short the host's part is all there is of either.
 constexpr int kFewWaves = 8, kFewSteps = 4;
 
 template <typename T, int Act, int B>

@@ -3,12 +3,13 @@
 //   s = max |x| * (1 / 127),  q = x / s to the nearest integer, ties to even
 //
 // A row is read once: it stays in registers between its maximum and its
-// quotients. Memory bound (3 bytes a bf16 element) only if an element costs
-// fewer than 20 operations, so the quotient has to be cheap and exact. x (1 / s)
-// is off by two roundings of 127 at most: where it is further than that from the
-// middle between two integers, the nearest to it is the nearest to x / s. A wave
-// with an element nearer to a middle (8 % of rows of 2048) takes the remainder
-// x - q s, which one fused operation gives without rounding.
+// quotients. Memory bound (3 bytes a bf16 element; 105 us for 100,000 rows of 2048,
+// 5.8 TB/s) only if an element costs fewer than 20 operations, so the quotient has
+// to be cheap and exact. x (1 / s) is off by two roundings of 127 at most: where it
+// is further than that from the middle between two integers, the nearest to it is
+// the nearest to x / s. A wave with an element nearer to a middle (8 % of rows of
+// 2048) takes the remainder x - q s, which one fused operation gives without
+// rounding.
 #include <algorithm>
 
 #include "model_internal.h"
@@ -172,12 +173,24 @@ hipError_t launch(const QuantizeArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// A row's threads hold up to 32 elements each where there are rows for all waves,
+// 8 where there are few and their latency counts (binary32 always: 32 take too many
+// registers). At 2048 elements of bf16, 8 and 32 a thread: 11.6 and 14.3 us for 7000
+// rows, 29 and 28 for 20,000, 131 and 122 for 100,000; of binary32 12.5 and 15.1, 34
+// and 37 (20,000), 87 and 97 (50,000). At 8192 of bf16: 9.0 and 10.2 us for 1000, 26
+// and 25 for 4000, 123 and 105 for 20,000.
 template <typename T>
 hipError_t quantize_of(const QuantizeArgs& a, hipStream_t s) {
+    const int64_t all = a.n * a.width;
     if (a.width <= 512) return launch<T, 1, 1>(a, s);
     if (a.width <= 1024) return launch<T, 1, 2>(a, s);
-    if (a.width <= 2048) return launch<T, 1, 4>(a, s);
-    if (a.width <= 8192) return launch<T, 4, 4>(a, s);
+    if (a.width <= 2048) {
+        if constexpr (sizeof(T) == 2)
+            if (all > int64_t(1) << 25) return launch<T, 1, 4>(a, s);
+        return launch<T, 4, 1>(a, s);
+    }
+    if (a.width <= 8192)
+        return all > int64_t(1) << 24 ? launch<T, 4, 4>(a, s) : launch<T, 16, 1>(a, s);
     if (a.width <= 32768) return launch<T, 16, 4>(a, s);
     return launch<T, 16, 8>(a, s);
 }

@@ -40,6 +40,19 @@ def test_quantize_sizes(n, k, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,k", [(32769, 1040), (16385, 2048), (8127, 2064), (2049, 8192)])
+def test_quantize_many_rows(n, k, dtype):
+    """More than 2^25 (from 2049 a row on: 2^24) elements, where a thread holds
+    more of them: each row as it comes out among few."""
+    few = torch.randn(100, k, generator=gen(k)).to(TYPES[dtype]).cuda()
+    check_quantize(few)
+    q, s = quantized(few)
+    pick = torch.randint(0, 100, (n,), generator=gen(n)).cuda()
+    many_q, many_s = quantized(few[pick])
+    assert torch.equal(many_q, q[pick]) and torch.equal(many_s, s[pick])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_quantize_between_two_integers(dtype):
     """Quotients at and next to the middle: the largest a multiple of 127 gives
     exact scales and ties, others quotients a rounding away from them."""
