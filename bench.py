@@ -71,6 +71,11 @@ KERNEL_SOURCES = {
     "rotary_kernels": ["block_rotary.hip", "block_internal.h", "p3d_internal.h"],
     "attention_kernels": ["attention.hip", "attention_bwd.hip", "attn_tile.h",
                           "block_internal.h", "p3d_internal.h"],
+    "group_norm_kernels": ["group_norm.hip", "model_internal.h", "block_internal.h",
+                           "p3d_internal.h"],
+    "adamw_kernels": ["adamw.hip", "model_internal.h", "block_internal.h", "p3d_internal.h"],
+    "linear_i8_kernels": ["linear_i8.hip", "quantize.hip", "attn_tile.h", "model_internal.h",
+                          "block_internal.h", "p3d_internal.h"],
 }
 
 

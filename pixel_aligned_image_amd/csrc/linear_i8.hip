@@ -37,6 +37,31 @@ __device__ __forceinline__ i32x16 mfma(i32x4 a, i32x4 b, i32x16 c) {
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
 }
 
+// Eight neighbouring numbers of a row as they lie.
+template <typename T>
+struct Eight {
+    uint4 v[sizeof(T) / 2];
+
+    __device__ __forceinline__ void load(const void* base, int64_t i) {
+        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(base) +
+                                                        i * (int64_t)sizeof(T));
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) v[k] = p[k];
+    }
+    __device__ __forceinline__ void widen(float (&f)[8]) const {
+        if constexpr (sizeof(T) == 2) {
+            Vec<Bf16>::widen(v[0], f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint4& q = v[e >> 2];
+                f[e] = __uint_as_float((e & 3) == 0 ? q.x : (e & 3) == 1 ? q.y
+                                                        : (e & 3) == 2 ? q.z : q.w);
+            }
+        }
+    }
+};
+
 // Eight neighbouring outputs of a token: scales, bias, activation, residual.
 template <typename T, int Act>
 struct Finish {
@@ -46,31 +71,23 @@ struct Finish {
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = a.weight_scale[d + e];
         if (a.bias) {
-            read(a.bias, d, b);
+            Eight<T> q;
+            q.load(a.bias, d);
+            q.widen(b);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) b[e] = 0.f;
         }
     }
-    static __device__ __forceinline__ void read(const void* base, int64_t i, float (&f)[8]) {
-        if constexpr (sizeof(T) == 2) {
-            Vec<Bf16>::widen(*reinterpret_cast<const uint4*>(
-                                 reinterpret_cast<const uint16_t*>(base) + i), f);
-        } else {
-            const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + i);
-            const float4 x = p[0], y = p[1];
-            f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-            f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-        }
-    }
     // (f: the sums times the token's scale)
+    template <bool Res>
     __device__ __forceinline__ void write(const LinearArgs& a, int64_t token, int d,
-                                          float (&f)[8]) const {
+                                          const Eight<T>& residual, float (&f)[8]) const {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = activate<Act>(f[e] * t[e] + b[e]);
-        if (a.residual) {
+        if constexpr (Res) {
             float r[8];
-            read(a.residual, token * a.residual_stride + d, r);
+            residual.widen(r);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] += r[e];
         }
@@ -124,19 +141,27 @@ __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory");
 
 // A workgroup takes tiles in turn. The next tile's first two stages are on their
 // way while this one's results are turned and stored, which hides the memory's
-// latency at a tile's start and its own stores.
-template <typename T, int Act, typename S>
+// latency at a tile's start and its own stores. With a residual (Res), that of a
+// turn is loaded as the turn before is stored, in the registers that its half of
+// the features' scales and biases leave: 381 us for 100,000 x 2048 x 1536, 429 where
+// it was loaded as it was added, 330 without one. (The same code for both kept those
+// registers from the stages: 346 us without one.)
+template <typename T, int Act, bool Res, typename S>
 __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, int tiles_m,
                                                                int tiles) {
     constexpr int BI = S::BI, BJ = S::BJ, LM = S::LM, LN = S::LN, kLoads = LM + LN;
     extern __shared__ __align__(256) char lds[];    // (fragments reach a slot by an exclusive or)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     // Workgroups go round the 8 dies: each die takes a run of tiles, features
-    // fastest, so that a token tile is read into one die's L2 once.
+    // fastest, so that a token tile is read into one die's L2 once; in bands of at
+    // most 8 feature tiles, whose weights stay there meanwhile (12,289 x 1536 x 6144:
+    // 143 us without bands, 135 with).
     const int per = (tiles + 7) / 8, turn = gridDim.x >> 3;
     const int first = (blockIdx.x & 7) * per, end = min(first + per, tiles);
     int tile = first + (blockIdx.x >> 3);
     if (tile >= end) return;
+    const int tiles_n = tiles / tiles_m, bands = (tiles_m + 7) / 8;
+    const int wide = (tiles_m + bands - 1) / bands;
     const int stages = (a.in_dim + kStep - 1) / kStep;
 
     // Loads: 16 rows an instruction, a uniform base and a 32-bit offset a lane
@@ -150,8 +175,10 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
     int64_t n0;
     const int8_t *wm0, *qn0;
     const auto begin = [&](int t) {
-        m0 = t % tiles_m * S::M;
-        n0 = (int64_t)(t / tiles_m) * S::N;
+        const int band = t / (wide * tiles_n), in = t - band * wide * tiles_n;
+        const int width = min(wide, tiles_m - band * wide), down = in / width;
+        m0 = (band * wide + in - down * width) * S::M;
+        n0 = (int64_t)down * S::N;
         wm0 = a.weight + (int64_t)m0 * a.in_dim;
         qn0 = a.q + n0 * a.q_stride;
         const int last_m = min(a.out_dim - m0, S::M) - 1;
@@ -255,19 +282,22 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
 
     // The epilogue: lanes of a token, tokens at once, turns of the features.
     constexpr int kAcross = S::kTurn * 4, kDown = 64 / kAcross, kTurns = BI / S::kTurn;
+    constexpr int kRows = 32 / kDown;               // tokens of a lane in a turn
+    const auto turn_h = [](int u) { return Res ? u / BJ : u % kTurns; };
+    const auto turn_j = [](int u) { return Res ? u % BJ : u / kTurns; };
     float* turned = reinterpret_cast<float*>(lds + 2 * S::kStage) + wave * 32 * S::kPitch;
 
     begin(tile);
     load_stage(0);
     load_stage(1);
     for (;;) {
-        // What the epilogue needs: the scales of the lane's tokens, and those of
+        // What the epilogue needs (first): the scales of the lane's tokens, and those of
         // eight of its features in every turn.
         const int d0 = m0 + wm + (lane % kAcross) * 8;
         const int64_t token0 = n0 + wn;
         Finish<T, Act> finish[kTurns];
 #pragma unroll
-        for (int h = 0; h < kTurns; ++h)
+        for (int h = 0; h < (Res ? 1 : kTurns); ++h)
             if (d0 + h * S::kTurn * 32 < a.out_dim) finish[h].load(a, d0 + h * S::kTurn * 32);
         float scale[BJ];
 #pragma unroll
@@ -296,6 +326,22 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
         if (stages - st >= 3) stage(st++, integral_constant<int, 1>(), No(), Yes());
         if (stages - st >= 2) stage(st++, integral_constant<int, 0>(), No(), Yes());
         stage(st, integral_constant<int, 0>(), No(), No());
+        // (loads of every lane, kept inside the tensor: what a lane left out would be a
+        // register to keep)
+        Eight<T> residual[kRows];
+        const auto fetch = [&](int u, int k) {
+            const int d = min(d0 + turn_h(u) * S::kTurn * 32, a.out_dim - 8);
+            const int64_t token = token0 + turn_j(u) * 32 + lane / kAcross + k * kDown;
+            residual[k].load(a.residual,
+                             (token < a.n ? token : a.n - 1) * a.residual_stride + d);
+        };
+        if constexpr (Res) {
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) fetch(0, k);
+#pragma unroll
+            for (int h = 1; h < kTurns; ++h)
+                finish[h].load(a, min(d0 + h * S::kTurn * 32, a.out_dim - 8));
+        }
         tile_barrier();                 // nothing reads or writes the stages now
 
         tile += turn;
@@ -308,33 +354,36 @@ __global__ __launch_bounds__(S::kThreads, 2) void linear_kernel(LinearArgs a, in
         // A wave turns 32 tokens and kTurn blocks of features at a time in LDS, so
         // that a token's features leave in 16-byte pieces of whole lines.
 #pragma unroll
-        for (int j = 0; j < BJ; ++j)
+        for (int u = 0; u < kTurns * BJ; ++u) {
+            const int h = turn_h(u), j = turn_j(u);
 #pragma unroll
-            for (int h = 0; h < kTurns; ++h) {
+            for (int i = 0; i < S::kTurn; ++i)
 #pragma unroll
-                for (int i = 0; i < S::kTurn; ++i)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const i32x16& v = acc[h * S::kTurn + i][j];
-                        *reinterpret_cast<float4*>(turned + r32 * S::kPitch + i * 32 + q * 8 +
-                                                   (lane >> 5) * 4) =
-                            make_float4((float)v[4 * q] * scale[j], (float)v[4 * q + 1] * scale[j],
-                                        (float)v[4 * q + 2] * scale[j],
-                                        (float)v[4 * q + 3] * scale[j]);
-                    }
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                const int d = d0 + h * S::kTurn * 32;
-#pragma unroll 2
-                for (int r = lane / kAcross; r < 32; r += kDown) {
-                    const int64_t token = token0 + j * 32 + r;
-                    const float* from = turned + r * S::kPitch + (lane % kAcross) * 8;
-                    const float4 x = *reinterpret_cast<const float4*>(from),
-                                 y = *reinterpret_cast<const float4*>(from + 4);
-                    float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                    if (token < a.n && d < a.out_dim) finish[h].write(a, token, d, f);
+                for (int q = 0; q < 4; ++q) {
+                    const i32x16& v = acc[h * S::kTurn + i][j];
+                    *reinterpret_cast<float4*>(turned + r32 * S::kPitch + i * 32 + q * 8 +
+                                               (lane >> 5) * 4) =
+                        make_float4((float)v[4 * q] * scale[j], (float)v[4 * q + 1] * scale[j],
+                                    (float)v[4 * q + 2] * scale[j],
+                                    (float)v[4 * q + 3] * scale[j]);
                 }
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            const int d = d0 + h * S::kTurn * 32;
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                const int r = lane / kAcross + k * kDown;
+                const int64_t token = token0 + j * 32 + r;
+                const float* from = turned + r * S::kPitch + (lane % kAcross) * 8;
+                const float4 x = *reinterpret_cast<const float4*>(from),
+                             y = *reinterpret_cast<const float4*>(from + 4);
+                float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                if (token < a.n && d < a.out_dim)
+                    finish[h].template write<Res>(a, token, d, residual[k], f);
+                if constexpr (Res)
+                    if (u + 1 < kTurns * BJ) fetch(u + 1, k);
             }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
         if (!more) return;
         meet();                         // the turned tile's place is the stages' again
     }
@@ -403,7 +452,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinearArgs a
         }
         Finish<T, Act> finish;
         finish.load(a, d0 + d);
-        finish.write(a, token, d0 + d, f);
+        Eight<T> residual;
+        if (a.residual) {
+            residual.load(a.residual, token * a.residual_stride + d0 + d);
+            finish.template write<true>(a, token, d0 + d, residual, f);
+        } else {
+            finish.template write<false>(a, token, d0 + d, residual, f);
+        }
     }
 }
 
@@ -417,8 +472,13 @@ template <typename T, int Act, typename S>
 hipError_t tiles_of(const LinearArgs& a, hipStream_t s) {
     const int64_t tiles = tiles_in<S>(a);
     const int64_t grid = std::min<int64_t>((tiles + 7) / 8 * 8, S::kPerCu * kComputeUnits);
-    linear_kernel<T, Act, S><<<(unsigned)grid, S::kThreads, S::kLds, s>>>(
-        a, (a.out_dim + S::M - 1) / S::M, (int)tiles);
+    const int tiles_m = (a.out_dim + S::M - 1) / S::M;
+    if (a.residual)
+        linear_kernel<T, Act, true, S>
+            <<<(unsigned)grid, S::kThreads, S::kLds, s>>>(a, tiles_m, (int)tiles);
+    else
+        linear_kernel<T, Act, false, S>
+            <<<(unsigned)grid, S::kThreads, S::kLds, s>>>(a, tiles_m, (int)tiles);
     return hipGetLastError();
 }
 
@@ -430,18 +490,26 @@ hipError_t linear_of(const LinearArgs& a, hipStream_t s) {
     else if (fits && a.n <= 32) linear_few_kernel<T, Act, 2><<<few, 64 * kFewWaves, 0, s>>>(a);
     else if (fits && a.n <= 64) linear_few_kernel<T, Act, 4><<<few, 64 * kFewWaves, 0, s>>>(a);
     else {
-        // Rounds of tiles over the chip, times a round's length (us where K is
-        // 2048, measured; the lengths' ratios hardly change with K).
+        // Rounds of tiles over the chip, times a round's length: us where K is 2048,
+        // of a full round and of one with a tile or two (what is left of a round runs
+        // at a higher clock). Measured: 27 us in B and 29 to 41 in the others for
+        // 7000 x 2048 x 1536, 49 in B and 54 to 67 for 12,289, 66 in A and 76 to 97
+        // for 20,000, 12 in D and 13 to 24 for 1500, 8.7 in E and 10 to 22 for 300.
+        // The lengths' ratios hardly change with K (1024 and 6144 choose alike).
         using A = Shape<4, 2, 2, 4>;        // 256 features x 256 tokens
         using B = Shape<2, 3, 4, 2>;        // 256 x 192
         using C = Shape<4, 1, 2, 4>;        // 256 x 128
         using D = Shape<2, 2, 2, 2>;        // 128 x 128
         using E = Shape<2, 1, 2, 2>;        // 128 x 64
-        const auto rounds = [](int64_t tiles) { return (tiles + kComputeUnits - 1) / kComputeUnits; };
+        const auto time = [](int64_t tiles, double full, double least) {
+            const int64_t rest = tiles % kComputeUnits;
+            const double last = least + (full - least) * rest / kComputeUnits;
+            return (double)(tiles / kComputeUnits) * full + (rest ? last : 0.);
+        };
         const double times[] = {
-            rounds(tiles_in<A>(a)) * 32., rounds(tiles_in<B>(a)) * 27.5,
-            rounds(tiles_in<C>(a)) * 18., rounds(tiles_in<D>(a)) * 10.8,
-            rounds(tiles_in<E>(a)) * 7.4};
+            time(tiles_in<A>(a), 34., 22.), time(tiles_in<B>(a), 28.4, 18.),
+            time(tiles_in<C>(a), 21., 13.5), time(tiles_in<D>(a), 11.3, 10.),
+            time(tiles_in<E>(a), 7., 6.3)};
         switch (std::min_element(times, times + 5) - times) {
             case 0: return tiles_of<T, Act, A>(a, s);
             case 1: return tiles_of<T, Act, B>(a, s);
