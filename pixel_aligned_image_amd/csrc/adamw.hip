@@ -5,12 +5,13 @@
 //   w = w (1 - lr decay) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
 // One pass over the data: memory bound at 28 bytes an element (binary32
-// weights and states) down to 10 (bf16 weights, 8-bit states): 231 us for 44
-// million elements of 28 bytes, 5.4 TB/s, and 166 us for 89 million of 10, 5.3;
-// the norm of 89 million bf16 gradients takes 30 us, 5.9 TB/s. The tensors'
-// table travels in the kernel arguments, kTensors a launch; a workgroup takes
-// one chunk of one tensor, found by a search over the chunks' first numbers,
-// so that a launch over many small tensors fills the chip as a large one does.
+// weights and states) down to 10 (bf16 weights, 8-bit states): 217 us for 44
+// million elements of 28 bytes, 5.7 TB/s, and 153 us for 88 million of 10, 5.9, where
+// the vector units are as busy; the norm of 88 million bf16 gradients takes 30 us by
+// itself and 47 after a step. The tensors' table travels in the kernel arguments,
+// kTensors a launch; a workgroup takes one chunk of one tensor, which its lanes find
+// among the tensors' first chunks, so that a launch over many small tensors fills
+// the chip as a large one does.
 //
 // 8-bit states: a thread holds 8 neighbouring elements and 32 neighbouring
 // threads a block of 256 that shares a scale, so a block's largest state is a
@@ -93,7 +94,7 @@ __device__ __forceinline__ void widen8(const float* p, float (&f)[8]) {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
-// (past the caches: 231 us for 252 where 44 million elements of 28 bytes stream by)
+// (past the caches: 231 us, not 252, where 44 million elements of 28 bytes stream by)
 __device__ __forceinline__ void narrow8(Bf16* p, const float (&f)[8]) {
     store_nt16(p, Vec<Bf16>::narrow(f));
 }

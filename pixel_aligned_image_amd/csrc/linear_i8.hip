@@ -9,10 +9,10 @@
 // results are neighbouring features of one token. K advances in stages of 64
 // integers, four of them in LDS: while one is multiplied the next has arrived
 // and two more are on their way, which covers the memory's latency with one
-// workgroup on a CU. Measured: 100,000 x 2048 x 1536 in 342 us, 1.84 PFLOP/s,
-// 12,289 x 1536 x 6144 with GELU in 137 us, 1.69 (a library's bare product: 1.72
-// to 1.83 and 1.52 to 1.61). Under this load the clock drops to about 1.6 GHz: the
-// matrix cores' power bounds it, and instructions saved elsewhere no longer show.
+// workgroup on a CU. Measured: 100,000 x 2048 x 1536 in 323 to 333 us,
+// 1.9 PFLOP/s, 12,289 x 1536 x 6144 in 134 us, 1.73, and with GELU in 154 (a
+// library's bare products: 1.72 to 1.83 and 1.52 to 1.61). Under this load the clock
+// drops to 1.6 to 1.9 GHz: the matrix cores' power bounds it.
 #include <algorithm>
 #include <type_traits>
 
