@@ -202,6 +202,20 @@ def test_added_into_the_residual(n):
     check_out(out, s, torch.bfloat16, "none")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,d", [(300, 1544), (1500, 1544), (3900, 1544), (6990, 1544),
+                                 (15000, 1544), (20000, 1544), (2500, 6152), (600, 12296)])
+def test_residuals_in_every_tile(n, d, dtype):
+    """Each tile's shape, one and several rounds, bands of features, ragged at both
+    ends: added in place and into another tensor, the same."""
+    s = made(n, 80, d, TYPES[dtype], n + d, residual=True)
+    out, other = s["r"].clone(), torch.full_like(s["r"], 9)
+    p3d.p3d_linear_i8(s["q"], s["s"], s["w"], s["t"], out, s["b"], "silu", residual=out)
+    p3d.p3d_linear_i8(s["q"], s["s"], s["w"], s["t"], other, s["b"], "silu", residual=s["r"])
+    assert torch.equal(out, other)
+    check_out(out, s, TYPES[dtype], "silu")
+
+
 def test_the_same_call_gives_the_same_bytes():
     for n in (5, 1000, 20000):
         s = made(n, 1024, 520, torch.bfloat16, 7)
