@@ -14,6 +14,7 @@
 // library's bare products: 1.72 to 1.83 and 1.52 to 1.61). Under this load the clock
 // drops to 1.6 to 1.9 GHz: the matrix cores' power bounds it.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "attn_tile.h"
@@ -468,17 +469,19 @@ int64_t tiles_in(const LinearArgs& a) {
     return ((a.out_dim + S::M - 1) / S::M) * ((a.n + S::N - 1) / S::N);
 }
 
-template <typename T, int Act, typename S>
+template <typename T, int Act, typename S, bool Added = true>
 hipError_t tiles_of(const LinearArgs& a, hipStream_t s) {
     const int64_t tiles = tiles_in<S>(a);
     const int64_t grid = std::min<int64_t>((tiles + 7) / 8 * 8, S::kPerCu * kComputeUnits);
     const int tiles_m = (a.out_dim + S::M - 1) / S::M;
-    if (a.residual)
-        linear_kernel<T, Act, true, S>
-            <<<(unsigned)grid, S::kThreads, S::kLds, s>>>(a, tiles_m, (int)tiles);
-    else
-        linear_kernel<T, Act, false, S>
-            <<<(unsigned)grid, S::kThreads, S::kLds, s>>>(a, tiles_m, (int)tiles);
+    if constexpr (Added)
+        if (a.residual) {
+            linear_kernel<T, Act, true, S>
+                <<<(unsigned)grid, S::kThreads, S::kLds, s>>>(a, tiles_m, (int)tiles);
+            return hipGetLastError();
+        }
+    linear_kernel<T, Act, false, S>
+        <<<(unsigned)grid, S::kThreads, S::kLds, s>>>(a, tiles_m, (int)tiles);
     return hipGetLastError();
 }
 
@@ -495,7 +498,9 @@ hipError_t linear_of(const LinearArgs& a, hipStream_t s) {
         // at a higher clock). Measured: 27 us in B and 29 to 41 in the others for
         // 7000 x 2048 x 1536, 49 in B and 54 to 67 for 12,289, 66 in A and 76 to 97
         // for 20,000, 12 in D and 13 to 24 for 1500, 8.7 in E and 10 to 22 for 300.
-        // The lengths' ratios hardly change with K (1024 and 6144 choose alike).
+        // The lengths' ratios hardly change with K (1024 and 6144 choose alike). C not
+        // with a residual, whose first loads a tile of so few columns does not cover:
+        // 19 us without one and 23.4 with it, D 20.6 and 21.8 (4000 x 2048 x 1536).
         using A = Shape<4, 2, 2, 4>;        // 256 features x 256 tokens
         using B = Shape<2, 3, 4, 2>;        // 256 x 192
         using C = Shape<4, 1, 2, 4>;        // 256 x 128
@@ -508,12 +513,12 @@ hipError_t linear_of(const LinearArgs& a, hipStream_t s) {
         };
         const double times[] = {
             time(tiles_in<A>(a), 34., 22.), time(tiles_in<B>(a), 28.4, 18.),
-            time(tiles_in<C>(a), 21., 13.5), time(tiles_in<D>(a), 11.3, 10.),
-            time(tiles_in<E>(a), 7., 6.3)};
+            a.residual ? INFINITY : time(tiles_in<C>(a), 21., 13.5),
+            time(tiles_in<D>(a), 11.3, 8.5), time(tiles_in<E>(a), 7.4, 6.6)};
         switch (std::min_element(times, times + 5) - times) {
             case 0: return tiles_of<T, Act, A>(a, s);
             case 1: return tiles_of<T, Act, B>(a, s);
-            case 2: return tiles_of<T, Act, C>(a, s);
+            case 2: return tiles_of<T, Act, C, false>(a, s);
             case 3: return tiles_of<T, Act, D>(a, s);
             default: return tiles_of<T, Act, E>(a, s);
         }
