@@ -48,8 +48,9 @@ struct Step {
     float b1, b2, c1, c2;       // c = 1 - b
     float rate;                 // lr / (1 - b1^t)
     float norm;                 // 1 / sqrt(1 - b2^t)
-    float eps;
+    float eps;                  // (these three times lift)
     int32_t count;
+    double lift;
     double lr, log_b1, log_b2;  // (log2) where lr or t are the device's
     int64_t t;
     uint64_t seed;
@@ -237,8 +238,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table table, Step s) {
         int64_t n = s.device_step ? (int64_t)*s.device_step : s.t;
         n = n < 1 ? 1 : n;
         keep = (float)(1. - lr * (double)t.keep);
-        s.rate = (float)(lr / (1. - exp2((double)n * s.log_b1)));
-        s.norm = (float)(1. / sqrt(1. - exp2((double)n * s.log_b2)));
+        s.rate = (float)(s.lift * (lr / (1. - exp2((double)n * s.log_b1))));
+        s.norm = (float)(s.lift * (1. / sqrt(1. - exp2((double)n * s.log_b2))));
         if (Bits == 8 && s.device_step) key = mix(key ^ seed_key(s.seed + (uint64_t)n));
     }
     const int64_t i = (int64_t)(blockIdx.x - table.first[at]) * kChunk + threadIdx.x * kPer;
@@ -287,6 +288,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table table, Step s) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) root[e] = sqrtf(v[e]);
         }
+        // (the hardware's reciprocal takes and gives normal numbers: see `lift_of`)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             w[e] = w[e] * keep -
@@ -481,6 +483,17 @@ hipError_t adamw_grad(const p3d_adamw_desc& d, const Step& step, bool master, hi
     return master ? adamw_bits<Bf16, G, true>(d, step, s) : adamw_bits<Bf16, G, false>(d, step, s);
 }
 
+// What the update's factor, the root's and eps are multiplied by, a power of two, so
+// that the hardware's reciprocal serves every eps that binary32 holds: of a number
+// below 2^-126 it gives infinity (and 0 times that is NaN, where an element without a
+// gradient has nothing to divide), of one above 2^126 0. Denominators lie between eps
+// and eps + 2^91, as a root is below 2^64 and its factor below 2^27. 32-bit states
+// are divided.
+double lift_of(const p3d_adamw_desc& d) {
+    if (d.state_bits != 8) return 1.;
+    return d.eps < 0x1p-126 ? 0x1p24 : d.eps > 0x1p100 ? 0x1p-64 : 1.;
+}
+
 }  // namespace
 
 // (a launch's chunks, of which it has at most kNormGrid parts, in as many
@@ -522,9 +535,10 @@ hipError_t launch_adamw(const p3d_adamw_desc& d, hipStream_t s) {
     step.b2 = (float)d.beta2;
     step.c1 = (float)(1. - d.beta1);
     step.c2 = (float)(1. - d.beta2);
-    step.rate = (float)(d.lr / (1. - std::pow(d.beta1, (double)d.step)));
-    step.norm = (float)(1. / std::sqrt(1. - std::pow(d.beta2, (double)d.step)));
-    step.eps = (float)d.eps;
+    step.lift = lift_of(d);
+    step.rate = (float)(step.lift * (d.lr / (1. - std::pow(d.beta1, (double)d.step))));
+    step.norm = (float)(step.lift * (1. / std::sqrt(1. - std::pow(d.beta2, (double)d.step))));
+    step.eps = (float)(step.lift * d.eps);
     step.lr = d.lr;
     step.log_b1 = std::log2(d.beta1);
     step.log_b2 = std::log2(d.beta2);

@@ -334,3 +334,38 @@ def test_a_tensor_whose_elements_pass_32_bits():
     check_codes(m[-700:], ms[at:], m1, 6 * ref.U * m1.abs(), bits & 0xffff, False, "m")
     check_codes(v[-700:], vs[at:], v1.sqrt(), 8 * ref.U * v1.sqrt(), bits >> 16, True, "v")
     assert not w[:1 << 20].any() and not vs[:at].any()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 1.1754942e-38, 1.1754944e-38, 1e-30])
+def test_every_eps_that_binary32_holds(eps, bits):
+    """An element without a gradient and without states keeps its weight (0 / eps
+    is 0), however small eps is."""
+    model = Model(SIZES, bits=bits, late=False, seed=11)
+    assert any(bool((g == 0).any()) for g in model.g)
+    hyper = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=eps)
+    step_and_check(model, 1, hyper=hyper)
+    # a block, and a tensor, of which nothing has a gradient
+    model = Model([700, 300], bits=bits, late=False, seed=12)
+    model.g[0][256:512] = 0
+    model.g[1].zero_()
+    step_and_check(model, 1, hyper=hyper)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e30, 1e38])
+def test_an_eps_beyond_the_reciprocals(eps, bits):
+    """m / eps where 1 / eps is no normal number of binary32: m = 1e36 moves a
+    weight of 0 by lr m / eps (of 0.9 m, as the gradient is 0)."""
+    n = 600
+    w, g = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    if bits == 32:
+        m, v = torch.full((n,), 1e36, device="cuda"), torch.zeros(n, device="cuda")
+        table = p3d.make_adamw_tensors([w], [g], [m], [v])
+    else:
+        m, v = (torch.full((n,), x, device="cuda").to(torch.float8_e4m3fn) for x in (256.0, 0.0))
+        ms, vs = torch.full((3,), 1e36 / 256, device="cuda"), torch.zeros(3, device="cuda")
+        table = p3d.make_adamw_tensors([w], [g], [m], [v], m_scales=[ms], v_scales=[vs])
+    p3d.p3d_adamw(table, 1.0, 0.9, 0.99, eps, 1000000)
+    want = -0.9 * 1e36 / eps
+    assert torch.all((w.double() - want).abs() <= 16 * ref.U * abs(want))
