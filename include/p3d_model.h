@@ -236,8 +236,9 @@ p3d_status p3d_adamw(const p3d_adamw_desc* desc, void* stream);
 /* p3d_grad_norm -- the norm over every tensor's gradient, and the factor that
  * clips it, for p3d_adamw's grad_scale:
  *   out[0] = norm = sqrt(sum of squares)   (summed in binary64)
- *   out[1] = norm > max_norm ? max_norm / norm : 1;  NaN where the norm is not
- *            finite, so that the step is left out
+ *   out[1] = norm > max_norm ? max_norm / norm : 1;  NaN where out[0] is not
+ *            finite (a norm beyond binary32 among them), so that the step is
+ *            left out
  * out: DEVICE float [2], no part of a gradient. Of desc, count, grad_dtype and the tensors' grad and
  * size are read. max_norm > 0 (infinity: no clipping).
  * workspace: p3d_grad_norm_workspace_size(desc) bytes. */

@@ -413,7 +413,8 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const double* __restric
     for (int k = 0; k < 16; ++k) sum += wave[k];
     const double norm = sqrt(sum);
     out[0] = (float)norm;
-    out[1] = !(norm < INFINITY) ? NAN
+    // (finite as out[0] has it: the two say the same of a norm beyond binary32)
+    out[1] = !(out[0] < INFINITY) ? NAN
              : norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
 }
 

@@ -369,3 +369,24 @@ def test_an_eps_beyond_the_reciprocals(eps, bits):
     p3d.p3d_adamw(table, 1.0, 0.9, 0.99, eps, 1000000)
     want = -0.9 * 1e36 / eps
     assert torch.all((w.double() - want).abs() <= 16 * ref.U * abs(want))
+
+
+@pytest.mark.parametrize("most", [1.0, math.inf])
+def test_a_norm_beyond_binary32_leaves_the_step_out(most):
+    """Gradients that are finite, their norm 2^128 and more: the two results agree
+    that it is none, and just below it that it is one."""
+    n, out = 4096, torch.empty(2, device="cuda")
+    g = torch.full((n,), 2.0 ** 122, device="cuda")              # norm 2^128
+    w, m, v = torch.ones(n, device="cuda"), torch.zeros(n, device="cuda"), torch.zeros(
+        n, device="cuda")
+    table = p3d.make_adamw_tensors([w], [g], [m], [v])
+    p3d.p3d_grad_norm(table, out, most)
+    assert math.isinf(float(out[0])) and math.isnan(float(out[1]))
+    p3d.p3d_adamw(table, grad_scale=out[1:], **HYPER)
+    assert (w == 1).all() and not m.any() and not v.any()
+    g[0] = 0
+    p3d.p3d_grad_norm(table, out, most)
+    norm = math.sqrt(4095) * 2.0 ** 122
+    assert math.isclose(float(out[0]), norm, rel_tol=2 * ref.U)
+    # (1 / norm is below the normal numbers: within half of their step)
+    assert abs(float(out[1]) - min(1.0, most / norm)) <= 2.0 ** -150
