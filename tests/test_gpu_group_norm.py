@@ -254,3 +254,48 @@ def test_gradient_against_differences():
         # derivative of a few units)
         assert abs((ends[0] - ends[1]) / (2 * h) - float(dx.view(-1)[i])) < 640 ** 0.5 * 3 * (
             2.0 ** -20) / h + 10 * h * h, i
+
+
+@pytest.mark.parametrize("value", [0.1, 100.3, 12345.678, -3e5 - 1 / 3])
+@pytest.mark.parametrize("n,c,groups", [
+    (45, 32, 4), (500, 32, 1), (501, 24, 8), (5003, 16, 16), (50000, 32, 4),
+    # (8 rows a thread and more)
+    (20011, 1024, 32), (9001, 2048, 1), (20011, 1024, 1024), (30011, 320, 32)])
+def test_constant_rows_whose_sums_are_rounded(n, c, groups, value):
+    """A variance of 0 about a mean whose multiples binary32 does not hold: out is
+    act(bias), rstd 1 / sqrt(eps), in the gradient's x^ nothing is left either."""
+    s = made(n, c, torch.float32, 7)
+    s["x"] = torch.full((n, c), value, device="cuda")
+    out, mean, rstd = torch.empty_like(s["x"]), torch.empty(1, groups, device="cuda"), torch.empty(
+        1, groups, device="cuda")
+    p3d.p3d_group_norm(s["x"], out, groups, weight=s["w"], bias=s["b"], mean=mean, rstd=rstd)
+    top = abs(float(s["x"][0, 0]))
+    r = 1e-5 ** -0.5
+    # Items in registers: the sum of at most 128 rows is off by 64 roundings (32 in a
+    # thread, then a tree), so deviations are 64 U of the value at most, and their own
+    # mean, taken off again, is off by as many roundings of that. Chunks: batches are
+    # exact, 1023 of them are joined in binary64.
+    left = 64 * ref.U * 64 * ref.U * top + 1100 * 2.0 ** -53 * top
+    bound = left * r * s["w"].abs().double() + 2 * ref.U * s["b"].abs().double() + 1e-37
+    assert torch.all((out.double() - s["b"].double()).abs() <= bound)
+    assert (mean == s["x"][0, 0]).all()
+    # (the variance: 64 roundings of the deviations' squares)
+    var = 64 * ref.U * (64 * ref.U * top) ** 2 + left ** 2
+    assert torch.all((rstd.double() / r - 1).abs() <= 4 * ref.U + var / 1e-5)
+    dx, dw, db = torch.empty_like(out), *(torch.empty(c, device="cuda") for _ in range(2))
+    p3d.p3d_group_norm_backward(s["dout"], s["x"], mean, rstd, dx, groups, weight=s["w"],
+                                dweight=dw, dbias=db)
+    assert not dw.any()
+    assert torch.allclose(db.double(), s["dout"].double().sum(0),
+                          atol=float(s["dout"].double().abs().sum(0).max()) * 64 * ref.U)
+
+
+@pytest.mark.parametrize("value", [100.5, -3e5])
+def test_constant_rows_in_bf16(value):
+    n, c, groups = 20011, 1024, 32
+    x = torch.full((n, c), value, dtype=torch.bfloat16, device="cuda")
+    out, mean, rstd = torch.empty_like(x), *(torch.empty(1, groups, device="cuda") for _ in "ab")
+    b = made(n, c, torch.bfloat16, 7)["b"]
+    p3d.p3d_group_norm(x, out, groups, bias=b, mean=mean, rstd=rstd)
+    assert torch.equal(out, b.expand(n, c)) and (mean == x[0, 0].float()).all()
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
