@@ -299,3 +299,92 @@ def test_constant_rows_in_bf16(value):
     p3d.p3d_group_norm(x, out, groups, bias=b, mean=mean, rstd=rstd)
     assert torch.equal(out, b.expand(n, c)) and (mean == x[0, 0].float()).all()
     assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
+
+
+def check_group_by_group(n, c, groups, dtype, kind, off, stride=0, in_place=False, seed=0, eps=1e-5):
+    """As check, of maps whose 64-bit form would not be quick on the CPU: a group
+    at a time, on the device."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def randn(*shape, scale=1.0, base=0.0):
+        return (torch.randn(*shape, generator=g, device="cuda") * scale + base).to(dtype)
+
+    def buffer(t, more):
+        wide = torch.full((n, c + more), float("nan"), dtype=dtype, device="cuda")
+        wide[:, more // 2:more // 2 + c] = t
+        return wide[:, more // 2:more // 2 + c]
+
+    x = randn(n, c, scale=1.5) + randn(c, scale=0.5)
+    dout, w, b = randn(n, c), randn(c, scale=0.3, base=1.0), randn(c, scale=0.5)
+    items, per = len(off) - 1, c // groups
+    mean, rstd = (torch.full((items, groups), float("nan"), device="cuda") for _ in range(2))
+    keep, kept = x.clone(), dout.clone()
+    if stride:
+        x, dout = buffer(x, stride), buffer(dout, 3 * stride)
+    out = x if in_place else buffer(torch.full_like(keep, float("nan")), 2 * stride)
+    p3d.p3d_group_norm(x, out, groups, off, w, b, kind, eps, mean, rstd)
+    out = out.clone()
+    if in_place:
+        x.copy_(keep)
+    dx = dout if in_place else buffer(torch.full_like(keep, float("nan")), 2 * stride)
+    dweight, dbias = (torch.full((c,), float("nan"), device="cuda") for _ in range(2))
+    p3d.p3d_group_norm_backward(dout, x, mean, rstd, dx, groups, off, w, b, kind, dweight, dbias)
+    lengths = torch.tensor(off, device="cuda").diff()
+    item = torch.repeat_interleave(torch.arange(items, device="cuda"), lengths)
+    count = (lengths * per).clamp(min=1).double()[:, None]
+
+    def over(v):                             # [n, per] -> averages [items, 1]
+        return torch.stack([v[i:k].sum() for i, k in zip(off, off[1:])])[:, None] / count
+
+    def close(got, want, dtype, slack, what):
+        bound = ref.HALF[dtype] * want.abs() + slack * (1 + 2 * ref.HALF[dtype]) + 1e-37
+        off_ = (got.double() - want).abs()
+        assert bool((off_ <= bound).all()), (what, float((off_ / bound).max()))
+
+    for j in range(groups):
+        cols = slice(j * per, (j + 1) * per)
+        x64, d64, w64, b64 = (t[..., cols].double() for t in (keep, kept, w, b))
+        m64 = over(x64)
+        r64 = (over((x64 - m64[item]).square()) + eps).rsqrt()
+        top = float(x64.abs().max())
+        # (bounds as in check)
+        assert torch.all((mean[:, j:j + 1] - m64).abs() <= 2 * ref.U * m64.abs() + 64 * ref.U * top)
+        assert torch.all((rstd[:, j:j + 1] - r64).abs()
+                         <= 64 * ref.U * r64 * (1 + r64 * top * 1e-2))
+        xn = (x64 - m64[item]) * r64[item]
+        u = (xn * w64 + b64).requires_grad_(True)
+        want = ref.act(u, kind)
+        slope, = torch.autograd.grad(want.sum(), u)
+        u, want = u.detach(), want.detach()
+        gain = r64[item] * w64.abs()
+        size = u.abs() + b64.abs()
+        slack = 1.2 * (64 * ref.U * top * gain + 80 * ref.U * size) + 4 * ref.U * want.abs() * (
+            2 + 2 * u.abs())
+        close(out[:, cols], want, dtype, slack, ("out", j))
+        du64 = d64 * slope
+        dn = du64 * w64
+        dx64 = r64[item] * (dn - over(dn)[item] - xn * over(dn * xn)[item])
+        big = d64.abs() * 1.2
+        du = big * (64 * ref.U * (2 + size) + 64 * ref.U * top * gain)
+        each = du * w64.abs() + 128 * ref.U * big * w64.abs()
+        slack = r64[item] * (each + over(each)[item]
+                             + (xn.abs() + 1) * over(each * (xn.abs() + 1))[item])
+        close(dx[:, cols], dx64, dtype, slack, ("dx", j))
+        sums = du + 128 * ref.U * big
+        close(dbias[cols], du64.sum(0), torch.float32, sums.sum(0), ("dbias", j))
+        close(dweight[cols], (du64 * xn).sum(0), torch.float32,
+              (sums * (xn.abs() + 1)).sum(0), ("dweight", j))
+
+
+@pytest.mark.parametrize("n,c,groups,dtype,items,kind,stride,in_place", [
+    (110001, 1024, 32, "bf16", 1, "silu", 0, False), (110001, 1024, 32, "bf16", 3, "gelu", 16, False),
+    (110001, 1024, 32, "bf16", 3, "silu", 0, True),
+    # few groups, many items: the chunks of either fit the bound of joining them in place
+    (110001, 1024, 1, "bf16", 1, "silu", 0, False), (110001, 1024, 2, "bf16", 1, "none", 0, True),
+    (262144, 1024, 32, "bf16", 16, "silu", 0, False),
+    # groups that straddle vectors, and one channel each
+    (110001, 1000, 40, "bf16", 2, "silu", 16, False), (1700001, 64, 64, "bf16", 2, "silu", 0, False),
+    (60001, 1024, 32, "f32", 2, "silu", 16, False), (60001, 1000, 200, "f32", 1, "gelu", 0, True)])
+def test_maps_larger_than_the_caches(n, c, groups, dtype, items, kind, stride, in_place):
+    check_group_by_group(n, c, groups, TYPES[dtype], kind, uneven(n, items), stride, in_place,
+                         seed=n + groups)
