@@ -993,8 +993,12 @@ __global__ __launch_bounds__(kSmallThreads) void group_small_backward_kernel(
 // ----------------------------------------------------------------- launch ---
 // Whether the second kernel's workgroups join their item's chunks, of `bytes`
 // each, themselves: what they read for it, all together, against a launch of 4 us.
-// (4096 rows of 512 channels: 16.7 us for the gradient, 19 with a launch of its own.
-// A map cut into all of 1023 chunks is 16 times over the bound and more.)
+// Here and with a launch of its own, us: the forward call 27.7 and 29.4 (40,000 rows
+// of 512 in 2 groups, 16 MB), 104.0 and 105.5 (90,000 of 1024 in 16 items, 16 MB),
+// 30.0 and 29.2 (20,000 of 1024 in one group, 8 MB); the gradient 17.6 and 19.0 (4096
+// of 512, 4 MB), 19.5 and 21.3 (10,000 in 2 items, 12 MB), 19.9 and 19.0 (7000, 12 MB),
+// 21.2 and 18.9 (4096 of 1024, 8 MB). The bound is on the sum, so a map of all of 1023
+// chunks passes where it has 2 groups or fewer.
 bool join_in_apply(const GroupArgs& a, const GroupPlan& p, size_t bytes) {
     int64_t pairs = 0;
     for (int b = 0; b < a.batch; ++b) {
@@ -1032,7 +1036,11 @@ hipError_t forward_of(const GroupArgs& a, const GroupPlan& p, float2* partial, f
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const bool here = join_in_apply(a, p, a.groups * sizeof(float2));
+    // (A map loaded past the caches has its chunks joined before: of 262,144 rows of
+    // 1024 channels in one group 264 us, 286 where the workgroups joined them and loaded
+    // through the caches.)
+    const bool past = is_past(a, Vec<T>::N);
+    const bool here = !past && join_in_apply(a, p, a.groups * sizeof(float2));
     if (!here) {
         const int64_t waves = (int64_t)a.batch * a.groups;
         group_join_kernel<<<(unsigned)((waves + 3) / 4), kThreads, 0, s>>>(a, p.chunk, p.ty,
@@ -1040,7 +1048,6 @@ hipError_t forward_of(const GroupArgs& a, const GroupPlan& p, float2* partial, f
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !chunks) return e;
     }
-    const bool past = is_past(a, Vec<T>::N);
     return with_act([&](auto act) {
         constexpr int A = decltype(act)::value;
         const size_t lds = here ? a.groups / p.slices * sizeof(float4) : 0;
