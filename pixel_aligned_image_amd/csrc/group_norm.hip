@@ -753,11 +753,13 @@ __global__ __launch_bounds__(kThreads, 4) void group_dx_kernel(GroupArgs a, Item
 // Items whose slice of channels fits a workgroup's registers take one launch: a
 // workgroup holds the slice of all of an item's rows between the sums and their
 // use, so the data is read once and the statistics are about the exact mean.
-// What it saves is a launch or two on the host: 12 us where the chunks' kernels
-// take 14.5 and, of the gradient, 13 where they take 18.5 (256 rows of 256 to 1024
-// channels). With more than a workgroup a CU, or longer items, it is the slower:
-// 24 us where they take 18.5 (1000 rows of 256, bf16, the gradient), 51 for their
-// 36 (64 items of 64 rows of 1024).
+// What it saves is a launch or two. Here and in the chunks' kernels, us, bf16 with 32
+// groups: the forward call 10 and 14 (64 rows of 1024 in one item, 1024 in 16 items),
+// 12 and 17 (64 items of 64 rows of 1024), 19 and 23 (256 of 64 of 512); the gradient
+// 11.8 and 15.4, 15.8 and 16.0, 18.5 and 18.8 (binary32: 22 and 20), and 35 and 24 for
+// the last of these, whose workgroups, a whole item each, hold all that they can. With
+// more than a workgroup a CU it is the slower: 14 us, not 12, and the gradient 24, not
+// 18.5, for those 64 items in 8 slices each.
 constexpr int kSmallThreads = 1024;
 
 // Vectors that a thread holds: 32 elements.
