@@ -133,7 +133,8 @@ p3d_status p3d_quantize_rows(const void* x, p3d_dtype dtype, int64_t n, int32_t 
  *                with equal strides
  *   out          [n, D], rows out_stride (>= D, a multiple of 8 / 4) apart;
  *                must not overlap another tensor of the call
- *   Alignment: 16 bytes (scale, weight_scale: 4). n, D < 2^30.
+ *   Alignment: 16 bytes (scale, weight_scale: 4). n, D < 2^30, and their
+ *   product, each rounded up to a multiple of 64, below 2^36.
  * --------------------------------------------------------------------- */
 typedef struct p3d_linear_i8_desc {
     int64_t n;                  /* tokens */

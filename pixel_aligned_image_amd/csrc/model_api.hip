@@ -404,8 +404,9 @@ p3d_status p3d_linear_i8(const p3d_linear_i8_desc* desc, const int8_t* q, int64_
                          (long long)d);
     // (the kernels number their tiles, of 128 x 64 or more, in 32 bits)
     if (((n + 63) / 64) * ((d + 63) / 64) >= int64_t(1) << 24)
-        return set_error(P3D_ERR_UNSUPPORTED, "%s: n * out_dim must be below 2^36, got %lld * %lld",
-                         fn, (long long)n, (long long)d);
+        return set_error(P3D_ERR_UNSUPPORTED,
+                         "%s: n * out_dim, each rounded up to a multiple of 64, must be below 2^36, "
+                         "got %lld * %lld", fn, (long long)n, (long long)d);
     const int unit = desc->dtype == P3D_BF16 ? 8 : 4, e = 16 / unit;
     const bool some = n > 0;
     P3D_TRY(check_tensor(fn, "weight", desc->weight, some));

@@ -252,6 +252,23 @@ def test_linear_checks(p3d):
     call(INVALID, "out must not overlap residual", r=O + 256, rs=128)
 
 
+def test_linear_sizes(p3d):
+    """Both sides of the limit on tokens times features, each in 64s: the next
+    check refuses what this one takes."""
+    def call(n, out_dim, needle):
+        d = p3d.model.p3d_linear_i8_desc(n, 64, out_dim, p3d.P3D_BF16, 0, None, None, None)
+        refused(p3d, p3d.lib.p3d_linear_i8(d, None, 64, None, None, 0, None, out_dim, None),
+                INVALID if "NULL" in needle else UNSUPPORTED, needle, "p3d_linear_i8")
+
+    big = 1 << 30
+    for n, out_dim in ((1, big - 64), (64, big - 64), (65, big // 2 - 64), (big - 64, 8),
+                       (1 << 20, (1 << 16) - 64)):
+        call(n, out_dim, "weight is NULL")
+    for n, out_dim in ((1, big - 56), (1, big - 8), (65, big // 2 - 56), (big - 63, 8),
+                       (big - 1, 64), ((1 << 20) - 63, 1 << 16)):
+        call(n, out_dim, "each rounded up to a multiple of 64, must be below 2^36")
+
+
 # ------------------------------------------------------------------- adamw ---
 def table(p3d, count=3, bits=32, master=False, **kw):
     """count tensors of 1000 elements, a megabyte apart."""
