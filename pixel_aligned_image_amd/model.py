@@ -119,6 +119,15 @@ def _ptr(t, name, dtype, dev, shape):
     _refuse(t, name, dtype, dev, "%s and contiguous" % (list(shape),))
 
 
+def _work(workspace, size, dev, stream):
+    """As block._work, on the device that the call runs on."""
+    if workspace is None:
+        return block._work(None, size, torch.device("cuda", dev), stream)
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev:
+        _refuse(workspace, "workspace", torch.uint8, dev, "a buffer of bytes")
+    return block._work(workspace, size, None, stream)
+
+
 def _choice(table, name, value):
     if value not in table:
         raise ValueError("%s must be one of %s, got %r" % (name, ", ".join(table), value))
@@ -159,8 +168,7 @@ def p3d_group_norm(x, out, groups, offsets=None, weight=None, bias=None, act="no
     xp, xs = _rows(x, "x", x.dtype, dev)
     op, os = _rows(out, "out", x.dtype, dev, x.shape)
     stats = (d.batch, d.groups)
-    keep, ws, nbytes = block._work(workspace, lambda: lib.p3d_group_norm_workspace_size(d),
-                                   x.device, stream)
+    keep, ws, nbytes = _work(workspace, lambda: lib.p3d_group_norm_workspace_size(d), dev, stream)
     _core._check(lib.p3d_group_norm(d, xp, xs, op, os, _ptr(mean, "mean", f, dev, stats),
                                     _ptr(rstd, "rstd", f, dev, stats), ws, nbytes,
                                     block._stream(stream)))
@@ -178,8 +186,7 @@ def p3d_group_norm_backward(dout, x, mean, rstd, dx, groups, offsets=None, weigh
     dp, ds = _rows(dout, "dout", dt, dev, x.shape)
     op, os = _rows(dx, "dx", dt, dev, x.shape)
     stats, cols = (d.batch, d.groups), (d.channels,)
-    keep, ws, nbytes = block._work(workspace, lambda: lib.p3d_group_norm_workspace_size(d),
-                                   x.device, stream)
+    keep, ws, nbytes = _work(workspace, lambda: lib.p3d_group_norm_workspace_size(d), dev, stream)
     _core._check(lib.p3d_group_norm_backward(
         d, dp, ds, xp, xs, _ptr(mean, "mean", f, dev, stats), _ptr(rstd, "rstd", f, dev, stats),
         op, os, _ptr(dweight, "dweight", f, dev, cols), _ptr(dbias, "dbias", f, dev, cols), ws,
@@ -338,7 +345,6 @@ def p3d_grad_norm(tensors, out, max_norm=float("inf"), workspace=None, stream=No
     gradients, and the factor that brings it to max_norm where it is above (NaN
     where it is not finite)."""
     dev, d = _adamw(tensors)
-    keep, ws, nbytes = block._work(workspace, lambda: lib.p3d_grad_norm_workspace_size(d),
-                                   torch.device("cuda", dev), stream)
+    keep, ws, nbytes = _work(workspace, lambda: lib.p3d_grad_norm_workspace_size(d), dev, stream)
     _core._check(lib.p3d_grad_norm(d, max_norm, _ptr(out, "out", torch.float32, dev, (2,)), ws,
                                    nbytes, block._stream(stream)))

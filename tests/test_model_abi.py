@@ -447,3 +447,39 @@ def test_group_workspace_size_through_the_binding(p3d):
         x, 8, [0, 100])
     with pytest.raises(p3d.P3DError, match="groups"):
         p3d.p3d_group_norm_workspace_size(x, 7)
+
+
+class _On(torch.Tensor):
+    """A tensor that says of itself that it is on a GPU."""
+    at = 0
+    is_cuda = True
+    device = property(lambda self: torch.device("cuda", self.at))
+
+    def get_device(self):
+        return self.at
+
+
+def test_a_workspace_on_another_device_is_refused(p3d, monkeypatch):
+    def on(t, at):
+        t = t.as_subclass(_On)
+        t.at = at
+        return t
+
+    def reached(*a):
+        raise AssertionError("the library is not called")
+
+    monkeypatch.setattr(p3d.model, "_device", lambda: 0)
+    x, s = (on(torch.zeros(shape), 0) for shape in ((4, 64), (1, 8)))
+    v = on(torch.zeros(100), 0)
+    table = p3d.make_adamw_tensors([v], [v], [v], [v])
+    for name in ("p3d_group_norm", "p3d_group_norm_backward", "p3d_grad_norm"):
+        monkeypatch.setattr(p3d.model.lib, name, reached)
+    for workspace, error, words in (
+            (on(torch.zeros(1 << 20, dtype=torch.uint8), 1), ValueError, "current device"),
+            (torch.zeros(1 << 20, dtype=torch.uint8), ValueError, "on the GPU"),
+            (bytearray(1 << 20), TypeError, "a torch.Tensor")):
+        for call in (lambda: p3d.p3d_group_norm(x, x, 8, workspace=workspace),
+                     lambda: p3d.p3d_group_norm_backward(x, x, s, s, x, 8, workspace=workspace),
+                     lambda: p3d.p3d_grad_norm(table, s, workspace=workspace)):
+            with pytest.raises(error, match="workspace must be.*" + words):
+                call()
