@@ -229,3 +229,12 @@ def test_no_tokens():
     s = made(0, 64, 16, torch.float32, 8)
     p3d.p3d_linear_i8(s["q"], s["s"], s["w"], s["t"], torch.empty(0, 16, device="cuda"), s["b"])
     p3d.p3d_quantize_rows(torch.empty(0, 64, device="cuda"), s["q"], s["s"])
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("k", [16, 48, 64, 112, 128, 176, 192, 240, 256, 320])
+def test_several_tiles_of_few_stages(k, residual):
+    """Rows of one stage to five, the last of every length, where a workgroup goes on
+    to other tiles: the loads of the next stand beside the end of one."""
+    for n, d in ((21000, 1544), (3000, 4104)):
+        check(n, k, d, torch.bfloat16, "none", True, residual)
