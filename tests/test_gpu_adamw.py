@@ -390,3 +390,17 @@ def test_a_norm_beyond_binary32_leaves_the_step_out(most):
     assert math.isclose(float(out[0]), norm, rel_tol=2 * ref.U)
     # (1 / norm is below the normal numbers: within half of their step)
     assert abs(float(out[1]) - min(1.0, most / norm)) <= 2.0 ** -150
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-40, 1e38])
+def test_any_eps_with_step_and_rate_on_the_device(eps, bits):
+    a, b = Model(SIZES, bits=bits, late=False, seed=13), Model(SIZES, bits=bits, late=False, seed=13)
+    lr = torch.tensor([1e-3], device="cuda")
+    hyper = dict(lr=float(lr), beta1=0.9, beta2=0.999, eps=eps)
+    p3d.p3d_adamw(a.table, step=2, seed=2, **hyper)
+    p3d.p3d_adamw(b.table, step=9, **{**hyper, "lr": 7.0}, device_lr=lr,
+                  device_step=torch.tensor([2], dtype=torch.int32, device="cuda"))
+    for x, y in zip(a.table, b.table):
+        assert torch.isfinite(x.float()).all()
+        assert torch.allclose(x.float(), y.float(), rtol=1e-6, atol=1e-12)
