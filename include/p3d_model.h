@@ -85,6 +85,9 @@ p3d_status p3d_group_norm(const p3d_group_desc* desc, const void* x, int64_t x_s
  *                  stride) and must not overlap them otherwise
  *   dweight, dbias float [C], each NULL where it is not wanted; overwritten,
  *                  0 where there are no rows
+ * mean is a binary32 number here, and a more exact one within the forward call:
+ * of a mean that is t deviations from 0, x^ is off by t 2^-25 in the gradient
+ * alone.
  * No result overlaps another tensor of the call (dx in place apart). */
 p3d_status p3d_group_norm_backward(const p3d_group_desc* desc, const void* dout,
                                    int64_t dout_stride, const void* x, int64_t x_stride,
@@ -204,6 +207,8 @@ p3d_status p3d_linear_i8(const p3d_linear_i8_desc* desc, const int8_t* q, int64_
  *   lr           finite, >= 0; beta1, beta2 in [0, 1); eps finite, > 0;
  *   step         >= 1 (its value is used without device_step)
  *   weight_decay finite, per tensor
+ * eps is what binary32 makes of it: the smallest is 2^-149, below the normal
+ * numbers.
  *   Alignment: 16 bytes (the scales and device scalars: 4).
  * --------------------------------------------------------------------- */
 typedef struct p3d_adamw_tensor {

@@ -160,9 +160,10 @@ def p3d_group_norm(x, out, groups, offsets=None, weight=None, bias=None, act="no
     """Enqueue p3d_group_norm: out = act((x - mean) rstd weight + bias) with an
     item's mean and rstd over its rows and each of `groups` ranges of channels.
     x, out: [n, channels] float32 or bfloat16 (rows may be strided; out may be
-    x); weight, bias: [channels]; act: "none", "silu" or "gelu"; mean, rstd:
-    float32 [batch, groups], written unless None (the gradient needs them);
-    offsets: the items' rows (None: one item)."""
+    x); weight, bias: [channels]; act: "none", "silu" or "gelu" (its tanh form:
+    torch's approximate="tanh"); mean, rstd: float32 [batch, groups], written
+    unless None (the gradient needs them); offsets: the items' rows (None: one
+    item)."""
     dev, f = _device(), torch.float32
     d, off = _group(x, groups, offsets, weight, bias, act, eps, dev)
     xp, xs = _rows(x, "x", x.dtype, dev)
@@ -215,7 +216,7 @@ def p3d_linear_i8(q, scale, weight, weight_scale, out, bias=None, act="none", re
     residual. q: int8 [n, in] (rows may be strided) and scale: float32 [n] of
     p3d_quantize_rows; weight: int8 [out, in]; weight_scale: float32 [out];
     out, residual: [n, out] and bias: [out], float32 or bfloat16 (residual may
-    be out)."""
+    be out); act: "none", "silu" or "gelu" (its tanh form)."""
     dev, dt, f = _device(), out.dtype, torch.float32
     qp, qs = _rows(q, "q", torch.int8, dev)
     n, k = q.shape
@@ -257,7 +258,10 @@ def make_adamw_tensors(params, grads, m, v, masters=None, m_scales=None, v_scale
     (size + 255) // 256; masters: float32 copies of bfloat16 params, or None;
     weight_decay: a number or one for each. The table keeps the memory
     that the tensors have now: a gradient in another tensor, or a parameter whose
-    .data was replaced, needs another table."""
+    .data was replaced, needs another table. (torch's zero_grad() drops the
+    gradients, and the next backward makes others: a step with the old table would
+    take the old ones. zero_grad(set_to_none=False) keeps them.) Making a
+    table costs some 3 us a tensor."""
     params, grads, m, v = list(params), list(grads), list(m), list(v)
     n = len(params)
     lists = [("grads", grads), ("m", m), ("v", v)]
@@ -322,7 +326,10 @@ def p3d_adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0, gra
     second of p3d_grad_norm's result) or None; seed: of the random bits that
     8-bit states are rounded by, another for every step (a device_step is added
     to it); device_lr, device_step: float32 / int32 device tensors of one element
-    that are read instead of lr and step when the work runs, or None."""
+    that are read instead of lr and step when the work runs, or None. The weights
+    are written as memory: their torch version counters stay, so a graph that was
+    recorded before the step must not be differentiated after it (torch would not
+    notice)."""
     dev, d = _adamw(tensors)
     d.lr, d.beta1, d.beta2, d.eps, d.step = lr, beta1, beta2, eps, step
     d.seed = seed & 0xffffffffffffffff
